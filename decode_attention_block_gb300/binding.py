@@ -1,5 +1,6 @@
-"""ctypes binding of ``libspark_attn.so`` (the C ABI in ``include/spark_attn.h``
-and ``include/spark_layer.h``).
+"""ctypes binding of ``libspark_attn.so`` (the C ABI in ``include/spark_attn.h``,
+``include/spark_layer.h``, ``include/spark_paged.h`` and
+``include/spark_score.h``).
 
 Argument marshalling only: every step of the block runs in the library's CUDA
 kernels.  Tensors are PyTorch CUDA tensors (PyTorch provides device memory and
@@ -26,6 +27,9 @@ SPARK_BF16 = 1
 SPARK_SLIDING = 0
 SPARK_FULL = 1
 SPARK_MAX_BATCH = 1024
+SPARK_MAX_TOP = 32
+# bits of a workspace's error word (spark_attn_error_word)
+SPARK_ERRBIT_TIMEOUT, SPARK_ERRBIT_INDEX, SPARK_ERRBIT_PAGES = 1, 2, 4
 
 _DTYPE_CODE = {torch.float32: SPARK_F32, torch.bfloat16: SPARK_BF16}
 
@@ -82,6 +86,28 @@ class SparkMlpWeights(ctypes.Structure):
     ]
 
 
+class SparkPagePool(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class SparkPagedBatch(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("max_q_len", ctypes.c_int32),
+    ]
+
+
 # every symbol include/*.h declares, with its ctypes signature
 _P = ctypes.c_void_p
 _SIGNATURES = {
@@ -120,6 +146,26 @@ _SIGNATURES = {
                                         ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "spark_head_logits": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "spark_paged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SparkGeom)]),
+    "spark_paged_append": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                          ctypes.POINTER(SparkPagePool), ctypes.POINTER(SparkPagedBatch), _P,
+                                          ctypes.c_size_t, _P]),
+    "spark_paged_attention": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.POINTER(SparkPagePool), ctypes.c_int32,
+                                             ctypes.POINTER(SparkPagedBatch), _P, _P, ctypes.c_size_t, _P]),
+    "spark_attn_paged": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, ctypes.POINTER(SparkLayerWeights),
+                                        ctypes.POINTER(SparkPagePool), ctypes.c_int32,
+                                        ctypes.POINTER(SparkPagedBatch), ctypes.POINTER(ctypes.c_int32), _P, _P,
+                                        ctypes.c_size_t, _P, ctypes.c_size_t, _P]),
+    "spark_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32]),
+    "spark_pages_remap": (ctypes.c_int, [ctypes.POINTER(SparkGeom), ctypes.POINTER(SparkPagePool), ctypes.c_int32,
+                                         _P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                                         _P]),
+    "spark_pages_compact": (ctypes.c_int, [ctypes.POINTER(SparkGeom), ctypes.POINTER(SparkPagePool), ctypes.c_int32,
+                                           _P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "spark_logprobs_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "spark_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P,
+                                            ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "spark_attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "spark_attn_abi_version": (ctypes.c_int32, []),
 }
@@ -261,6 +307,67 @@ class MlpWeights(_CachedC):
         return SparkMlpWeights(_dev_ptr(self.norm_w, "norm_w", dt), _dev_ptr(self.gate_w, "gate_w", dt),
                                _dev_ptr(self.up_w, "up_w", dt), _dev_ptr(self.down_w, "down_w", dt),
                                int(self.gate_w.shape[0]), _DTYPE_CODE[dt])
+
+
+def _rows(t: torch.Tensor, name: str) -> tuple:
+    """Address, row stride (elements) and dtype code of a matrix whose rows
+    are contiguous but may lie apart (a slice of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPE_CODE:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], _DTYPE_CODE[t.dtype]
+
+
+@dataclass
+class PagePool(_CachedC):
+    """One layer's pages as CUDA tensors ``k``, ``v`` of shape
+    ``[n_pages, page_size, n_kv, head_dim]`` (float32 or bfloat16)."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    _c: object = field(default=None, init=False, repr=False, compare=False)
+
+    def _build_c(self) -> SparkPagePool:
+        dt = self.k.dtype
+        if dt not in _DTYPE_CODE:
+            raise TypeError(f"pages must be float32 or bfloat16, got {dt}")
+        if self.k.dim() != 4 or self.k.shape != self.v.shape:
+            raise ValueError("k and v must both be [n_pages, page_size, n_kv, head_dim]")
+        return SparkPagePool(_dev_ptr(self.k, "k", dt), _dev_ptr(self.v, "v", dt), int(self.k.shape[0]),
+                             int(self.k.shape[1]), _DTYPE_CODE[dt])
+
+
+@dataclass
+class PagedBatch(_CachedC):
+    """The sequences of a call: int32 CUDA tensors ``table [n_seqs,
+    max_pages]``, ``q_start [n_seqs + 1]`` and ``seq_len [n_seqs]``, whose
+    values are read when the work runs, the rows ``n_tokens`` of the call's
+    token tensors and the most new tokens of a sequence ``max_q_len``."""
+
+    table: torch.Tensor
+    q_start: torch.Tensor
+    seq_len: torch.Tensor
+    n_tokens: int
+    max_q_len: int
+    _c: object = field(default=None, init=False, repr=False, compare=False)
+
+    def _build_c(self) -> SparkPagedBatch:
+        if self.table.dim() != 2 or self.q_start.shape != (self.table.shape[0] + 1,) or \
+                self.seq_len.shape != (self.table.shape[0],):
+            raise ValueError("table must be [n_seqs, max_pages], q_start [n_seqs + 1], seq_len [n_seqs]")
+        return SparkPagedBatch(_dev_ptr(self.table, "table", torch.int32),
+                               _dev_ptr(self.q_start, "q_start", torch.int32),
+                               _dev_ptr(self.seq_len, "seq_len", torch.int32), int(self.table.shape[0]),
+                               int(self.table.shape[1]), int(self.n_tokens), int(self.max_q_len))
+
+
+def _pool_heads(geom: SparkGeom, pool: PagePool) -> None:
+    if tuple(pool.k.shape[2:]) != (geom.n_kv, geom.head_dim):
+        raise ValueError(f"pages of {tuple(pool.k.shape[2:])} (heads, dims) do not fit the geometry "
+                         f"({geom.n_kv}, {geom.head_dim})")
 
 
 # ---------------------------------------------------------------------------
@@ -440,6 +547,148 @@ def spark_head_logits(geom: SparkGeom, h: torch.Tensor, norm_w: torch.Tensor, em
                                     _dev_ptr(logits, "logits", torch.float32), int(path),
                                     _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
            "spark_head_logits")
+
+
+def _workspace(nbytes: int, what: str, device, stream) -> torch.Tensor:
+    if nbytes == 0:
+        raise ValueError(f"invalid {what} for a workspace")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    spark_attn_workspace_init(ws, stream)
+    return ws
+
+
+def spark_paged_workspace_bytes(geom: SparkGeom) -> int:
+    return int(load().spark_paged_workspace_bytes(ctypes.byref(geom)))
+
+
+def make_paged_workspace(geom: SparkGeom, device=None, stream=None) -> torch.Tensor:
+    """Allocate (through PyTorch) and initialise a workspace for
+    spark_paged_append and spark_paged_attention (any batch)."""
+    return _workspace(spark_paged_workspace_bytes(geom), "geometry", device, stream)
+
+
+def spark_paged_append(geom: SparkGeom, k: torch.Tensor, v: torch.Tensor, pool: PagePool, batch: PagedBatch,
+                       ws: torch.Tensor, stream=None) -> None:
+    """Write the new tokens' rows k, v [n_tokens, n_kv * 256] into their pages."""
+    kp, ld, dt = _rows(k, "k")
+    vp, vld, vdt = _rows(v, "v")
+    kv_dim = geom.n_kv * geom.head_dim
+    if k.shape != (batch.n_tokens, kv_dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [n_tokens, {kv_dim}]")
+    if vdt != dt or vld != ld:
+        raise ValueError("k and v must have the same dtype and row stride")
+    _pool_heads(geom, pool)
+    pc, bc = pool.to_c(), batch.to_c()
+    _check(load().spark_paged_append(ctypes.byref(geom), kp, vp, ld, dt, ctypes.byref(pc), ctypes.byref(bc),
+                                     _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+           "spark_paged_append")
+
+
+def spark_paged_attention(geom: SparkGeom, q: torch.Tensor, pool: PagePool, layer_class: int, batch: PagedBatch,
+                          a: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """a [n_tokens, n_q * 256] = attention of the rotated queries q (float32
+    or bfloat16, a alike) over each sequence's pages."""
+    qp, ld, dt = _rows(q, "q")
+    if q.shape != (batch.n_tokens, geom.n_q * geom.head_dim) or a.shape != q.shape:
+        raise ValueError(f"q and a must be [n_tokens, {geom.n_q * geom.head_dim}]")
+    _pool_heads(geom, pool)
+    pc, bc = pool.to_c(), batch.to_c()
+    _check(load().spark_paged_attention(ctypes.byref(geom), qp, ld, dt, ctypes.byref(pc), int(layer_class),
+                                        ctypes.byref(bc), _dev_ptr(a, "a", q.dtype), _dev_ptr(ws, "workspace"),
+                                        ws.numel() * ws.element_size(), _stream(stream)), "spark_paged_attention")
+
+
+def spark_attn_paged(geom: SparkGeom, h: torch.Tensor, weights: LayerWeights, pool: PagePool, layer_class: int,
+                     batch: PagedBatch, positions, out: torch.Tensor, ws: torch.Tensor, paged_ws: torch.Tensor,
+                     stream=None) -> None:
+    """The attention block for the batch's new tokens on a paged cache: h,
+    out [n_tokens, hidden]; positions: each row's rope position (host)."""
+    if h.shape != (batch.n_tokens, geom.hidden) or out.shape != h.shape or len(positions) != batch.n_tokens:
+        raise ValueError("h and out must be [n_tokens, hidden], with one position per row")
+    _pool_heads(geom, pool)
+    wc, pc, bc = weights.to_c(), pool.to_c(), batch.to_c()
+    _check(load().spark_attn_paged(ctypes.byref(geom), _dev_ptr(h, "h", torch.float32), ctypes.byref(wc),
+                                   ctypes.byref(pc), int(layer_class), ctypes.byref(bc), _positions(positions),
+                                   _dev_ptr(out, "out", torch.float32), _dev_ptr(ws, "workspace"),
+                                   ws.numel() * ws.element_size(), _dev_ptr(paged_ws, "paged workspace"),
+                                   paged_ws.numel() * paged_ws.element_size(), _stream(stream)), "spark_attn_paged")
+
+
+def spark_pages_workspace_bytes(n_pages: int, n_slots: int) -> int:
+    return int(load().spark_pages_workspace_bytes(int(n_pages), int(n_slots)))
+
+
+def make_pages_workspace(n_pages: int, n_slots: int, device=None, stream=None) -> torch.Tensor:
+    """Allocate (through PyTorch) and initialise a workspace for
+    spark_pages_remap and spark_pages_compact."""
+    return _workspace(spark_pages_workspace_bytes(n_pages, n_slots), "number of pages or slots", device, stream)
+
+
+def _pools(geom: SparkGeom, pools) -> ctypes.Array:
+    for p in pools:
+        _pool_heads(geom, p)
+    return (SparkPagePool * len(pools))(*[p.to_c() for p in pools])
+
+
+def spark_pages_remap(geom: SparkGeom, pools, table: torch.Tensor, parent: torch.Tensor, keep_len: torch.Tensor,
+                      new_len: torch.Tensor, new_table: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """The page tables of a step: row s of new_table holds the first
+    keep_len[s] positions of table's row parent[s] (-1: nothing) and has room
+    for new_len[s]; ``pools``: every layer's PagePool."""
+    n = table.shape[0]
+    if table.dim() != 2 or new_table.shape != table.shape or not parent.shape == keep_len.shape == new_len.shape == (n,):
+        raise ValueError("table and new_table must be [n_slots, max_pages], the lists [n_slots]")
+    i32 = torch.int32
+    _check(load().spark_pages_remap(ctypes.byref(geom), _pools(geom, pools), len(pools), _dev_ptr(table, "table", i32),
+                                    n, int(table.shape[1]), _dev_ptr(parent, "parent", i32),
+                                    _dev_ptr(keep_len, "keep_len", i32), _dev_ptr(new_len, "new_len", i32),
+                                    _dev_ptr(new_table, "new_table", i32), _dev_ptr(ws, "workspace"),
+                                    ws.numel() * ws.element_size(), _stream(stream)), "spark_pages_remap")
+
+
+def spark_pages_compact(geom: SparkGeom, pools, table: torch.Tensor, new_table: torch.Tensor, n_live: torch.Tensor,
+                        ws: torch.Tensor, stream=None) -> None:
+    """Move the pages in use to the front of every pool; n_live (int32, one
+    element) receives their number.  new_table may be table."""
+    if table.dim() != 2 or new_table.shape != table.shape or n_live.numel() != 1:
+        raise ValueError("table and new_table must be [n_slots, max_pages], n_live one element")
+    i32 = torch.int32
+    _check(load().spark_pages_compact(ctypes.byref(geom), _pools(geom, pools), len(pools),
+                                      _dev_ptr(table, "table", i32), int(table.shape[0]), int(table.shape[1]),
+                                      _dev_ptr(new_table, "new_table", i32), _dev_ptr(n_live, "n_live", i32),
+                                      _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+           "spark_pages_compact")
+
+
+def spark_logprobs_workspace_bytes(n_rows: int, top_k: int) -> int:
+    return int(load().spark_logprobs_workspace_bytes(int(n_rows), int(top_k)))
+
+
+def make_logprobs_workspace(n_rows: int, top_k: int, device=None, stream=None) -> torch.Tensor:
+    """Allocate (through PyTorch) and initialise a workspace for
+    spark_token_logprobs."""
+    return _workspace(spark_logprobs_workspace_bytes(n_rows, top_k), "number of rows or alternatives", device, stream)
+
+
+def spark_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, logprob: torch.Tensor, entropy: torch.Tensor,
+                         top_ids: torch.Tensor, top_logprobs: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Log probabilities of the targets [n] under logits [n, vocab] (float32
+    or bfloat16; -1: none), the rows' entropies, and their top_ids.shape[1]
+    highest logits' indices and log probabilities (None, None: none)."""
+    lp, ld, dt = _rows(logits, "logits")
+    n, vocab = logits.shape
+    k = 0 if top_ids is None else int(top_ids.shape[1])
+    if targets.shape != (n,) or logprob.shape != (n,) or entropy.shape != (n,):
+        raise ValueError("targets, logprob and entropy must be [n]")
+    if k and (top_ids.shape != (n, k) or top_logprobs.shape != (n, k)):
+        raise ValueError("top_ids and top_logprobs must be [n, k]")
+    _check(load().spark_token_logprobs(lp, ld, dt, n, vocab, _dev_ptr(targets, "targets", torch.int32), k,
+                                       _dev_ptr(logprob, "logprob", torch.float32),
+                                       _dev_ptr(entropy, "entropy", torch.float32),
+                                       _dev_ptr(top_ids, "top_ids", torch.int32) if k else None,
+                                       _dev_ptr(top_logprobs, "top_logprobs", torch.float32) if k else None,
+                                       _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+           "spark_token_logprobs")
 
 
 def spark_attn_status_string(status: int) -> str:

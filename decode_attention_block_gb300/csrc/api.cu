@@ -19,6 +19,7 @@
 
 #include "checks.h"
 #include "launch.h"
+#include "paged_checks.h"
 
 namespace spark {
 
@@ -322,6 +323,53 @@ int spark_attn_prefill(const spark_geom* g, const float* h, const spark_layer_we
   if (e == cudaSuccess)
     e = run_oproj(pick_path(SPARK_PATH_AUTO, w->dtype, g, 0, m), g, a, g_logits, h, w, m, out, err,
                   workspace, L, st);
+  return cuda_status(e);
+}
+
+int spark_attn_paged(const spark_geom* g, const float* h, const spark_layer_weights* w,
+                     const spark_page_pool* pool, int32_t layer_class, const spark_paged_batch* batch,
+                     const int32_t* positions, float* out, void* workspace, size_t workspace_bytes,
+                     void* paged_workspace, size_t paged_workspace_bytes, void* stream) {
+  int s;
+  if ((s = check_geom(g)) != SPARK_OK) return s;
+  if ((s = check_weights(w, true, true)) != SPARK_OK) return s;
+  if ((s = check_pool(g, pool)) != SPARK_OK) return s;
+  if (layer_class != SPARK_FULL && layer_class != SPARK_SLIDING) return SPARK_ERR_INVALID_ARG;
+  if ((s = check_paged_batch(batch, pool)) != SPARK_OK) return s;
+  const int32_t m = batch->n_tokens;
+  if ((s = check_batch(m)) != SPARK_OK) return s;
+  if (!positions) return SPARK_ERR_INVALID_ARG;
+  for (int32_t t = 0; t < m; ++t)
+    if (positions[t] < 0 || positions[t] >= INT32_MAX - 1) return SPARK_ERR_POSITION;
+  if ((s = check_ws(g, m, workspace, workspace_bytes)) != SPARK_OK) return s;
+  if ((s = check_paged_ws(paged_workspace, paged_workspace_bytes)) != SPARK_OK) return s;
+  if (!h || !out || !aligned16(h) || !aligned16(out)) return SPARK_ERR_INVALID_ARG;
+  const WsLayout L = ws_layout(g->hidden, g->n_q, g->n_kv, m);
+  cudaStream_t st = (cudaStream_t)stream;
+  float* g_logits = ws_at<float>(workspace, L.g);
+  float* q_rot = ws_at<float>(workspace, L.q_rot);
+  float* a = ws_at<float>(workspace, L.a);
+  uint32_t* err = ws_at<uint32_t>(workspace, L.err);
+  // k and v in the pool's type, staged as "sequences" of one row each (as a
+  // chunk's), then written through the tables
+  const size_t row = (size_t)g->n_kv * kHeadDim;
+  unsigned char* ks = ws_at<unsigned char>(workspace, L.stage);
+  unsigned char* vs = ks + (size_t)m * row * (pool->dtype == SPARK_BF16 ? 2 : 4);
+  spark_kv_layer staged = {ks, vs, 1, 1, pool->dtype};
+  int rotary_dim;
+  double theta;
+  rope_for(g, layer_class, &rotary_dim, &theta);
+  paged::Args p = paged_args(g, pool, layer_class, batch, paged_workspace);
+  p.q = q_rot;
+  p.q_ld = (int64_t)g->n_q * kHeadDim;
+  p.a = a;
+  cudaError_t e = run_qkv(pick_path(SPARK_PATH_AUTO, w->dtype, g, rotary_dim, m), g, h, w, &staged, rotary_dim, theta,
+                          positions, m, q_rot, g_logits, err, workspace, L, st);
+  if (e == cudaSuccess)
+    e = launch_paged_append(p, pool->dtype, pool->dtype, ks, vs, (int64_t)row, pool->k, pool->v, st);
+  if (e == cudaSuccess) e = launch_paged_attention(p, SPARK_F32, pool->dtype, pool->k, pool->v, st);
+  if (e == cudaSuccess)
+    e = run_oproj(pick_path(SPARK_PATH_AUTO, w->dtype, g, 0, m), g, a, g_logits, h, w, m, out, err, workspace, L, st);
   return cuda_status(e);
 }
 

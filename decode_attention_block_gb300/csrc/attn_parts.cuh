@@ -163,15 +163,14 @@ __device__ __forceinline__ void attn_load_q(float* q_s, const float* qg, int tid
   }
 }
 
-// One warp folds an n-row tile (rows 0..n-1 of the K and V half-stages) into
-// its state.  q.k: lanes (sl, ri) cover dims [64 sl, 64 sl + 64) of rows ri
+// One warp folds rows [row_lo, n) of a tile (K and V half-stages) into its
+// state; rows outside are not read by p.v and take probability 0.  q.k: lanes (sl, ri) cover dims [64 sl, 64 sl + 64) of rows ri
 // and ri + 8 with packed fp32x2 FMAs, then sum over the four slices by
 // shuffles; p.v: lane l owns dims [8 l, 8 l + 8).  p_w is the warp's 16-row
 // probability scratch in shared memory.
 template <typename CT>
-__device__ __forceinline__ void attn_tile(const unsigned char* kst, const unsigned char* vst, int n,
-                                          const float* q_s, float4* p_w, float scale_log2,
-                                          AttnState& st) {
+__device__ __forceinline__ void attn_tile_rows(const unsigned char* kst, const unsigned char* vst, int row_lo, int n,
+                                               const float* q_s, float4* p_w, float scale_log2, AttnState& st) {
   const int lane = threadIdx.x & 31;
   const int sl = lane >> 3, ri = lane & 7;
   float2 acc[2][4];
@@ -209,7 +208,7 @@ __device__ __forceinline__ void attn_tile(const unsigned char* kst, const unsign
       float v = acc[rr][h].x + acc[rr][h].y;
       v += __shfl_xor_sync(0xffffffffu, v, 8);
       v += __shfl_xor_sync(0xffffffffu, v, 16);
-      sc[rr][h] = (ri + 8 * rr) < n ? v * scale_log2 : -INFINITY;
+      sc[rr][h] = (ri + 8 * rr) >= row_lo && (ri + 8 * rr) < n ? v * scale_log2 : -INFINITY;
     }
   // online softmax (base 2)
   float pr[2][4];
@@ -250,12 +249,20 @@ __device__ __forceinline__ void attn_tile(const unsigned char* kst, const unsign
       st.o[3][i] = ffma2(vv[i], make_float2(pp.w, pp.w), st.o[3][i]);
     }
   };
-  if (n == kTile) {
+  if (row_lo == 0 && n == kTile) {
 #pragma unroll 4
     for (int t = 0; t < kTile; ++t) pv_row(t);
   } else {
-    for (int t = 0; t < n; ++t) pv_row(t);
+    for (int t = row_lo; t < n; ++t) pv_row(t);
   }
+}
+
+// The decode kernels' tile: rows [0, n).
+template <typename CT>
+__device__ __forceinline__ void attn_tile(const unsigned char* kst, const unsigned char* vst, int n,
+                                          const float* q_s, float4* p_w, float scale_log2,
+                                          AttnState& st) {
+  attn_tile_rows<CT>(kst, vst, 0, n, q_s, p_w, scale_log2, st);
 }
 
 // The CTA that holds the last row of flat position x, for a grid of G CTAs
@@ -506,9 +513,10 @@ __device__ __forceinline__ void mma_q_from_smem(MmaQ& Q, const float* q_s) {
 
 // One warp folds rows [row_lo, n) of a tile into its state (bf16 K and V
 // half-stages); rows outside take probability 0.  p_w: the warp's 16 x 4 fp32
-// probability scratch.  kZeroTail: rows n..15 of the V half-stage are zeroed
-// first (their probability is 0, and 0 * a non-finite stale value would not
-// be); without it the caller has zeroed them, or they hold finite rows.
+// probability scratch.  kZeroTail: rows outside [row_lo, n) of the V
+// half-stage are zeroed first (their probability is 0, and 0 * a non-finite
+// stale value would not be); without it the caller has zeroed them, or they
+// hold finite rows.
 template <bool kZeroTail>
 __device__ __forceinline__ void attn_tile_mma_rows(unsigned char* kst, unsigned char* vst, int row_lo, int n,
                                                    const MmaQ& Q, float* p_w, float scale_log2,
@@ -529,10 +537,13 @@ __device__ __forceinline__ void attn_tile_mma_rows(unsigned char* kst, unsigned 
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) c[i] += c2[i];
-  if (kZeroTail && n < kTile) {
-    for (int r = n; r < kTile; ++r)
+  if (kZeroTail && (row_lo > 0 || n < kTile)) {
+    auto zero_row = [&](int r) {
       *reinterpret_cast<uint4*>(vst + (lane >> 3) * kSubBytes + r * kLine + (lane & 7) * 16) =
           make_uint4(0u, 0u, 0u, 0u);
+    };
+    for (int r = 0; r < row_lo; ++r) zero_row(r);
+    for (int r = n; r < kTile; ++r) zero_row(r);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA refills the stage
   }
   // hi + lo columns, scale, mask: sc[r][j] = row (g + 8 r), head 2 (t & 1) + j

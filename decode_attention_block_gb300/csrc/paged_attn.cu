@@ -1,0 +1,411 @@
+// paged_attn.cu -- attention of new tokens over a paged cache, one token and
+// KV head at a time, and the write of new rows into pages.
+//
+// a[t, h] = sum_x softmax_x(scale q[t, h] . k[x, h / 4]) v[x, h / 4] over the
+// positions x the token attends to.  A group is one token's four query heads
+// of one KV head: each row it reads serves all four.  The work is bound by
+// the rows read from HBM; it is split evenly over the GPU whatever the
+// lengths are (paged.h: tiles of 16 positions, equal shares, the last CTA of
+// a split group merges the partial softmax states in CTA order), and inside a
+// CTA one producer warp streams tiles through a shared-memory ring (one TMA
+// box per K or V tile, the page number from the table) to four consumer warps
+// holding the softmax states: the schedule and the tile of the contiguous
+// cache's decode attention (attn.cu, attn_parts.cuh).
+#include <math.h>
+
+#include <type_traits>
+
+#include "attn_parts.cuh"
+#include "launch.h"
+#include "paged_launch.h"
+#include "paged_parts.cuh"
+
+namespace spark {
+namespace {
+
+using paged::Args;
+using paged::Cursor;
+using paged::Shape;
+
+constexpr int kTokThreads = (kConsumers + 1) * 32;
+constexpr int kStages = 4;    // 16-row K + V tiles in flight per CTA
+constexpr int kMinUnits = 4;  // tiles per CTA at least: one per consumer warp
+
+template <typename CT>
+struct TokSmem {
+  static constexpr int kHalf = kv_half_bytes<CT>();
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kQ = kStages * kStage;
+  static constexpr int kP = kQ + 4 * kQStride * 4;
+  static constexpr int kM = kP + kConsumers * kTile * 16;
+  static constexpr int kL = kM + kConsumers * 16;
+  static constexpr int kO = kL + kConsumers * 16;
+  static constexpr int kBars = kO + kConsumers * 4 * kHeadDim * 4;
+  static constexpr int kFlags = kBars + 2 * kStages * 8;
+  static constexpr int kSums = kFlags + 16;
+  static constexpr int kPrefix = kSums + 64;
+  static constexpr int kBytes = kPrefix + 8 * (SPARK_MAX_BATCH + 2);
+  static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 (128B swizzle)
+};
+
+// the four heads' queries of one (token, KV head), as attn_load_q lays them
+// out (fp32 in 64-dim slices); consumer threads only
+__device__ __forceinline__ void load_q(float* q_s, const float* qg, int tid) { attn_load_q<kConsumerThreads>(q_s, qg, tid); }
+__device__ __forceinline__ void load_q(float* q_s, const __nv_bfloat16* qg, int tid) {
+  const uint4 w = __ldcg(reinterpret_cast<const uint4*>(qg) + tid);  // 8 elements of 4 x 256
+  const int e = 8 * tid, h = e >> 8, d = e & 255;
+  float* dst = q_s + (d >> 6) * kQStride + h * 64 + (d & 63);
+  const float2 a = bf16x2_to_f32x2(w.x), b = bf16x2_to_f32x2(w.y), c = bf16x2_to_f32x2(w.z), f = bf16x2_to_f32x2(w.w);
+  reinterpret_cast<float4*>(dst)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(c.x, c.y, f.x, f.y);
+}
+
+// eight output dims of one head
+__device__ __forceinline__ void store8(float* dst, const float (&o)[8], float inv) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&o)[8], float inv) {
+  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                                              pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+}
+
+// The group's state from the consumer warps' states in `sm`: finished if
+// whole, else this CTA's partial; the last of the group's CTAs c_first ..
+// c_last to arrive merges them in CTA order.  Warp h takes query head h, lane
+// l its dims [8 l, 8 l + 8).
+template <typename QT>
+__device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* flags, const Args& p, QT* a_head0,
+                                             int64_t begin, int64_t end, int64_t total, int G, int c) {
+  const int tid = threadIdx.x, h = tid >> 5, lane = tid & 31;
+  named_bar_sync(kBarConsumers, kConsumerThreads);
+  float M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sm.ms[w * 4 + h]);
+  float L = 0.f, O[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) O[i] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kConsumers; ++w) {
+    const float mw = sm.ms[w * 4 + h];
+    const float scl = mw == -INFINITY ? 0.f : exp2f(mw - M);
+    L = fmaf(sm.ls[w * 4 + h], scl, L);
+    const float4* src = reinterpret_cast<const float4*>(sm.os + (w * 4 + h) * kHeadDim + 8 * lane);
+    const float4 x0 = src[0], x1 = src[1];
+    O[0] = fmaf(x0.x, scl, O[0]); O[1] = fmaf(x0.y, scl, O[1]);
+    O[2] = fmaf(x0.z, scl, O[2]); O[3] = fmaf(x0.w, scl, O[3]);
+    O[4] = fmaf(x1.x, scl, O[4]); O[5] = fmaf(x1.y, scl, O[5]);
+    O[6] = fmaf(x1.z, scl, O[6]); O[7] = fmaf(x1.w, scl, O[7]);
+  }
+  QT* dst = a_head0 + h * kHeadDim + 8 * lane;
+  const int c_first = paged::cta_at(begin, total, G), c_last = paged::cta_at(end - 1, total, G);
+  if (c_first == c_last) {
+    if (!flags[0]) store8(dst, O, 1.0f / L);
+    return;
+  }
+  float* P = p.part + (int64_t)paged::partial_slot(c, begin, total, G) * kPartFloats;
+  float4* po = reinterpret_cast<float4*>(P + 8 + h * kHeadDim + 8 * lane);
+  po[0] = make_float4(O[0], O[1], O[2], O[3]);
+  po[1] = make_float4(O[4], O[5], O[6], O[7]);
+  if (lane == 0) {
+    P[h] = M;
+    P[4 + h] = L;
+  }
+  __threadfence();
+  named_bar_sync(kBarMerge, kConsumerThreads);
+  if (tid == 0) {
+    // the group's ticket is that of its first CTA, where no other split group
+    // begins; every arrival counts, so the ticket is back at zero after it
+    const int last = atomicAdd(&p.tickets[c_first], 1u) == (uint32_t)(c_last - c_first);
+    if (last) p.tickets[c_first] = 0;
+    flags[1] = last && !flags[0];
+  }
+  named_bar_sync(kBarMerge, kConsumerThreads);
+  if (!flags[1]) return;
+  __threadfence();
+  float M2 = -INFINITY, L2 = 0.f, O2[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) O2[i] = 0.f;
+  constexpr int kBatch = 8;  // partials loaded per round trip
+  for (int q0 = c_first; q0 <= c_last; q0 += kBatch) {
+    float mq[kBatch], lq[kBatch];
+    float4 x0[kBatch], x1[kBatch];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      if (q0 + t <= c_last) {
+        const float* Pq = p.part + (int64_t)paged::partial_slot(q0 + t, begin, total, G) * kPartFloats;
+        mq[t] = __ldcg(Pq + h);
+        lq[t] = __ldcg(Pq + 4 + h);
+        x0[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane));
+        x1[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane + 4));
+      } else {
+        mq[t] = -INFINITY;
+        lq[t] = 0.f;
+        x0[t] = x1[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float mb = M2;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) mb = fmaxf(mb, mq[t]);
+    const float rs = M2 == -INFINITY ? 0.f : exp2f(M2 - mb);
+    L2 *= rs;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) O2[i] *= rs;
+    M2 = mb;
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      const float scl = mq[t] == -INFINITY ? 0.f : exp2f(mq[t] - M2);
+      L2 = fmaf(lq[t], scl, L2);
+      O2[0] = fmaf(x0[t].x, scl, O2[0]); O2[1] = fmaf(x0[t].y, scl, O2[1]);
+      O2[2] = fmaf(x0[t].z, scl, O2[2]); O2[3] = fmaf(x0[t].w, scl, O2[3]);
+      O2[4] = fmaf(x1[t].x, scl, O2[4]); O2[5] = fmaf(x1[t].y, scl, O2[5]);
+      O2[6] = fmaf(x1[t].z, scl, O2[6]); O2[7] = fmaf(x1[t].w, scl, O2[7]);
+    }
+  }
+  store8(dst, O2, 1.0f / L2);
+}
+
+template <typename CT, typename QT, int MINB>
+__global__ void __launch_bounds__(kTokThreads, MINB)
+    k_paged_token(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ Args p) {
+  using S = TokSmem<CT>;
+  constexpr bool kMma = std::is_same<CT, __nv_bfloat16>::value;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* q_s = reinterpret_cast<float*>(base + S::kQ);
+  float4* p_s = reinterpret_cast<float4*>(base + S::kP);
+  const MergeSmem msm{reinterpret_cast<float*>(base + S::kM), reinterpret_cast<float*>(base + S::kL),
+                      reinterpret_cast<float*>(base + S::kO)};
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(base + S::kBars);
+  uint64_t* empty_bar = full_bar + kStages;
+  volatile int* flags = reinterpret_cast<volatile int*>(base + S::kFlags);  // [0] abort, [1] last
+  int64_t* prefix = reinterpret_cast<int64_t*>(base + S::kPrefix);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    flags[0] = 0;
+    flags[1] = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  // tables, lengths, rows and queries may come from the kernel before
+  pdl_wait();
+  pdl_trigger();
+  const Shape sh{1, kTile, p.window};
+  paged::work_prefix<kTokThreads>(p, sh, prefix, reinterpret_cast<int64_t*>(base + S::kSums));
+  const int64_t total = prefix[p.n_seqs];
+  if (total == 0) return;
+  const int G = paged::ctas_for(total, kMinUnits, gridDim.x), c = blockIdx.x;
+  if (c >= G) return;
+  const int64_t u0 = paged::share_begin(total, G, c), u1 = paged::share_begin(total, G, c + 1);
+
+  Cursor cur;
+  cur.seek(p, sh, prefix, u0);
+  if (warp == kConsumers) {
+    // ---- producer
+    uint32_t k = 0;
+    bool ok = true;
+    for (;;) {
+      const int64_t t1 = cur.end < u1 ? cur.end : u1;
+      for (int64_t u = cur.begin > u0 ? cur.begin : u0; u < t1; u += 32) {
+        // the pages of the next 32 tiles, one per lane
+        const int n = t1 - u < 32 ? (int)(t1 - u) : 32;
+        const int pos = (cur.g.tile0 + (int)(u - cur.begin) + lane) * kTile;
+        int z = 0;
+        if (lane < n)
+          z = page_at(p, cur.s, paged::page_col(pos, p.page_size)) * p.page_size + paged::page_row(pos, p.page_size);
+        for (int i = 0; i < n; ++i, ++k) {
+          const int zi = __shfl_sync(0xffffffffu, z, i);
+          if (lane == 0) {
+            const int s = (int)(k % kStages);
+            const uint32_t r = k / kStages;
+            if (ok && r > 0 && !mbar_wait_bounded(&empty_bar[s], (r - 1) & 1, flags, kWaitLimitNs)) {
+              ok = false;
+              flags[0] = 1;
+              atomicOr(p.err, kErrWaitTimeout);
+            }
+            if (ok) {
+              mbar_arrive_expect_tx(&full_bar[s], S::kStage);
+              unsigned char* kd = base + s * S::kStage;
+              tma_load_4d(kd, &tm_k, &full_bar[s], 0, zi, 0, cur.j);
+              tma_load_4d(kd + S::kHalf, &tm_v, &full_bar[s], 0, zi, 0, cur.j);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+        }
+        if (!ok) break;
+      }
+      if (!ok || cur.end >= u1) break;
+      cur.next(p, sh);
+    }
+    if (lane == 0 && flags[0]) {
+      // let the copies in flight land before the CTA can exit
+      int never = 0;
+      for (uint32_t i = k > kStages ? k - kStages : 0; i < k; ++i)
+        mbar_wait_bounded(&full_bar[i % kStages], (i / kStages) & 1, &never, kWaitLimitNs);
+    }
+    return;
+  }
+  // ---- consumers
+  uint32_t k = 0;
+  AttnState st;
+  MmaQ mq;
+  MmaState mst;
+  const QT* q = static_cast<const QT*>(p.q);
+  QT* a = static_cast<QT*>(p.a);
+  for (;;) {
+    const int64_t t1 = cur.end < u1 ? cur.end : u1;
+    const int64_t row = cur.seq.q0 + cur.g.tok;
+    named_bar_sync(kBarConsumers, kConsumerThreads);  // the previous group's merge is done
+    load_q(q_s, q + row * p.q_ld + (int64_t)cur.j * kGroup * kHeadDim, tid);
+    named_bar_sync(kBarConsumers, kConsumerThreads);
+    if constexpr (kMma) {
+      mma_q_from_smem(mq, q_s);
+      mst.reset();
+    } else {
+      st.reset();
+    }
+    for (int64_t u = cur.begin > u0 ? cur.begin : u0; u < t1; ++u, ++k) {
+      if ((int)(k % kConsumers) != warp) continue;
+      const int s = (int)(k % kStages);
+      const bool ok =
+          __all_sync(0xffffffffu, !flags[0] && mbar_wait_bounded(&full_bar[s], (k / kStages) & 1, flags, kWaitLimitNs));
+      if (!ok) {
+        if (lane == 0 && !flags[0]) {
+          flags[0] = 1;
+          atomicOr(p.err, kErrWaitTimeout);
+        }
+      } else {
+        const int pos = (cur.g.tile0 + (int)(u - cur.begin)) * kTile;
+        const int r0 = cur.g.lo > pos ? cur.g.lo - pos : 0;
+        const int r1 = cur.g.hi + 1 - pos < kTile ? cur.g.hi + 1 - pos : kTile;
+        unsigned char* kst = base + s * S::kStage;
+        if constexpr (kMma)
+          attn_tile_mma_rows<true>(kst, kst + S::kHalf, r0, r1, mq, reinterpret_cast<float*>(p_s + warp * kTile),
+                                   p.scale_log2, mst);
+        else
+          attn_tile_rows<CT>(kst, kst + S::kHalf, r0, r1, q_s, p_s + warp * kTile, p.scale_log2, st);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty_bar[s]);
+    }
+    if constexpr (kMma)
+      attn_store_state_mma(mst, msm);
+    else
+      attn_store_state(st, msm);
+    finish_group(msm, flags, p, a + (row * p.n_kv + cur.j) * kGroup * kHeadDim, cur.begin, cur.end, total, G, c);
+    if (cur.end >= u1) break;
+    cur.next(p, sh);
+  }
+}
+
+template <typename CT, typename QT>
+cudaError_t launch_token(const Args& p, const void* k, const void* v, cudaStream_t st) {
+  using S = TokSmem<CT>;
+  constexpr int kMinB = CacheT<CT>::kDeepBlocks;
+  CUtensorMap mk, mv;
+  const bool bf16 = std::is_same<CT, __nv_bfloat16>::value;
+  const int64_t rows = (int64_t)p.n_pages * p.page_size;
+  if (!make_kv_tile_map(&mk, k, bf16, p.n_kv, rows) || !make_kv_tile_map(&mv, v, bf16, p.n_kv, rows))
+    return cudaErrorInvalidValue;
+  auto kern = k_paged_token<CT, QT, kMinB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
+  if (e != cudaSuccess) return e;
+  int grid = kMinB * device_sm_count();
+  if (grid > paged::kMaxCtas) grid = paged::kMaxCtas;
+  return launch_pdl(kern, dim3(grid), dim3(kTokThreads), S::kAlloc, st, mk, mv, p);
+}
+
+// ---------------------------------------------------------------------------
+// the write of new rows
+// ---------------------------------------------------------------------------
+
+// four elements in the pool's type, rounded once
+__device__ __forceinline__ float4 load4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
+  const float2 a = bf16x2_to_f32x2(w.x), b = bf16x2_to_f32x2(w.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// One CTA per new token: its sequence by binary search in q_start, then its K
+// and V rows.  Bound by the rows' bytes; a row is 512 B to 8 KB.
+template <typename XT, typename CT>
+__global__ void __launch_bounds__(256)
+    k_paged_append(const XT* k, const XT* v, int64_t ld, CT* pk, CT* pv,
+                   const __grid_constant__ Args p) {
+  pdl_wait();
+  // no early trigger: a kernel that reads pages before its own wait must not
+  // start before these rows are written
+  const int t = blockIdx.x;
+  int lo = 0, hi = p.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldcg(p.q_start + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  const paged::Seq s = paged::load_seq(p, lo);
+  if (s.bad) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
+    return;
+  }
+  if (t < s.q0 || t >= s.q0 + s.n) return;  // behind the last sequence
+  const int pos = s.p0 + (t - s.q0);
+  const int pg = __ldcg(p.table + (int64_t)lo * p.max_pages + paged::page_col(pos, p.page_size));
+  if (pg < 0 || pg >= p.n_pages) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
+    return;
+  }
+  const int row = p.n_kv * kHeadDim;
+  const int64_t to = ((int64_t)pg * p.page_size + paged::page_row(pos, p.page_size)) * row;
+  for (int e = 4 * threadIdx.x; e < row; e += 4 * 256) {
+    const float4 x = load4(k + t * ld + e), y = load4(v + t * ld + e);
+    store4(pk + to + e, x);
+    store4(pv + to + e, y);
+  }
+}
+
+template <typename XT, typename CT>
+cudaError_t launch_append_t(const Args& p, const void* k, const void* v, int64_t ld, void* pk, void* pv,
+                            cudaStream_t st) {
+  return launch_pdl(k_paged_append<XT, CT>, dim3(p.n_tokens), dim3(256), 0, st, static_cast<const XT*>(k),
+                    static_cast<const XT*>(v), ld, static_cast<CT*>(pk), static_cast<CT*>(pv), p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
+                               cudaStream_t st) {
+  if (cdtype == SPARK_BF16)
+    return qdtype == SPARK_BF16 ? launch_token<__nv_bfloat16, __nv_bfloat16>(p, k, v, st)
+                                : launch_token<__nv_bfloat16, float>(p, k, v, st);
+  return qdtype == SPARK_BF16 ? launch_token<float, __nv_bfloat16>(p, k, v, st)
+                              : launch_token<float, float>(p, k, v, st);
+}
+
+cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
+                                   cudaStream_t st) {
+  return launch_paged_token(p, qdtype, cdtype, k, v, st);
+}
+
+cudaError_t launch_paged_append(const paged::Args& p, int xdtype, int cdtype, const void* k, const void* v, int64_t ld,
+                                void* pk, void* pv, cudaStream_t st) {
+  if (cdtype == SPARK_BF16)
+    return xdtype == SPARK_BF16 ? launch_append_t<__nv_bfloat16, __nv_bfloat16>(p, k, v, ld, pk, pv, st)
+                                : launch_append_t<float, __nv_bfloat16>(p, k, v, ld, pk, pv, st);
+  return xdtype == SPARK_BF16 ? launch_append_t<__nv_bfloat16, float>(p, k, v, ld, pk, pv, st)
+                              : launch_append_t<float, float>(p, k, v, ld, pk, pv, st);
+}
+
+}  // namespace spark

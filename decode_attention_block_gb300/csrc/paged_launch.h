@@ -1,0 +1,21 @@
+// paged_launch.h -- host launchers of the paged cache's kernels and of the
+// token scores (internal to the library).
+#pragma once
+
+#include "paged_parts.cuh"
+
+namespace spark {
+
+// Attention of every new token over its pages.
+cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
+                                   cudaStream_t st);
+
+// The same, token by token (any pool type).
+cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
+                               cudaStream_t st);
+
+// The new tokens' k and v rows into their pages.
+cudaError_t launch_paged_append(const paged::Args& p, int xdtype, int cdtype, const void* k, const void* v, int64_t ld,
+                                void* pk, void* pv, cudaStream_t st);
+
+}  // namespace spark
