@@ -396,6 +396,7 @@ cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, con
 
 cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                    cudaStream_t st) {
+  if (cdtype == SPARK_BF16 && p.max_q > 1) return launch_paged_chunk(p, qdtype, k, v, st);
   return launch_paged_token(p, qdtype, cdtype, k, v, st);
 }
 

@@ -11,14 +11,15 @@
 namespace spark {
 
 // Workspace of spark_paged_append and spark_paged_attention: error word,
-// merge tickets, partial states.
+// merge tickets, the chunk kernel's joins, partial states.
 struct PagedWsLayout {
-  size_t tickets, part, total;
+  size_t tickets, joins, part, total;
 };
 inline PagedWsLayout paged_ws_layout() {
   PagedWsLayout L;
   L.tickets = 256;  // the error word sits at 0
-  L.part = align_up(L.tickets + sizeof(uint32_t) * paged::kMaxCtas, 256);
+  L.joins = align_up(L.tickets + sizeof(uint32_t) * paged::kMaxCtas, 256);
+  L.part = align_up(L.joins + sizeof(paged::Join) * paged::kMaxChunkCtas, 256);
   L.total = align_up(L.part + paged::kPartBytes, 256);
   return L;
 }
@@ -82,6 +83,7 @@ inline paged::Args paged_args(const spark_geom* g, const spark_page_pool* pool, 
   p.scale_log2 = g->scale * 1.4426950408889634f;
   p.err = ws_at<uint32_t>(ws, 0);
   p.tickets = ws_at<uint32_t>(ws, L.tickets);
+  p.joins = ws_at<paged::Join>(ws, L.joins);
   p.part = ws_at<float>(ws, L.part);
   return p;
 }

@@ -11,8 +11,24 @@ namespace paged {
 
 // CTAs of an attention launch at most (two partial slots each)
 constexpr int kMaxCtas = 320;
-// bytes of their partial states
-constexpr size_t kPartBytes = sizeof(float) * 2 * kMaxCtas * kPartFloats;
+// the chunk kernel: tokens of a group, CTAs at most, floats of a partial
+// state (128 rows of 256 dims, their maxima, their sums)
+constexpr int kChunkTokens = 32;
+constexpr int kMaxChunkCtas = 160;
+constexpr int kChunkPart = kGroup * kChunkTokens * (kHeadDim + 2);
+// bytes of the partial states of either kernel
+constexpr size_t kTokenPartBytes = sizeof(float) * 2 * kMaxCtas * kPartFloats;
+constexpr size_t kChunkPartBytes = sizeof(float) * 2 * kMaxChunkCtas * kChunkPart;
+constexpr size_t kPartBytes = kTokenPartBytes > kChunkPartBytes ? kTokenPartBytes : kChunkPartBytes;
+
+// A group of the chunk kernel that begins in a CTA's share and goes on behind
+// it: what the join needs.  n_rows 0: there is none.
+struct Join {
+  int32_t row0, n_rows;  // first token's row, rows (4 per token)
+  int32_t head, last;    // KV head, last CTA
+  int64_t begin, total;  // the group's first unit, units of the call
+  int32_t G, unused;     // CTAs that share them
+};
 
 struct Args {
   const int32_t* table;
@@ -27,6 +43,7 @@ struct Args {
   float scale_log2;
   uint32_t* err;
   uint32_t* tickets;  // [kMaxCtas], zero between launches
+  Join* joins;        // [kMaxChunkCtas]
   float* part;        // partial states, two slots per CTA
 };
 
