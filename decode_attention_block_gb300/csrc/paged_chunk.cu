@@ -17,7 +17,8 @@
 // K), and so is P: 16 significant bits each, fp32 sums.
 //
 // Tensor memory (512 columns): O 256, two buffers of 128 for S; P overwrites
-// its own S (hi in the first 64 columns, lo in the others).  Shared memory: Q
+// its own S, 32 positions at a time (hi in the first 16 of their columns, lo
+// in the others).  Shared memory: Q
 // (64 KB, 128 KB in two halves) and a ring of 32 KB slots, each 128 positions
 // x 128 dims of K or V.  Warp 0 fills the ring (TMA boxes of the part of a
 // page inside the tile), warp 1 issues the MMAs in the order S(i+1), P V(i),
@@ -73,6 +74,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return ffma2(a, make_float2(1.f, 1.f), b); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -134,6 +136,81 @@ __device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, 
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
+}
+
+// The columns x0 .. x1 of a tile that a row sees, as one bit per column of
+// the 32 from `first`.
+__device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
+  const int a = x0 - first, b = x1 + 1 - first;  // bits [a, b)
+  const uint32_t below_b = b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1u;
+  const uint32_t below_a = a >= 32 ? 0xffffffffu : a <= 0 ? 0u : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
+// The largest score of a row's tile at `ts` (EDGE: among the columns it sees).
+template <bool EDGE>
+__device__ __forceinline__ float tile_max(uint32_t ts, int x0, int x1) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t a[32], b[32];
+  auto fold = [&](const uint32_t (&s)[32], int first) {
+    const uint32_t seen = EDGE ? seen32(x0, x1, first) : 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      mx[i & 3] = fmaxf(mx[i & 3], !EDGE || ((seen >> i) & 1u) ? __uint_as_float(s[i]) : -INFINITY);
+  };
+  tc::ld32(ts, a);
+#pragma unroll 1
+  for (int ch = 0; ch < kPos; ch += 64) {
+    tc::wait_ld(a);
+    tc::ld32(ts + ch + 32, b);
+    fold(a, ch);
+    tc::wait_ld(b);
+    if (ch == 0) tc::ld32(ts + 64, a);
+    fold(b, ch + 32);
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// S at `ts` becomes P = e^(scale s - ref) in bf16 (SPLIT: and the remainders),
+// 32 columns at a time over their own scores; returns the row's sum.
+template <bool EDGE, bool SPLIT>
+__device__ __forceinline__ float tile_exp(uint32_t ts, float scale, float ref, int x0, int x1) {
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t a[32], b[32];
+  auto fold = [&](const uint32_t (&s)[32], int first) {
+    const uint32_t seen = EDGE ? seen32(x0, x1, first) : 0u;
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 t = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                             make_float2(scale, scale), make_float2(-ref, -ref));
+      float2 e = make_float2(ex2(t.x), ex2(t.y));
+      if (EDGE) {
+        e.x = ((seen >> (2 * i)) & 1u) ? e.x : 0.f;
+        e.y = ((seen >> (2 * i + 1)) & 1u) ? e.y : 0.f;
+      }
+      sum[i & 1] = fadd2(sum[i & 1], e);
+      hi[i] = pack2(e.x, e.y);
+      if (SPLIT) {
+        const float2 f = bf16x2_to_f32x2(hi[i]);
+        lo[i] = pack2(e.x - f.x, e.y - f.y);
+      }
+    }
+    tc::st16(ts + first, hi);
+    if (SPLIT) tc::st16(ts + first + 16, lo);
+  };
+  tc::ld32(ts, a);
+#pragma unroll 1
+  for (int ch = 0; ch < kPos; ch += 64) {
+    tc::wait_ld(a);
+    tc::ld32(ts + ch + 32, b);
+    fold(a, ch);
+    tc::wait_ld(b);
+    if (ch == 0) tc::ld32(ts + 64, a);
+    fold(b, ch + 32);
+  }
+  tc::wait_st();
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // 32 output dims of a row
@@ -330,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
             for (int ks = 0; ks < kPos / 16; ++ks)  // 16 positions: two 8-row groups, eight columns of P
-              tc::mma_ts(d, a + part * 64 + ks * 8, b + ks * (2048 >> 4), kIdO, !first || part + ks > 0);
+              tc::mma_ts(d, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b + ks * (2048 >> 4), kIdO,
+                         !first || part + ks > 0);
           tc::commit(&empty[s]);
         }
       }
@@ -398,20 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
           const int pos = (g.tile0 + (int)(u - cur.begin)) * kPos;
           const uint32_t ts = tmem + lanes + kColS + buf * kPos;
-          uint32_t s[kPos];
-          tc::ld128(ts, s);
           const bool whole = pos + kPos - 1 <= w_hi && pos >= w_lo;  // every row of the warp sees every position
           const int x0 = pos_lo - pos, x1 = pos_hi - pos;            // columns the row sees
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < kPos; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < kPos; ++i)
-              mx[i & 3] = fmaxf(mx[i & 3], i >= x0 && i <= x1 ? __uint_as_float(s[i]) : -INFINITY);
-          }
-          float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float mt = whole ? tile_max<false>(ts, 0, 0) : tile_max<true>(ts, x0, x1);
           mt = mt == -INFINITY ? mt : mt * scale;
           if (u == t0) {
             m = mt;
@@ -426,39 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int d = 0; d < kHeadDim; d += 32) {
               uint32_t o[32];
               tc::ld32(tmem + lanes + d, o);
+              tc::wait_ld(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
               tc::st32(tmem + lanes + d, o);
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t hi[32], lo[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int col = 64 * h + 2 * i;
-              const float2 t = ffma2(make_float2(__uint_as_float(s[col]), __uint_as_float(s[col + 1])),
-                                     make_float2(scale, scale), make_float2(-ref, -ref));
-              float2 e = make_float2(ex2(t.x), ex2(t.y));
-              if (!whole) {
-                e.x = col >= x0 && col <= x1 ? e.x : 0.f;
-                e.y = col + 1 >= x0 && col + 1 <= x1 ? e.y : 0.f;
-              }
-              sum[i & 1].x += e.x;
-              sum[i & 1].y += e.y;
-              hi[i] = pack2(e.x, e.y);
-              if (kSplit) {
-                const float2 f = bf16x2_to_f32x2(hi[i]);
-                lo[i] = pack2(e.x - f.x, e.y - f.y);
-              }
-            }
-            tc::st32(ts + 32 * h, hi);
-            if (kSplit) tc::st32(ts + 64 + 32 * h, lo);
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          tc::wait_st();
+          l += whole ? tile_exp<false, kSplit>(ts, scale, ref, 0, 0) : tile_exp<true, kSplit>(ts, scale, ref, x0, x1);
         }
         tc::fence_before();
         mbar_arrive(&p_full[buf]);
@@ -484,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = 0; d < kHeadDim; d += 32) {
           uint32_t o[32];
           tc::ld32(tmem + lanes + d, o);
+          tc::wait_ld(o);
           if (tok < g.n_tok) {
             if (split)
               store32(part + row * kHeadDim + d, o, 1.0f);
