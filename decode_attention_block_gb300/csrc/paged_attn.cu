@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(kTokThreads, MINB)
         const int pos = (cur.g.tile0 + (int)(u - cur.begin) + lane) * kTile;
         int z = 0;
         if (lane < n)
-          z = page_at(p, cur.s, paged::page_col(pos, p.page_size)) * p.page_size + paged::page_row(pos, p.page_size);
+          z = paged::page_of(p, paged::page_entry(p, cur.s, paged::page_col(pos, p.page_size))) * p.page_size +
+              paged::page_row(pos, p.page_size);
         for (int i = 0; i < n; ++i, ++k) {
           const int zi = __shfl_sync(0xffffffffu, z, i);
           if (lane == 0) {

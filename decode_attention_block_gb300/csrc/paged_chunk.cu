@@ -147,72 +147,45 @@ __device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
   return below_b & ~below_a;
 }
 
-// The largest score of a row's tile at `ts` (EDGE: among the columns it sees).
-template <bool EDGE>
-__device__ __forceinline__ float tile_max(uint32_t ts, int x0, int x1) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  uint32_t a[32], b[32];
-  auto fold = [&](const uint32_t (&s)[32], int first) {
-    const uint32_t seen = EDGE ? seen32(x0, x1, first) : 0u;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      mx[i & 3] = fmaxf(mx[i & 3], !EDGE || ((seen >> i) & 1u) ? __uint_as_float(s[i]) : -INFINITY);
-  };
-  tc::ld32(ts, a);
-#pragma unroll 1
-  for (int ch = 0; ch < kPos; ch += 64) {
-    tc::wait_ld(a);
-    tc::ld32(ts + ch + 32, b);
-    fold(a, ch);
-    tc::wait_ld(b);
-    if (ch == 0) tc::ld32(ts + 64, a);
-    fold(b, ch + 32);
-  }
-  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-}
-
-// S at `ts` becomes P = e^(scale s - ref) in bf16 (SPLIT: and the remainders),
-// 32 columns at a time over their own scores; returns the row's sum.
+// 32 scores of a row become P = e^(scale s - ref) in bf16 (SPLIT: and the
+// remainders) over their own columns at `ts`.
 template <bool EDGE, bool SPLIT>
-__device__ __forceinline__ float tile_exp(uint32_t ts, float scale, float ref, int x0, int x1) {
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  uint32_t a[32], b[32];
-  auto fold = [&](const uint32_t (&s)[32], int first) {
-    const uint32_t seen = EDGE ? seen32(x0, x1, first) : 0u;
-    uint32_t hi[16], lo[16];
+__device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], float scale, float ref, uint32_t seen,
+                                      float2 (&sum)[2]) {
+  uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 t = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                             make_float2(scale, scale), make_float2(-ref, -ref));
-      float2 e = make_float2(ex2(t.x), ex2(t.y));
-      if (EDGE) {
-        e.x = ((seen >> (2 * i)) & 1u) ? e.x : 0.f;
-        e.y = ((seen >> (2 * i + 1)) & 1u) ? e.y : 0.f;
-      }
-      sum[i & 1] = fadd2(sum[i & 1], e);
-      hi[i] = pack2(e.x, e.y);
-      if (SPLIT) {
-        const float2 f = bf16x2_to_f32x2(hi[i]);
-        lo[i] = pack2(e.x - f.x, e.y - f.y);
-      }
+  for (int i = 0; i < 16; ++i) {
+    const float2 t = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                           make_float2(scale, scale), make_float2(-ref, -ref));
+    float2 e = make_float2(ex2(t.x), ex2(t.y));
+    if (EDGE) {
+      e.x = ((seen >> (2 * i)) & 1u) ? e.x : 0.f;
+      e.y = ((seen >> (2 * i + 1)) & 1u) ? e.y : 0.f;
     }
-    tc::st16(ts + first, hi);
-    if (SPLIT) tc::st16(ts + first + 16, lo);
-  };
-  tc::ld32(ts, a);
-#pragma unroll 1
-  for (int ch = 0; ch < kPos; ch += 64) {
-    tc::wait_ld(a);
-    tc::ld32(ts + ch + 32, b);
-    fold(a, ch);
-    tc::wait_ld(b);
-    if (ch == 0) tc::ld32(ts + 64, a);
-    fold(b, ch + 32);
+    sum[i & 1] = fadd2(sum[i & 1], e);
+    hi[i] = pack2(e.x, e.y);
+    if (SPLIT) {
+      const float2 f = bf16x2_to_f32x2(hi[i]);
+      lo[i] = pack2(e.x - f.x, e.y - f.y);
+    }
   }
-  tc::wait_st();
-  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  tc::st16(ts, hi);
+  if (SPLIT) tc::st16(ts + 16, lo);
 }
 
+template <bool EDGE>
+__device__ __forceinline__ void max32(const uint32_t (&s)[32], uint32_t seen, float (&mx)[4]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = !EDGE || ((seen >> (i + k)) & 1u) ? __uint_as_float(s[i + k]) : -INFINITY;
+      const float y = !EDGE || ((seen >> (i + k + 4)) & 1u) ? __uint_as_float(s[i + k + 4]) : -INFINITY;
+      mx[k] = fmaxf(mx[k], fmaxf(x, y));
+    }
+}
+
+// 32 output dims of a row
 // 32 output dims of a row
 __device__ __forceinline__ void store32(float* dst, const uint32_t (&o)[32], float inv) {
 #pragma unroll
@@ -250,7 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] abort
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp's number, and below the MMA warp's loop bounds, by way of a
+  // shuffle: known to be the same in every lane, they and what follows from
+  // them stay in uniform registers, where an MMA takes its operands from)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
@@ -290,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 0) {
     // ---- producer: K(0), then K(i), V(i - 1) for the tiles of each group
@@ -317,16 +293,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (;;) {
       const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
+      // the boxes [b0, b1) of tile u that hold rows the group reads; the table's
+      // entry for the lane's box, asked for one tile ahead
+      auto boxes = [&](int64_t u, int& pos, int& b0, int& b1) {
+        pos = (cur.g.tile0 + (int)(u - cur.begin)) * kPos;
+        b0 = cur.g.lo > pos ? (cur.g.lo - pos) / box : 0;
+        b1 = cur.g.hi - pos >= kPos ? per : (cur.g.hi - pos) / box + 1;
+      };
+      auto entry = [&](int64_t u) {
+        int pos, b0, b1;
+        boxes(u, pos, b0, b1);
+        const int b = lane % per;
+        return b >= b0 && b < b1 ? paged::page_entry(p, cur.s, paged::page_col(pos + b * box, p.page_size)) : 0;
+      };
       int z_v = 0, v0 = 0, v1 = 0;  // the tile before
+      int ahead = entry(t0);
       for (int64_t u = t0; u <= t1 && ok; ++u) {
         int z = 0, b0 = 0, b1 = 0;
         if (u < t1) {
-          const int pos = (cur.g.tile0 + (int)(u - cur.begin)) * kPos;
-          b0 = cur.g.lo > pos ? (cur.g.lo - pos) / box : 0;
-          b1 = cur.g.hi - pos >= kPos ? per : (cur.g.hi - pos) / box + 1;
-          const int b = lane % per, x = pos + b * box;
-          if (b >= b0 && b < b1)
-            z = paged::page_at(p, cur.s, paged::page_col(x, p.page_size)) * p.page_size + paged::page_row(x, p.page_size);
+          int pos;
+          boxes(u, pos, b0, b1);
+          z = paged::page_of(p, ahead) * p.page_size + paged::page_row(pos + (lane % per) * box, p.page_size);
+          if (u + 1 < t1) ahead = entry(u + 1);
           slot(&tm_k, 0, z, b0, b1);
           slot(&tm_k, 1, z, b0, b1);
         }
@@ -352,12 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(&full[i % NS], (i / NS) & 1, &never, kWaitLimitNs);
     }
   } else if (warp == 1) {
-    // ---- MMA issuer (lane 0); the whole warp clears the rows of V tiles that
+    // ---- MMA issuer (one elected lane); the whole warp clears the rows of V tiles that
     // no token of the group sees (their P is 0, but they may hold anything)
     constexpr uint32_t kIdS = tc::idesc(kRows, kPos, false), kIdO = tc::idesc(kRows, kPos, true);
     const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + S::kRing);
     uint32_t k = 0, tile = 0, item = 0;
     bool ok = true;
+    const bool one = tc::elect();
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, flags, kWaitLimitNs));
       tc::fence_after();
@@ -365,28 +354,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto scores = [&](uint32_t i) {
       const uint32_t d = tmem + kColS + (i & 1) * kPos;
+#pragma unroll
       for (int half = 0; half < 2; ++half, ++k) {
         const int s = (int)(k % NS);
         if (!wait(&full[s], (k / NS) & 1)) return;
-        if (lane == 0) {
+        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot), a0 = tc::desc_k_major(q_addr + 2 * half * kLineBytes);
+        if (one) {
 #pragma unroll
-          for (int line = 0; line < 2; ++line) {
-            const uint64_t b = tc::desc_k_major(ring + s * kSlot + line * kLineBytes);
+          for (int line = 0; line < 2; ++line)
 #pragma unroll
-            for (int part = 0; part < S::kQ; ++part) {
-              const uint64_t a = tc::desc_k_major(q_addr + part * kQBytes + (2 * half + line) * kLineBytes);
+            for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) tc::mma_ss(d, a + 2 * ks, b + 2 * ks, kIdS, half + line + part + ks > 0);
-            }
-          }
+              for (int ks = 0; ks < 4; ++ks)
+                tc::mma_ss(d, a0 + ((part * kQBytes + line * kLineBytes) >> 4) + 2 * ks,
+                           b0 + (line * kLineBytes >> 4) + 2 * ks, kIdS, half + line + part + ks > 0);
           tc::commit(&empty[s]);
+          if (half == 1) tc::commit(&s_full[i & 1]);
         }
+        __syncwarp();
       }
-      if (lane == 0) tc::commit(&s_full[i & 1]);
     };
     auto values = [&](uint32_t i, bool first, int r0, int r1) {
       const uint32_t a = tmem + kColS + (i & 1) * kPos;
       if (!wait(&p_full[i & 1], (i >> 1) & 1)) return;
+#pragma unroll
       for (int half = 0; half < 2; ++half, ++k) {
         const int s = (int)(k % NS);
         if (!wait(&full[s], (k / NS) & 1)) return;
@@ -400,38 +391,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        if (lane == 0) {
-          const uint64_t b = tc::desc_mn_major(ring + s * kSlot, kLineBytes);
-          const uint32_t d = tmem + half * 128;
+        const uint64_t b0 = tc::desc_mn_major(ring + s * kSlot, kLineBytes);
+        const uint32_t d = tmem + half * 128;
+        if (one) {
 #pragma unroll
           for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
             for (int ks = 0; ks < kPos / 16; ++ks)  // 16 positions: two 8-row groups, eight columns of P
-              tc::mma_ts(d, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b + ks * (2048 >> 4), kIdO,
+              tc::mma_ts(d, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b0 + ks * (2048 >> 4), kIdO,
                          !first || part + ks > 0);
           tc::commit(&empty[s]);
+          if (half == 1) tc::commit(&pv_done[i & 1]);
         }
+        __syncwarp();
       }
-      if (lane == 0) tc::commit(&pv_done[i & 1]);
     };
     for (;;) {
       const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
+      const int n = __shfl_sync(0xffffffffu, (int)(t1 - t0), 0);  // tiles of the group in this share
+      const int pos0 = __shfl_sync(0xffffffffu, (cur.g.tile0 + (int)(t0 - cur.begin)) * kPos, 0);
+      const int lo = __shfl_sync(0xffffffffu, cur.g.lo, 0), hi = __shfl_sync(0xffffffffu, cur.g.hi, 0);
       if (!wait(q_full, item & 1)) break;
       ++item;
-      for (int64_t u = t0; u <= t1 && ok; ++u) {
-        if (u < t1) scores(tile + (uint32_t)(u - t0));
-        if (u > t0 && ok) {
-          const int pos = (cur.g.tile0 + (int)(u - 1 - cur.begin)) * kPos;
-          const int r0 = cur.g.lo > pos ? cur.g.lo - pos : 0;
-          const int r1 = cur.g.hi + 1 - pos < kPos ? cur.g.hi + 1 - pos : kPos;
-          values(tile + (uint32_t)(u - 1 - t0), u - 1 == t0, r0, r1);
+      for (int i = 0; i <= n && ok; ++i) {
+        if (i < n) scores(tile + i);
+        if (i > 0 && ok) {
+          const int pos = pos0 + (i - 1) * kPos;
+          values(tile + i - 1, i == 1, lo > pos ? lo - pos : 0, hi + 1 - pos < kPos ? hi + 1 - pos : kPos);
         }
       }
-      tile += (uint32_t)(t1 - t0);
-      if (!ok || cur.end >= u1) break;
+      tile += n;
+      if (!ok || __shfl_sync(0xffffffffu, (int)(cur.end >= u1), 0)) break;
       cur.next(p, sh);
     }
-    if (lane == 0) {
+    if (one) {
       if (!ok) {
         if (!flags[0]) atomicOr(p.err, kErrWaitTimeout);
         flags[0] = 1;
@@ -478,7 +471,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ts = tmem + lanes + kColS + buf * kPos;
           const bool whole = pos + kPos - 1 <= w_hi && pos >= w_lo;  // every row of the warp sees every position
           const int x0 = pos_lo - pos, x1 = pos_hi - pos;            // columns the row sees
-          float mt = whole ? tile_max<false>(ts, 0, 0) : tile_max<true>(ts, x0, x1);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // a whole tile's scores stay in registers; a masked one (a group's
+          // last, or its first behind a window) is read twice by a short loop
+          uint32_t s0[32], s1[32], s2[32], s3[32];
+          if (whole) {
+            tc::ld32(ts, s0);
+            tc::ld32(ts + 32, s1);
+            tc::ld32(ts + 64, s2);
+            tc::ld32(ts + 96, s3);
+            tc::wait_ld(s0);
+            tc::wait_ld(s1);
+            tc::wait_ld(s2);
+            tc::wait_ld(s3);
+            max32<false>(s0, 0, mx);
+            max32<false>(s1, 0, mx);
+            max32<false>(s2, 0, mx);
+            max32<false>(s3, 0, mx);
+          } else {
+#pragma unroll 1
+            for (int ch = 0; ch < kPos; ch += 32) {
+              tc::ld32(ts + ch, s0);
+              tc::wait_ld(s0);
+              max32<true>(s0, seen32(x0, x1, ch), mx);
+            }
+          }
+          float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           mt = mt == -INFINITY ? mt : mt * scale;
           if (u == t0) {
             m = mt;
@@ -500,7 +518,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          l += whole ? tile_exp<false, kSplit>(ts, scale, ref, 0, 0) : tile_exp<true, kSplit>(ts, scale, ref, x0, x1);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          if (whole) {
+            exp32<false, kSplit>(ts, s0, scale, ref, 0, sum);
+            exp32<false, kSplit>(ts + 32, s1, scale, ref, 0, sum);
+            exp32<false, kSplit>(ts + 64, s2, scale, ref, 0, sum);
+            exp32<false, kSplit>(ts + 96, s3, scale, ref, 0, sum);
+          } else {
+#pragma unroll 1
+            for (int ch = 0; ch < kPos; ch += 32) {
+              tc::ld32(ts + ch, s0);
+              tc::wait_ld(s0);
+              exp32<true, kSplit>(ts + ch, s0, scale, ref, seen32(x0, x1, ch), sum);
+            }
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tc::wait_st();
         }
         tc::fence_before();
         mbar_arrive(&p_full[buf]);

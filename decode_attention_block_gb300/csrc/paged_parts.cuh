@@ -140,15 +140,15 @@ struct Cursor {
   }
 };
 
-// The page of column `col` of sequence s; an entry outside the pool is
-// reported and read as page 0.
-__device__ __forceinline__ int page_at(const Args& p, int s, int col) {
-  const int pg = __ldcg(p.table + (int64_t)s * p.max_pages + col);
-  if (pg < 0 || pg >= p.n_pages) {
-    atomicOr(p.err, kErrIndex);
-    return 0;
-  }
-  return pg;
+// The table's entry for column `col` of sequence s ...
+__device__ __forceinline__ int page_entry(const Args& p, int s, int col) {
+  return __ldcg(p.table + (int64_t)s * p.max_pages + col);
+}
+// ... as a page: an entry outside the pool is reported and read as page 0.
+__device__ __forceinline__ int page_of(const Args& p, int entry) {
+  if (entry >= 0 && entry < p.n_pages) return entry;
+  atomicOr(p.err, kErrIndex);
+  return 0;
 }
 
 #endif  // __CUDACC__

@@ -23,6 +23,17 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // this thread's writes to tensor memory have completed
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// true in one lane of the (converged) warp, the same one every time
+__device__ __forceinline__ bool elect() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
 // D (+)= A B^T, bf16 in, fp32 accumulate; A from shared memory ...
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
