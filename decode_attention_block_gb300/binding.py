@@ -198,8 +198,15 @@ def declared_symbols() -> list[str]:
 # marshalling helpers
 # ---------------------------------------------------------------------------
 
+# the current stream's handle without building a torch.cuda.Stream around it
+# (0.2 us a call instead of 3)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -330,14 +337,16 @@ class PagePool(_CachedC):
     v: torch.Tensor
     _c: object = field(default=None, init=False, repr=False, compare=False)
 
-    def _build_c(self) -> SparkPagePool:
+    def _build_c(self) -> tuple:
+        """The C struct, its bytes (for arrays of them) and (n_kv, head_dim)."""
         dt = self.k.dtype
         if dt not in _DTYPE_CODE:
             raise TypeError(f"pages must be float32 or bfloat16, got {dt}")
         if self.k.dim() != 4 or self.k.shape != self.v.shape:
             raise ValueError("k and v must both be [n_pages, page_size, n_kv, head_dim]")
-        return SparkPagePool(_dev_ptr(self.k, "k", dt), _dev_ptr(self.v, "v", dt), int(self.k.shape[0]),
-                             int(self.k.shape[1]), _DTYPE_CODE[dt])
+        c = SparkPagePool(_dev_ptr(self.k, "k", dt), _dev_ptr(self.v, "v", dt), int(self.k.shape[0]),
+                          int(self.k.shape[1]), _DTYPE_CODE[dt])
+        return c, bytes(c), (int(self.k.shape[2]), int(self.k.shape[3]))
 
 
 @dataclass
@@ -364,10 +373,24 @@ class PagedBatch(_CachedC):
                                int(self.table.shape[1]), int(self.n_tokens), int(self.max_q_len))
 
 
-def _pool_heads(geom: SparkGeom, pool: PagePool) -> None:
-    if tuple(pool.k.shape[2:]) != (geom.n_kv, geom.head_dim):
-        raise ValueError(f"pages of {tuple(pool.k.shape[2:])} (heads, dims) do not fit the geometry "
-                         f"({geom.n_kv}, {geom.head_dim})")
+def _heads_differ(got, want) -> ValueError:
+    return ValueError(f"pages of {got} (heads, dims) do not fit the geometry {want}")
+
+
+def _pool_c(geom: SparkGeom, pool: PagePool) -> SparkPagePool:
+    c, _, heads = pool.to_c()
+    if heads != (geom.n_kv, geom.head_dim):
+        raise _heads_differ(heads, (geom.n_kv, geom.head_dim))
+    return c
+
+
+def _pools_c(geom: SparkGeom, pools) -> ctypes.Array:
+    want = (geom.n_kv, geom.head_dim)
+    built = [p._c or p.to_c() for p in pools]
+    for _, _, heads in built:
+        if heads != want:
+            raise _heads_differ(heads, want)
+    return (SparkPagePool * len(built)).from_buffer_copy(b"".join([b[1] for b in built]) or bytes(ctypes.sizeof(SparkPagePool)))
 
 
 # ---------------------------------------------------------------------------
@@ -577,8 +600,7 @@ def spark_paged_append(geom: SparkGeom, k: torch.Tensor, v: torch.Tensor, pool: 
         raise ValueError(f"k and v must be [n_tokens, {kv_dim}]")
     if vdt != dt or vld != ld:
         raise ValueError("k and v must have the same dtype and row stride")
-    _pool_heads(geom, pool)
-    pc, bc = pool.to_c(), batch.to_c()
+    pc, bc = _pool_c(geom, pool), batch.to_c()
     _check(load().spark_paged_append(ctypes.byref(geom), kp, vp, ld, dt, ctypes.byref(pc), ctypes.byref(bc),
                                      _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
            "spark_paged_append")
@@ -591,8 +613,7 @@ def spark_paged_attention(geom: SparkGeom, q: torch.Tensor, pool: PagePool, laye
     qp, ld, dt = _rows(q, "q")
     if q.shape != (batch.n_tokens, geom.n_q * geom.head_dim) or a.shape != q.shape:
         raise ValueError(f"q and a must be [n_tokens, {geom.n_q * geom.head_dim}]")
-    _pool_heads(geom, pool)
-    pc, bc = pool.to_c(), batch.to_c()
+    pc, bc = _pool_c(geom, pool), batch.to_c()
     _check(load().spark_paged_attention(ctypes.byref(geom), qp, ld, dt, ctypes.byref(pc), int(layer_class),
                                         ctypes.byref(bc), _dev_ptr(a, "a", q.dtype), _dev_ptr(ws, "workspace"),
                                         ws.numel() * ws.element_size(), _stream(stream)), "spark_paged_attention")
@@ -605,8 +626,7 @@ def spark_attn_paged(geom: SparkGeom, h: torch.Tensor, weights: LayerWeights, po
     out [n_tokens, hidden]; positions: each row's rope position (host)."""
     if h.shape != (batch.n_tokens, geom.hidden) or out.shape != h.shape or len(positions) != batch.n_tokens:
         raise ValueError("h and out must be [n_tokens, hidden], with one position per row")
-    _pool_heads(geom, pool)
-    wc, pc, bc = weights.to_c(), pool.to_c(), batch.to_c()
+    wc, pc, bc = weights.to_c(), _pool_c(geom, pool), batch.to_c()
     _check(load().spark_attn_paged(ctypes.byref(geom), _dev_ptr(h, "h", torch.float32), ctypes.byref(wc),
                                    ctypes.byref(pc), int(layer_class), ctypes.byref(bc), _positions(positions),
                                    _dev_ptr(out, "out", torch.float32), _dev_ptr(ws, "workspace"),
@@ -624,12 +644,6 @@ def make_pages_workspace(n_pages: int, n_slots: int, device=None, stream=None) -
     return _workspace(spark_pages_workspace_bytes(n_pages, n_slots), "number of pages or slots", device, stream)
 
 
-def _pools(geom: SparkGeom, pools) -> ctypes.Array:
-    for p in pools:
-        _pool_heads(geom, p)
-    return (SparkPagePool * len(pools))(*[p.to_c() for p in pools])
-
-
 def spark_pages_remap(geom: SparkGeom, pools, table: torch.Tensor, parent: torch.Tensor, keep_len: torch.Tensor,
                       new_len: torch.Tensor, new_table: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """The page tables of a step: row s of new_table holds the first
@@ -639,7 +653,7 @@ def spark_pages_remap(geom: SparkGeom, pools, table: torch.Tensor, parent: torch
     if table.dim() != 2 or new_table.shape != table.shape or not parent.shape == keep_len.shape == new_len.shape == (n,):
         raise ValueError("table and new_table must be [n_slots, max_pages], the lists [n_slots]")
     i32 = torch.int32
-    _check(load().spark_pages_remap(ctypes.byref(geom), _pools(geom, pools), len(pools), _dev_ptr(table, "table", i32),
+    _check(load().spark_pages_remap(ctypes.byref(geom), _pools_c(geom, pools), len(pools), _dev_ptr(table, "table", i32),
                                     n, int(table.shape[1]), _dev_ptr(parent, "parent", i32),
                                     _dev_ptr(keep_len, "keep_len", i32), _dev_ptr(new_len, "new_len", i32),
                                     _dev_ptr(new_table, "new_table", i32), _dev_ptr(ws, "workspace"),
@@ -653,7 +667,7 @@ def spark_pages_compact(geom: SparkGeom, pools, table: torch.Tensor, new_table: 
     if table.dim() != 2 or new_table.shape != table.shape or n_live.numel() != 1:
         raise ValueError("table and new_table must be [n_slots, max_pages], n_live one element")
     i32 = torch.int32
-    _check(load().spark_pages_compact(ctypes.byref(geom), _pools(geom, pools), len(pools),
+    _check(load().spark_pages_compact(ctypes.byref(geom), _pools_c(geom, pools), len(pools),
                                       _dev_ptr(table, "table", i32), int(table.shape[0]), int(table.shape[1]),
                                       _dev_ptr(new_table, "new_table", i32), _dev_ptr(n_live, "n_live", i32),
                                       _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),

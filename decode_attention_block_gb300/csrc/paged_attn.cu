@@ -341,47 +341,81 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// One CTA per new token: its sequence by binary search in q_start, then its K
-// and V rows.  Bound by the rows' bytes; a row is 512 B to 8 KB.
+// A CTA takes up to kAppendTokens consecutive tokens: their page rows first,
+// one thread each (a binary search in q_start, then the table), then the
+// rows' words four at a time per thread, whatever rows they are of.  Bound by
+// the rows' bytes where there are many, by the chain of dependent loads where
+// there are few.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 16;
+constexpr int kAppendUnroll = 4;
+
 template <typename XT, typename CT>
-__global__ void __launch_bounds__(256)
-    k_paged_append(const XT* k, const XT* v, int64_t ld, CT* pk, CT* pv,
-                   const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(kAppendThreads)
+    k_paged_append(const XT* k, const XT* v, int64_t ld, CT* pk, CT* pv, int per, const __grid_constant__ Args p) {
+  __shared__ int64_t to[kAppendTokens];
   pdl_wait();
   // no early trigger: a kernel that reads pages before its own wait must not
   // start before these rows are written
-  const int t = blockIdx.x;
-  int lo = 0, hi = p.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldcg(p.q_start + mid) <= t) lo = mid; else hi = mid - 1;
+  const int t0 = blockIdx.x * per;
+  const int row4 = p.n_kv * kHeadDim / 4;  // words of four elements in a row
+  if (threadIdx.x < per) {
+    const int t = t0 + threadIdx.x;
+    int64_t at = -1;
+    if (t < p.n_tokens) {
+      int lo = 0, hi = p.n_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldcg(p.q_start + mid) <= t) lo = mid; else hi = mid - 1;
+      }
+      const paged::Seq s = paged::load_seq(p, lo);
+      if (s.bad) atomicOr(p.err, kErrIndex);
+      if (t >= s.q0 && t < s.q0 + s.n) {  // else: behind the last sequence, or a sequence that makes no sense
+        const int pos = s.p0 + (t - s.q0);
+        const int pg = paged::page_entry(p, lo, paged::page_col(pos, p.page_size));
+        if (pg >= 0 && pg < p.n_pages)
+          at = ((int64_t)pg * p.page_size + paged::page_row(pos, p.page_size)) * row4;
+        else
+          atomicOr(p.err, kErrIndex);
+      }
+    }
+    to[threadIdx.x] = at;
   }
-  const paged::Seq s = paged::load_seq(p, lo);
-  if (s.bad) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
-    return;
-  }
-  if (t < s.q0 || t >= s.q0 + s.n) return;  // behind the last sequence
-  const int pos = s.p0 + (t - s.q0);
-  const int pg = __ldcg(p.table + (int64_t)lo * p.max_pages + paged::page_col(pos, p.page_size));
-  if (pg < 0 || pg >= p.n_pages) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
-    return;
-  }
-  const int row = p.n_kv * kHeadDim;
-  const int64_t to = ((int64_t)pg * p.page_size + paged::page_row(pos, p.page_size)) * row;
-  for (int e = 4 * threadIdx.x; e < row; e += 4 * 256) {
-    const float4 x = load4(k + t * ld + e), y = load4(v + t * ld + e);
-    store4(pk + to + e, x);
-    store4(pv + to + e, y);
+  __syncthreads();
+  const int words = per * row4;
+  for (int w0 = threadIdx.x; w0 < words; w0 += kAppendThreads * kAppendUnroll) {
+    float4 x[kAppendUnroll], y[kAppendUnroll];
+    int64_t dst[kAppendUnroll];
+#pragma unroll
+    for (int i = 0; i < kAppendUnroll; ++i) {
+      const int w = w0 + i * kAppendThreads;
+      const int t = w < words ? w / row4 : 0, e = w - t * row4;
+      dst[i] = w < words && to[t] >= 0 ? to[t] + e : -1;
+      if (dst[i] >= 0) {
+        const int64_t src = (int64_t)(t0 + t) * ld + 4 * e;
+        x[i] = load4(k + src);
+        y[i] = load4(v + src);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendUnroll; ++i)
+      if (dst[i] >= 0) {
+        store4(pk + 4 * dst[i], x[i]);
+        store4(pv + 4 * dst[i], y[i]);
+      }
   }
 }
 
 template <typename XT, typename CT>
 cudaError_t launch_append_t(const Args& p, const void* k, const void* v, int64_t ld, void* pk, void* pv,
                             cudaStream_t st) {
-  return launch_pdl(k_paged_append<XT, CT>, dim3(p.n_tokens), dim3(256), 0, st, static_cast<const XT*>(k),
-                    static_cast<const XT*>(v), ld, static_cast<CT*>(pk), static_cast<CT*>(pv), p);
+  // one token per CTA until the CTAs that run at once (eight an SM) have one each
+  const int at_once = 8 * device_sm_count();
+  int per = (p.n_tokens + at_once - 1) / at_once;
+  if (per > kAppendTokens) per = kAppendTokens;
+  return launch_pdl(k_paged_append<XT, CT>, dim3((p.n_tokens + per - 1) / per), dim3(kAppendThreads), 0, st,
+                    static_cast<const XT*>(k), static_cast<const XT*>(v), ld, static_cast<CT*>(pk),
+                    static_cast<CT*>(pv), per, p);
 }
 
 }  // namespace

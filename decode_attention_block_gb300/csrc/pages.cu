@@ -7,10 +7,12 @@
 //            slot s the lowest of those that keep it so (an atomicMin, so the
 //            outcome does not depend on the order of arrivals);
 //   compact  0 unused, 1 used, then the page's rank among those that move.
-// The plan is a few dependent passes over tables and pages of a few hundred
-// KB at most in use: one cluster of 8 CTAs runs them, hardware cluster
-// barriers between the passes, so a step costs one launch for the plan and
-// one for the copies, which read the list of moves the plan left.
+// The plan is a few dependent passes over the tables and the pages' words.
+// Small pools and tables (kSmallPages, kSmallEntries) take one CTA with the
+// words in shared memory, larger ones a cluster of 8 CTAs with the words in
+// the workspace and hardware cluster barriers between the passes; so a step
+// costs one launch for the plan and one for the copies, which read the list
+// of moves the plan left.
 #include <limits.h>
 
 #include "attn_parts.cuh"
@@ -24,7 +26,8 @@ using pages::Move;
 
 constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanAll = kPlanCtas * kPlanThreads;
+constexpr int64_t kSmallPages = 24576;    // state and list: 192 KB of shared memory
+constexpr int64_t kSmallEntries = 65536;  // table entries: 256 KB, 64 a thread
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;                                   // 16-byte words per thread and piece
 constexpr int kPiece = kCopyThreads * kCopyVecs * 16;          // bytes a CTA copies at a time
@@ -77,35 +80,63 @@ struct PlanArgs {
   int32_t* list;   // [n_pages]
 };
 
-// the range of pages a thread of the cluster counts
-__device__ __forceinline__ void my_pages(const PlanArgs& p, int cta, int& lo, int& hi) {
-  const long long n = p.n_pages, i = (long long)cta * kPlanThreads + threadIdx.x;
-  lo = (int)(n * i / kPlanAll);
-  hi = (int)(n * (i + 1) / kPlanAll);
-}
-
-// pages counted by the CTAs before this one, and by all (after a cluster barrier)
-__device__ __forceinline__ void cta_totals(const PlanArgs& p, int cta, long long& before, long long& all) {
-  before = all = 0;
-  for (int c = 0; c < kPlanCtas; ++c) {
-    const int t = __ldcg(&p.head->totals[c]);
-    if (c < cta) before += t;
-    all += t;
+// The plan's CTAs, with the pages' words in shared memory (one CTA) or in the
+// workspace (a cluster).
+template <int CTAS>
+struct Plan {
+  static constexpr int kAll = CTAS * kPlanThreads;
+  int32_t *state, *list;
+  __device__ __forceinline__ explicit Plan(const PlanArgs& p) {
+    extern __shared__ int32_t small[];
+    state = CTAS == 1 ? small : p.state;
+    list = CTAS == 1 ? small + p.n_pages : p.list;
   }
-}
+  __device__ __forceinline__ static void sync() {
+    if (CTAS == 1)
+      __syncthreads();
+    else
+      cluster_sync_all();
+  }
+  // a word that other threads wrote
+  __device__ __forceinline__ static int get(const int32_t* w) { return CTAS == 1 ? *w : __ldcg(w); }
+  // the range of pages a thread counts
+  __device__ __forceinline__ static void my_pages(const PlanArgs& p, int cta, int& lo, int& hi) {
+    const long long n = p.n_pages, i = (long long)cta * kPlanThreads + threadIdx.x;
+    lo = (int)(n * i / kAll);
+    hi = (int)(n * (i + 1) / kAll);
+  }
+  // pages counted by the CTAs before this one, and by all
+  __device__ __forceinline__ static void totals(const PlanArgs& p, const PlanSmem& sm, int cta, long long& before,
+                                                long long& all) {
+    before = all = 0;
+    if (CTAS == 1) {
+      all = sm.total;
+      return;
+    }
+    if (threadIdx.x == 0) p.head->totals[cta] = (int)sm.total;
+    sync();
+    for (int c = 0; c < CTAS; ++c) {
+      const int t = __ldcg(&p.head->totals[c]);
+      if (c < cta) before += t;
+      all += t;
+    }
+  }
+};
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    k_pages_remap(const __grid_constant__ PlanArgs p) {
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanThreads) k_pages_remap(const __grid_constant__ PlanArgs p) {
   __shared__ PlanSmem sm;
+  using P = Plan<CTAS>;
+  const P pl(p);
   const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
-  const int all = cta * kPlanThreads + tid, warps = kPlanAll / 32, wid = all >> 5;
+  const int all = cta * kPlanThreads + tid, warps = P::kAll / 32, wid = all >> 5;
   pdl_wait();
-  for (int i = all; i < p.n_pages; i += kPlanAll) p.state[i] = INT_MAX;
+  for (int i = all; i < p.n_pages; i += P::kAll) pl.state[i] = INT_MAX;
   if (all == 0) {
     p.head->bad = 0;
     p.head->n_moves = 0;
   }
-  cluster_sync_all();
+  P::sync();
   // who keeps what
   for (int s = wid; s < p.n_slots; s += warps) {
     const int par = __ldcg(p.parent + s), keep = __ldcg(p.keep + s), grow = __ldcg(p.grow + s);
@@ -120,14 +151,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (pg < 0 || pg >= p.n_pages)
           bad = true;
         else if (i < whole)
-          p.state[pg] = -1;  // the lowest value there is: no order of arrival matters
+          pl.state[pg] = -1;  // the lowest value there is: no order of arrival matters
         else
-          atomicMin(&p.state[pg], s);
+          atomicMin(&pl.state[pg], s);
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) p.head->bad = 1;
   }
-  cluster_sync_all();
+  P::sync();
   const bool bad = __ldcg(&p.head->bad) != 0;  // the same in every CTA
   // pages each slot needs, and where they start among all new pages (every
   // CTA for itself: n_slots <= the block)
@@ -137,7 +168,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int rest = keep % p.page_size;
     if (rest != 0) {
       const int pg = __ldcg(p.table + (long long)__ldcg(p.parent + tid) * p.max_pages + keep / p.page_size);
-      copied = __ldcg(&p.state[pg]) != tid;
+      copied = P::get(&pl.state[pg]) != tid;
     }
     need = copied + (int)(((long long)grow + p.page_size - 1) / p.page_size) -
            (int)(((long long)keep + p.page_size - 1) / p.page_size);
@@ -152,21 +183,19 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   }
   // the free pages, lowest first
   int lo, hi, mine = 0;
-  my_pages(p, cta, lo, hi);
-  for (int i = lo; i < hi; ++i) mine += __ldcg(&p.state[i]) == INT_MAX;
+  P::my_pages(p, cta, lo, hi);
+  for (int i = lo; i < hi; ++i) mine += P::get(&pl.state[i]) == INT_MAX;
   const long long rank = block_scan(mine, sm);
-  if (tid == 0) p.head->totals[cta] = (int)sm.total;
-  cluster_sync_all();
   long long before, free_all;
-  cta_totals(p, cta, before, free_all);
+  P::totals(p, sm, cta, before, free_all);
   if (bad || want > free_all) {
     if (all == 0) atomicOr(p.err, bad ? kErrIndex : kErrPages);
     return;  // every CTA of the cluster alike
   }
   long long r = before + rank;
   for (int i = lo; i < hi && r < want; ++i)
-    if (__ldcg(&p.state[i]) == INT_MAX) p.list[r++] = i;
-  cluster_sync_all();
+    if (P::get(&pl.state[i]) == INT_MAX) pl.list[r++] = i;
+  P::sync();
   // the new tables and the copies
   for (int s = wid; s < p.n_slots; s += warps) {
     const int par = __ldcg(p.parent + s), keep = __ldcg(p.keep + s), grow = __ldcg(p.grow + s);
@@ -180,7 +209,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       if (i < whole || (i < kept && cp < 0)) {
         pg = __ldcg(old + i);
       } else if (i < end) {
-        pg = __ldcg(&p.list[off + i - whole - (cp < 0 && rest != 0 ? 1 : 0)]);
+        pg = P::get(&pl.list[off + i - whole - (cp < 0 && rest != 0 ? 1 : 0)]);
         if (i < kept) p.moves[cp] = Move{__ldcg(old + i), pg, rest, 0};
       }
       out[i] = pg;
@@ -189,38 +218,38 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   if (all == 0) p.head->n_moves = n_copies;
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    k_pages_compact(const __grid_constant__ PlanArgs p) {
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanThreads) k_pages_compact(const __grid_constant__ PlanArgs p) {
   __shared__ PlanSmem sm;
+  using P = Plan<CTAS>;
+  const P pl(p);
   const int tid = threadIdx.x, cta = blockIdx.x, all = cta * kPlanThreads + tid;
   const long long entries = (long long)p.n_slots * p.max_pages;
   pdl_wait();
-  for (int i = all; i < p.n_pages; i += kPlanAll) p.state[i] = 0;
+  for (int i = all; i < p.n_pages; i += P::kAll) pl.state[i] = 0;
   if (all == 0) {
     p.head->bad = 0;
     p.head->n_moves = 0;
     p.head->below = 0;
   }
-  cluster_sync_all();
+  P::sync();
   bool bad = false;
-  for (long long i = all; i < entries; i += kPlanAll) {
+  for (long long i = all; i < entries; i += P::kAll) {
     const int pg = __ldcg(p.table + i);
     if (pg < -1 || pg >= p.n_pages)
       bad = true;
     else if (pg >= 0)
-      p.state[pg] = 1;
+      pl.state[pg] = 1;
   }
   if (bad) p.head->bad = 1;
-  cluster_sync_all();
+  P::sync();
   bad = __ldcg(&p.head->bad) != 0;
   int lo, hi, mine = 0;
-  my_pages(p, cta, lo, hi);
-  for (int i = lo; i < hi; ++i) mine += __ldcg(&p.state[i]);
+  P::my_pages(p, cta, lo, hi);
+  for (int i = lo; i < hi; ++i) mine += P::get(&pl.state[i]);
   const long long rank = block_scan(mine, sm);
-  if (tid == 0) p.head->totals[cta] = (int)sm.total;
-  cluster_sync_all();
   long long before, n_live;
-  cta_totals(p, cta, before, n_live);
+  P::totals(p, sm, cta, before, n_live);
   if (bad) {
     if (all == 0) {
       atomicOr(p.err, kErrIndex);
@@ -231,17 +260,17 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   // used pages before page n_live
   if (lo <= n_live && n_live < hi) {
     int b = (int)(before + rank);
-    for (int i = lo; i < (int)n_live; ++i) b += __ldcg(&p.state[i]);
+    for (int i = lo; i < (int)n_live; ++i) b += P::get(&pl.state[i]);
     p.head->below = b;
   } else if (n_live == p.n_pages && all == 0) {
     p.head->below = p.n_pages;
   }
-  cluster_sync_all();
+  P::sync();
   const int below = __ldcg(&p.head->below);
   // move i: the i-th used page at or behind n_live to the i-th unused one before it
   int used = (int)(before + rank);
   for (int i = lo; i < hi; ++i) {
-    const int u = __ldcg(&p.state[i]);
+    const int u = P::get(&pl.state[i]);
     if (i < n_live) {
       if (u == 0) {
         p.moves[i - used].dst = i;
@@ -249,14 +278,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       }
     } else if (u != 0) {
       p.moves[used - below].src = i;
-      p.state[i] = used - below;
+      pl.state[i] = used - below;
     }
     used += u;
   }
-  cluster_sync_all();
-  for (long long i = all; i < entries; i += kPlanAll) {
+  P::sync();
+  for (long long i = all; i < entries; i += P::kAll) {
     const int pg = __ldcg(p.table + i);
-    p.new_table[i] = pg < n_live ? pg : __ldcg(&p.moves[__ldcg(&p.state[pg])].dst);
+    p.new_table[i] = pg < n_live ? pg : __ldcg(&p.moves[P::get(&pl.state[pg])].dst);
   }
   if (all == 0) {
     *p.n_live = (int)n_live;
@@ -265,49 +294,74 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 }
 
 // The moves of a plan in every pool's K and V: a CTA copies pieces of 16 KB,
-// all of a piece's loads in flight together.  Sources are kept pages and
-// targets free ones, so no page is read and written.
+// all of a piece's loads in flight together, the next piece's move asked for
+// before them.  Sources are kept pages and targets free ones, so no page is
+// read and written.  Pieces are numbered move by move, then by pool and side,
+// and dealt to the CTAs in turn.
 __global__ void __launch_bounds__(kCopyThreads)
     k_pages_copy(const pages::Head* head, const Move* moves, int row_bytes, int pieces, int n_pools,
                  const __grid_constant__ pages::Pools pools, int64_t page_bytes) {
   pdl_wait();
   const int n_moves = __ldcg(&head->n_moves);
-  const int sides = 2 * n_pools;
-  const int64_t units = (int64_t)n_moves * sides * pieces;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int piece = (int)(u % pieces);
-    const int64_t w = u / pieces;
-    const int side = (int)(w % sides), m = (int)(w / sides);
-    const int src = __ldcg(&moves[m].src), dst = __ldcg(&moves[m].dst), rows = __ldcg(&moves[m].rows);
-    const int64_t bytes = (int64_t)rows * row_bytes, at = (int64_t)piece * kPiece;
-    if (at >= bytes) continue;
+  const int per_move = 2 * n_pools * pieces;
+  int m = (int)(blockIdx.x / per_move), at = (int)(blockIdx.x % per_move);
+  const int dm = (int)(gridDim.x / per_move), dat = (int)(gridDim.x % per_move);
+  auto load = [&](int i) { return __ldcg(reinterpret_cast<const int4*>(moves) + i); };  // src, dst, rows
+  int4 next = m < n_moves ? load(m) : make_int4(0, 0, 0, 0);
+  while (m < n_moves) {
+    const int4 mv = next;
+    const int side = at / pieces;
+    const int64_t off = (int64_t)(at - side * pieces) * kPiece;
+    m += dm;
+    at += dat;
+    if (at >= per_move) {
+      at -= per_move;
+      ++m;
+    }
+    if (m < n_moves) next = load(m);
+    const int64_t bytes = (int64_t)mv.z * row_bytes;
+    if (off >= bytes) continue;
     unsigned char* base = static_cast<unsigned char*>(pools.p[side]);
-    const unsigned char* from = base + src * page_bytes + at;
-    unsigned char* to = base + dst * page_bytes + at;
+    const unsigned char* from = base + mv.x * page_bytes + off;
+    unsigned char* to = base + mv.y * page_bytes + off;
+    const int n = bytes - off < kPiece ? (int)(bytes - off) : kPiece;
     uint4 v[kCopyVecs];
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i) {
-      const int64_t o = 16 * (threadIdx.x + (int64_t)i * kCopyThreads);
-      if (at + o < bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(from + o));
+      const int o = 16 * ((int)threadIdx.x + i * kCopyThreads);
+      if (o < n) v[i] = __ldcs(reinterpret_cast<const uint4*>(from + o));
     }
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i) {
-      const int64_t o = 16 * (threadIdx.x + (int64_t)i * kCopyThreads);
-      if (at + o < bytes) __stcs(reinterpret_cast<uint4*>(to + o), v[i]);
+      const int o = 16 * ((int)threadIdx.x + i * kCopyThreads);
+      if (o < n) __stcs(reinterpret_cast<uint4*>(to + o), v[i]);
     }
   }
 }
 
-cudaError_t launch_plan(void (*kern)(PlanArgs), const PlanArgs& p, cudaStream_t st) {
+template <int CTAS>
+cudaError_t launch_plan(bool remap, const PlanArgs& p, cudaStream_t st) {
+  auto kern = remap ? k_pages_remap<CTAS> : k_pages_compact<CTAS>;
+  const size_t smem = CTAS == 1 ? 2 * sizeof(int32_t) * (size_t)p.n_pages : 0;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * sizeof(int32_t) * kSmallPages));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kPlanCtas);
+  cfg.gridDim = dim3(CTAS);
   cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -332,7 +386,9 @@ cudaError_t launch_pages(const pages::Call& c, cudaStream_t st) {
   p.moves = reinterpret_cast<Move*>(ws + L.moves);
   p.state = reinterpret_cast<int32_t*>(ws + L.state);
   p.list = reinterpret_cast<int32_t*>(ws + L.list);
-  cudaError_t e = launch_plan(c.parent ? k_pages_remap : k_pages_compact, p, st);
+  const bool small = c.n_pages <= kSmallPages && (int64_t)c.n_slots * c.max_pages <= kSmallEntries;
+  const bool remap = c.parent != nullptr;
+  cudaError_t e = small ? launch_plan<1>(remap, p, st) : launch_plan<kPlanCtas>(remap, p, st);
   if (e != cudaSuccess) return e;
   const int64_t page_bytes = (int64_t)c.page_size * c.row_bytes;
   const int pieces = (int)((page_bytes + kPiece - 1) / kPiece);

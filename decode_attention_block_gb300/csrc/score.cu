@@ -134,17 +134,29 @@ __device__ __forceinline__ void fold_top(Smem& sm, const Key (&key)[N], int k) {
 
 // (loads that stay behind the wait on the kernel before, whose output the
 // logits may be)
-__device__ __forceinline__ void unpack(const float* p, float (&x)[4]) {
-  const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ uint4 load_word(const void* p) { return __ldcs(static_cast<const uint4*>(p)); }
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[4]) {
   x[0] = __uint_as_float(w.x);
   x[1] = __uint_as_float(w.y);
   x[2] = __uint_as_float(w.z);
   x[3] = __uint_as_float(w.w);
 }
-__device__ __forceinline__ void unpack(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[8]) {
   const float2 a = bf16x2_to_f32x2(w.x), b = bf16x2_to_f32x2(w.y), c = bf16x2_to_f32x2(w.z), d = bf16x2_to_f32x2(w.w);
   x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y; x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+}
+__device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+// the larger of two, a NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float load1(const float* p) { return __ldcg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(__ldcg(p)); }
@@ -176,31 +188,52 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t w0 = words * c / parts, w1 = words * (c + 1) / parts;
   Stat st = {-INFINITY, 0.f, 0.f, 0};
   __syncthreads();
-  for (int64_t t = w0; t < w1; t += kThreads * kWords) {
-    float v[kPer];
-    int idx0[kWords];
+  float least = -INFINITY;  // value of the k-th best so far: nothing below it is an alternative
+  // the words of a tile; an edge of the row, or what lies behind the part, as
+  // the bits of -inf
+  auto fetch = [&](int64_t t, uint4 (&w)[kWords]) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int64_t w = t + tid + (int64_t)i * kThreads;
-      const int64_t e0 = w * kE - shift;  // index of the word's first element
-      idx0[i] = (int)e0;
-      float y[kE];
-      if (w < w1 && e0 >= 0 && e0 + kE <= vocab) {
-        unpack(base + w * kE, y);
+      const int64_t at = t + tid + (int64_t)i * kThreads;
+      const int64_t e0 = at * kE - shift;  // index of the word's first element
+      if (at < w1 && e0 >= 0 && e0 + kE <= vocab) {
+        w[i] = load_word(base + at * kE);
       } else {
+        constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+        uint32_t b[4] = {kNone, kNone, kNone, kNone};
+        if (at < w1) {
 #pragma unroll
-        for (int j = 0; j < kE; ++j)  // an edge of the row, or behind the part
-          y[j] = w < w1 && e0 + j >= 0 && e0 + j < vocab ? load1(x + e0 + j) : -INFINITY;
+          for (int j = 0; j < kE; ++j)
+            if (e0 + j >= 0 && e0 + j < vocab) {
+              const uint32_t v = bits_of(__ldcg(x + e0 + j));
+              if (sizeof(T) == 4)
+                b[j % 4] = v;
+              else
+                b[j / 2 % 4] = (j & 1) ? (b[j / 2 % 4] & 0xFFFFu) | (v << 16) : (b[j / 2 % 4] & 0xFFFF0000u) | v;
+            }
+        }
+        w[i] = make_uint4(b[0], b[1], b[2], b[3]);
       }
+    }
+  };
+  uint4 word[kWords];
+  if (w0 < w1) fetch(w0, word);
+  for (int64_t t = w0; t < w1; t += kThreads * kWords) {
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      float y[kE];
+      unpack(word[i], y);
 #pragma unroll
       for (int j = 0; j < kE; ++j) v[i * kE + j] = y[j];
     }
-    float tm = -INFINITY;
+    // the next tile's loads run while this one is folded in
+    if (t + kThreads * kWords < w1) fetch(t + kThreads * kWords, word);
+    float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      tm = fmaxf(tm, v[i]);
-      st.bad |= !(v[i] < INFINITY);
-    }
+    for (int i = 4; i < kPer; ++i) mx[i & 3] = max_nan(mx[i & 3], v[i]);
+    const float tm = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+    st.bad |= !(tm < INFINITY);
     if (tm > st.m) {
       const float d = st.m == -INFINITY ? 0.f : st.m - tm, e = expf(d);
       st.u = e > 0.f ? (st.u + d * st.z) * e : 0.f;
@@ -208,23 +241,35 @@ __global__ void __launch_bounds__(kThreads)
       st.m = tm;
     }
     const float ref = st.m == -INFINITY ? 0.f : st.m;
+    float2 z = make_float2(0.f, 0.f), u = z;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float d = v[i] - ref, e = exp2f(d * 1.4426950408889634f);
-      st.z += e;
-      st.u += e > 0.f ? d * e : 0.f;
+    for (int i = 0; i < kPer; i += 2) {
+      // e^-200 is 0 in fp32: what lies lower (-inf, a mask's value) adds the same nothing
+      const float2 d = make_float2(fmaxf(v[i] - ref, -200.f), fmaxf(v[i + 1] - ref, -200.f));
+      const float2 e = make_float2(ex2(d.x * 1.4426950408889634f), ex2(d.y * 1.4426950408889634f));
+      z.x += e.x;
+      z.y += e.y;
+      u = ffma2(d, e, u);
     }
-    if (k > 0) {
+    st.z += z.x + z.y;
+    st.u += u.x + u.y;
+    // (a NaN among them hides the others: then all of the tile is looked at)
+    if (k > 0 && __syncthreads_or(!(tm < least))) {
       Key key[kPer];
 #pragma unroll
-      for (int i = 0; i < kWords; ++i)
+      for (int i = 0; i < kWords; ++i) {
+        const int64_t at = t + tid + (int64_t)i * kThreads;
+        const int64_t e0 = at * kE - shift;
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
-          const int64_t w = t + tid + (int64_t)i * kThreads;
-          const int e = idx0[i] + j;
-          key[i * kE + j] = w < w1 && e >= 0 && e < vocab ? make_key(v[i * kE + j], (uint32_t)e) : 0;
+          const int64_t e = e0 + j;
+          key[i * kE + j] = at < w1 && e >= 0 && e < vocab ? make_key(v[i * kE + j], (uint32_t)e) : 0;
         }
+      }
       fold_top(sm, key, k);
+      const Key last = sm.best[sm.which][k - 1];
+      least = last == 0 ? -INFINITY : key_value(last);
+      if (!(least == least)) least = -INFINITY;  // a NaN is below everything
     }
   }
   st = warp_join(st);
