@@ -10,11 +10,13 @@
 //
 // The alternatives ride along.  A logit and its index form one 64-bit key
 // (value order first, then the lower index), so all keys differ and the
-// outcome does not depend on any order of arrival.  The CTA holds its best k
-// keys so far; after a row's first tile hardly a thread finds a larger one.  A
-// tile that does brings its candidates to shared memory, at most kBufThreads
-// threads' worth: where more threads hold one, a bound is found first, by
-// bisection over the threads' largest keys, that k to kBufThreads of them reach.
+// outcome does not depend on any order of arrival.  Each warp holds its best k
+// keys, lane i the i-th, and publishes a value that c = ceil(k / 8) of its
+// logits reach: the least of the eight warps' values is a floor that k logits
+// of the block reach, whenever it is read (the published values only rise).
+// Only what reaches the floor is offered to the lists, and a tile in which no
+// lane's maximum does costs one vote.  The lists meet in shared memory at the
+// end.
 #include <math.h>
 
 #include "launch.h"
@@ -25,20 +27,23 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;            // 16-byte words per thread and tile
-constexpr int kBufThreads = 64;     // threads whose candidates fit the buffer
 constexpr int kMaxK = SPARK_MAX_TOP;
+constexpr int kWarps = kThreads / 32;
 
 using Key = unsigned long long;
 
-__device__ __forceinline__ Key make_key(float x, uint32_t idx) {
-  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 and 0 are equal logits
-  const uint32_t o = x != x ? 0u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((Key)o << 32) | (0xFFFFFFFFu - idx);
+// the order of floats as that of integers: NaN lowest, -0 and 0 equal
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return x != x ? 0u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(Key k) {
-  const uint32_t o = (uint32_t)(k >> 32);
+__device__ __forceinline__ float value_of(uint32_t o) {
   return o == 0u ? __uint_as_float(0x7FC00000u) : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
+__device__ __forceinline__ Key make_key(float x, uint32_t idx) {
+  return ((Key)order_of(x) << 32) | (0xFFFFFFFFu - idx);
+}
+__device__ __forceinline__ float key_value(Key k) { return value_of((uint32_t)(k >> 32)); }
 __device__ __forceinline__ int32_t key_index(Key k) { return (int32_t)(0xFFFFFFFFu - (uint32_t)k); }
 
 struct Stat {
@@ -73,62 +78,78 @@ __device__ __forceinline__ Stat warp_join(Stat s) {
 }
 
 struct Smem {
-  Stat stat[kThreads / 32];
-  Key best[2][kMaxK];
-  Key buf[kBufThreads * 16 + kMaxK];
-  int count, which, last;
+  Stat stat[kWarps];
+  Key list[kWarps * kMaxK];  // the warps' keys at the end
+  Key best[kMaxK];
+  uint32_t reached[kWarps];  // c logits of the warp reach this (order_of)
+  int count;
+  int last;
 };
 
-// Fold the block's keys (N per thread, 0 for none) into the best k: into
-// sm.best[sm.which], in descending order.
-template <int N>
-__device__ __forceinline__ void fold_top(Smem& sm, const Key (&key)[N], int k) {
-  static_assert(N <= 16, "the buffer holds 16 keys a thread");
-  const int tid = threadIdx.x;
-  Key least = sm.best[sm.which][k - 1];  // 0 while there are fewer than k
-  Key mine = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) mine = key[i] > mine ? key[i] : mine;
-  const int have = __syncthreads_count(mine > least);
-  if (have == 0) return;
-  if (have > kBufThreads) {
-    // the highest bound found that at least k threads' largest keys reach
-    Key lo = least, hi = ~0ull;  // count(>= lo + 1) = have > kBufThreads; count(>= hi) < k
-    for (int it = 0; it < 64; ++it) {
-      const Key mid = lo + (hi - lo) / 2;
-      const int n = __syncthreads_count(mine > mid);
-      if (n >= k) {
-        lo = mid;
-        if (n <= kBufThreads) break;
-      } else {
-        hi = mid;
-      }
+constexpr uint32_t kLowest = 0x007FFFFFu;  // -inf
+
+// The c-th largest of the lanes' values (NaN: none).
+__device__ __forceinline__ uint32_t warp_kth(float mine, int c, int lane) {
+  uint32_t x = order_of(mine), top = 0;
+  for (int i = 0; i < c; ++i) {
+    top = __reduce_max_sync(0xffffffffu, x);
+    if (lane == __ffs(__ballot_sync(0xffffffffu, x == top)) - 1) x = 0;
+  }
+  return top;
+}
+
+__device__ __forceinline__ float floor_now(const Smem& sm, int lane) {
+  const uint32_t o = lane < kWarps ? *(const volatile uint32_t*)&sm.reached[lane] : 0xFFFFFFFFu;
+  const uint32_t least = __reduce_min_sync(0xffffffffu, o);
+  return value_of(least < kLowest ? kLowest : least);
+}
+
+// A warp's best k keys: lane i holds the i-th (0: none), every lane the k-th.
+struct WarpTop {
+  Key key, least;
+  __device__ __forceinline__ void reset() { key = least = 0; }
+  // one candidate per lane (0: none)
+  __device__ __forceinline__ void offer(Key cand, int k, int lane) {
+    unsigned m = __ballot_sync(0xffffffffu, cand > least);
+    while (m != 0) {
+      const int src = __ffs(m) - 1;
+      const Key c = __shfl_sync(0xffffffffu, cand, src);
+      const int pos = __popc(__ballot_sync(0xffffffffu, key > c));
+      const Key up = __shfl_up_sync(0xffffffffu, key, 1);
+      key = lane == pos ? c : lane > pos ? up : key;
+      least = __shfl_sync(0xffffffffu, key, k - 1);
+      m &= m - 1;
+      m &= __ballot_sync(0xffffffffu, cand > least);
     }
-    least = lo;
   }
-  if (tid == 0) sm.count = 0;
+};
+
+// Publish the c-th of a warp's list, if it has as many.
+__device__ __forceinline__ void publish(Smem& sm, const WarpTop& top, int c, int lane, int warp) {
+  if (lane == c - 1 && top.key != 0) *(volatile uint32_t*)&sm.reached[warp] = (uint32_t)(top.key >> 32);
+}
+
+// The best k of the warps' lists into sm.best, in descending order; every
+// thread of the block, the lists published, sm.count 0 (behind a barrier).
+// What reaches the floor is gathered; a key's rank is the number of larger ones.
+__device__ __forceinline__ void join_tops(Smem& sm, const WarpTop& top, int k) {
+  const int tid = threadIdx.x, lane = tid & 31;
   __syncthreads();
-  if (mine > least) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (key[i] > least) sm.buf[atomicAdd(&sm.count, 1)] = key[i];
-  }
-  const Key* old = sm.best[sm.which];
-  Key* out = sm.best[sm.which ^ 1];
+  const float floor = floor_now(sm, lane);
+  const bool in = lane < k && top.key != 0 && !(key_value(top.key) < floor);
+  const unsigned m = __ballot_sync(0xffffffffu, in);
+  int at = 0;
+  if (lane == 0) at = atomicAdd(&sm.count, __popc(m));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+  if (in) sm.list[at] = top.key;
   __syncthreads();
-  const int n0 = sm.count;
-  if (tid < k) sm.buf[n0 + tid] = old[tid];  // the best so far compete with them
-  __syncthreads();
-  const int n = n0 + k;
-  for (int i = tid; i < n; i += kThreads) {
-    const Key x = sm.buf[i];
+  const int n = sm.count;
+  if (tid < n) {
+    const Key x = sm.list[tid];
     int rank = 0;
-    // empty places (0) are equal: ordered by their place
-    for (int j = 0; j < n; ++j) rank += sm.buf[j] > x || (sm.buf[j] == x && j < i);
-    if (rank < k) out[rank] = x;
+    for (int j = 0; j < n; ++j) rank += sm.list[j] > x;
+    if (rank < k) sm.best[rank] = x;
   }
-  __syncthreads();
-  if (tid == 0) sm.which ^= 1;
   __syncthreads();
 }
 
@@ -164,7 +185,7 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 // CTA (row, part): part c of C covers the 16-byte words [W c / C, W (c+1) / C)
 // of the row's W aligned words (the first and last may belong to it in part).
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     k_score(const T* logits, int64_t ld, int vocab, const int32_t* targets, int k, int parts,
             float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs, uint32_t* err, uint32_t* tickets,
             score::Part* part) {
@@ -174,30 +195,40 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ Smem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / parts, c = blockIdx.x % parts;
-  if (tid < kMaxK) sm.best[0][tid] = 0;
   if (tid == 0) {
-    sm.which = 0;
     sm.last = 0;
+    sm.count = 0;
   }
+  const int share = (k + kWarps - 1) / kWarps;  // of the k, a warp's
+  WarpTop top;
+  top.reset();
   pdl_wait();
   pdl_trigger();
   const T* x = logits + row * ld;
   const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));  // elements before the row in its first word
   const T* base = x - shift;
-  const int64_t words = ((int64_t)shift + vocab + kE - 1) / kE;
-  const int64_t w0 = words * c / parts, w1 = words * (c + 1) / parts;
+  const int words = (shift + vocab + kE - 1) / kE;
+  const int w0 = (int)((int64_t)words * c / parts), w1 = (int)((int64_t)words * (c + 1) / parts);
+  constexpr int kTileWords = kThreads * kWords;
   Stat st = {-INFINITY, 0.f, 0.f, 0};
-  __syncthreads();
-  float least = -INFINITY;  // value of the k-th best so far: nothing below it is an alternative
+  float least = -INFINITY;  // nothing below it is an alternative
+  // a tile wholly inside the row and the part
+  auto inner = [&](int t) { return t + kTileWords <= w1 && t * kE >= shift && (t + kTileWords) * kE <= shift + vocab; };
   // the words of a tile; an edge of the row, or what lies behind the part, as
   // the bits of -inf
-  auto fetch = [&](int64_t t, uint4 (&w)[kWords]) {
+  auto fetch = [&](int t, uint4 (&w)[kWords]) {
+    if (inner(t)) {
+      const T* src = base + (int64_t)(t + tid) * kE;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = load_word(src + i * kThreads * kE);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int64_t at = t + tid + (int64_t)i * kThreads;
-      const int64_t e0 = at * kE - shift;  // index of the word's first element
+      const int at = t + tid + i * kThreads;
+      const int e0 = at * kE - shift;  // index of the word's first element
       if (at < w1 && e0 >= 0 && e0 + kE <= vocab) {
-        w[i] = load_word(base + at * kE);
+        w[i] = load_word(base + (int64_t)at * kE);
       } else {
         constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
         uint32_t b[4] = {kNone, kNone, kNone, kNone};
@@ -218,7 +249,7 @@ __global__ void __launch_bounds__(kThreads)
   };
   uint4 word[kWords];
   if (w0 < w1) fetch(w0, word);
-  for (int64_t t = w0; t < w1; t += kThreads * kWords) {
+  for (int t = w0; t < w1; t += kTileWords) {
     float v[kPer];
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
@@ -228,10 +259,10 @@ __global__ void __launch_bounds__(kThreads)
       for (int j = 0; j < kE; ++j) v[i * kE + j] = y[j];
     }
     // the next tile's loads run while this one is folded in
-    if (t + kThreads * kWords < w1) fetch(t + kThreads * kWords, word);
-    float mx[4] = {v[0], v[1], v[2], v[3]};
+    if (t + kTileWords < w1) fetch(t + kTileWords, word);
+    float mx[4];
 #pragma unroll
-    for (int i = 4; i < kPer; ++i) mx[i & 3] = max_nan(mx[i & 3], v[i]);
+    for (int i = 0; i < 4; ++i) mx[i] = max_nan(max_nan(v[4 * i], v[4 * i + 1]), max_nan(v[4 * i + 2], v[4 * i + 3]));
     const float tm = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
     st.bad |= !(tm < INFINITY);
     if (tm > st.m) {
@@ -245,33 +276,46 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) {
       // e^-200 is 0 in fp32: what lies lower (-inf, a mask's value) adds the same nothing
-      const float2 d = make_float2(fmaxf(v[i] - ref, -200.f), fmaxf(v[i + 1] - ref, -200.f));
-      const float2 e = make_float2(ex2(d.x * 1.4426950408889634f), ex2(d.y * 1.4426950408889634f));
-      z.x += e.x;
-      z.y += e.y;
+      float2 d = ffma2(make_float2(v[i], v[i + 1]), make_float2(1.f, 1.f), make_float2(-ref, -ref));
+      d = make_float2(fmaxf(d.x, -200.f), fmaxf(d.y, -200.f));
+      const float2 x2 = ffma2(d, make_float2(1.4426950408889634f, 1.4426950408889634f), make_float2(0.f, 0.f));
+      const float2 e = make_float2(ex2(x2.x), ex2(x2.y));
+      z = ffma2(e, make_float2(1.f, 1.f), z);
       u = ffma2(d, e, u);
     }
     st.z += z.x + z.y;
     st.u += u.x + u.y;
-    // (a NaN among them hides the others: then all of the tile is looked at)
-    if (k > 0 && __syncthreads_or(!(tm < least))) {
-      Key key[kPer];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const int64_t at = t + tid + (int64_t)i * kThreads;
-        const int64_t e0 = at * kE - shift;
-#pragma unroll
-        for (int j = 0; j < kE; ++j) {
-          const int64_t e = e0 + j;
-          key[i * kE + j] = at < w1 && e >= 0 && e < vocab ? make_key(v[i * kE + j], (uint32_t)e) : 0;
-        }
+    if (k > 0) {
+      if (t == w0) {
+        // (a NaN hides the thread's other logits: the floor is only lower)
+        const uint32_t o = warp_kth(tm, share, lane);
+        if (lane == 0) sm.reached[warp] = o;
+        __syncthreads();
       }
-      fold_top(sm, key, k);
-      const Key last = sm.best[sm.which][k - 1];
-      least = last == 0 ? -INFINITY : key_value(last);
-      if (!(least == least)) least = -INFINITY;  // a NaN is below everything
+      least = fmaxf(least, floor_now(sm, lane));
+    }
+    // (a NaN hides the others: then all of the tile is looked at)
+    if (k > 0 && __any_sync(0xffffffffu, !(tm < least))) {
+      // the lane's candidates, one a round
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) mask |= v[i] < least ? 0u : 1u << i;
+#pragma unroll 1
+      while (__any_sync(0xffffffffu, mask != 0)) {
+        const int bit = mask != 0 ? __ffs(mask) - 1 : 0;
+        float y = v[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) y = bit == i ? v[i] : y;
+        const int at = t + tid + bit / kE * kThreads, e = at * kE - shift + bit % kE;
+        top.offer(mask != 0 && at < w1 && e >= 0 && e < vocab ? make_key(y, (uint32_t)e) : 0, k, lane);
+        mask &= mask - 1;
+      }
+      // the list's last, once it is full (a NaN is below everything)
+      if (top.least != 0) least = fmaxf(least, key_value(top.least));
+      publish(sm, top, share, lane, warp);
     }
   }
+  if (k > 0) join_tops(sm, top, k);
   st = warp_join(st);
   if (lane == 0) sm.stat[warp] = st;
   __syncthreads();
@@ -285,7 +329,7 @@ __global__ void __launch_bounds__(kThreads)
       mine->u = st.u;
       mine->bad = st.bad;
     }
-    if (tid < k) mine->key[tid] = sm.best[sm.which][tid];
+    if (tid < k) mine->key[tid] = sm.best[tid];
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -296,26 +340,49 @@ __global__ void __launch_bounds__(kThreads)
     if (!sm.last) return;
     __threadfence();
     const score::Part* all = part + (int64_t)row * parts;
-    st = Stat{-INFINITY, 0.f, 0.f, 0};
-    for (int q = 0; q < parts; ++q) {
-      Stat s;
-      s.m = __ldcg(&all[q].m);
-      s.z = __ldcg(&all[q].z);
-      s.u = __ldcg(&all[q].u);
-      s.bad = __ldcg(&all[q].bad);
-      st = join(st, s);
+    // (every warp for itself: two parts a lane, then the tree over the lanes)
+    static_assert(score::kMaxParts <= 64, "two parts a lane");
+    Stat s2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = lane + 32 * i;
+      s2[i] = Stat{-INFINITY, 0.f, 0.f, 0};
+      if (q < parts) {
+        const int4 w = __ldcg(reinterpret_cast<const int4*>(&all[q]));
+        s2[i] = Stat{__int_as_float(w.x), __int_as_float(w.y), __int_as_float(w.z), w.w};
+      }
     }
+    st = warp_join(join(s2[0], s2[1]));
     if (k > 0) {
-      if (tid < kMaxK) sm.best[sm.which][tid] = 0;
-      __syncthreads();
+      top.reset();
       constexpr int kN = score::kMaxParts * kMaxK / kThreads;
       Key key[kN];
+      Key mine = 0;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        const int e = tid + i * kThreads;
-        key[i] = e < parts * k ? __ldcg(&all[e / k].key[e % k]) : 0;
+        const int e = tid + i * kThreads, q = e / kMaxK;  // (kMaxK keys of room a part, k of them in use)
+        key[i] = q < parts && e % kMaxK < k ? __ldcg(&all[q].key[e % kMaxK]) : 0;
+        mine = key[i] > mine ? key[i] : mine;
       }
-      fold_top(sm, key, k);
+      const uint32_t o = warp_kth(mine != 0 ? key_value(mine) : -INFINITY, share, lane);
+      if (lane == 0) sm.reached[warp] = o;
+      if (tid == 0) sm.count = 0;
+      __syncthreads();
+      const float floor = floor_now(sm, lane);
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) mask |= key[i] == 0 || key_value(key[i]) < floor ? 0u : 1u << i;
+#pragma unroll 1
+      while (__any_sync(0xffffffffu, mask != 0)) {
+        const int bit = mask != 0 ? __ffs(mask) - 1 : 0;
+        Key y = key[0];
+#pragma unroll
+        for (int i = 1; i < kN; ++i) y = bit == i ? key[i] : y;
+        top.offer(mask != 0 ? y : 0, k, lane);
+        mask &= mask - 1;
+      }
+      publish(sm, top, share, lane, warp);
+      join_tops(sm, top, k);
     }
   }
   const float lz = logf(st.z);
@@ -333,7 +400,7 @@ __global__ void __launch_bounds__(kThreads)
     entropy[row] = none ? nan : lz - st.u / st.z;
   }
   if (tid < k) {
-    const Key key = sm.best[sm.which][tid];
+    const Key key = sm.best[tid];
     top_ids[(int64_t)row * k + tid] = key_index(key);
     top_logprobs[(int64_t)row * k + tid] = none ? nan : key_value(key) - st.m - lz;
   }

@@ -14,7 +14,7 @@ constexpr int kMaxSplit = 2048;     // (row, part) pairs of a split call at most
 constexpr int kPartElems = 4096;    // elements of a part at least: one tile
 
 // what one part of a row leaves for the join
-struct Part {
+struct alignas(16) Part {
   float m, z, u;
   int bad;
   unsigned long long key[SPARK_MAX_TOP];
@@ -24,10 +24,10 @@ constexpr size_t kTickets = 256;    // uint32 [kMaxSplit], zero between launches
 constexpr size_t kParts = kTickets + 4 * kMaxSplit;
 constexpr size_t kTotal = kParts + sizeof(Part) * kMaxSplit;
 
-// Parts per row: enough CTAs for the GPU (about four an SM) where the rows
+// Parts per row: enough CTAs for the GPU (about two an SM) where the rows
 // alone are too few.
 inline int parts_for(int n_rows, int vocab, int sms) {
-  int64_t c = (4 * (int64_t)sms + n_rows - 1) / n_rows;
+  int64_t c = (2 * (int64_t)sms + n_rows - 1) / n_rows;
   const int64_t most = vocab / kPartElems;
   if (c > most) c = most;
   if (c > kMaxParts) c = kMaxParts;
