@@ -136,8 +136,12 @@ SPARK_HD int32_t partial_slot(int32_t c, int64_t begin, int64_t total, int32_t G
 }
 
 // Where position `pos` lives: the table's column and the row of the page.
-SPARK_HD int32_t page_col(int32_t pos, int32_t page_size) { return pos / page_size; }
-SPARK_HD int32_t page_row(int32_t pos, int32_t page_size) { return pos % page_size; }
+// The column by a product: with n = pos / 16 < 2^26, d = page_size / 16 <= 64
+// and m = floor(2^32 / d) + 1 the error n (m d - 2^32) / (2^32 d) of n m / 2^32
+// is below n / 2^32 < 1 / d, so floor(n m / 2^32) = floor(n / d).
+SPARK_HD uint64_t page_mul(int32_t page_size) { return ((uint64_t)1 << 32) / (uint64_t)(page_size / 16) + 1; }
+SPARK_HD int32_t page_col(int32_t pos, uint64_t mul) { return (int32_t)(((uint64_t)(pos >> 4) * mul) >> 32); }
+SPARK_HD int32_t page_row(int32_t pos, int32_t col, int32_t page_size) { return pos - col * page_size; }
 
 }  // namespace paged
 }  // namespace spark

@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kTokThreads, MINB)
         const int pos = (cur.g.tile0 + (int)(u - cur.begin) + lane) * kTile;
         int z = 0;
         if (lane < n)
-          z = paged::page_of(p, paged::page_entry(p, cur.s, paged::page_col(pos, p.page_size))) * p.page_size +
-              paged::page_row(pos, p.page_size);
+          z = paged::page_of(p, paged::page_entry(p, cur.s, paged::page_col(p, pos))) * p.page_size +
+              paged::page_row(p, pos);
         for (int i = 0; i < n; ++i, ++k) {
           const int zi = __shfl_sync(0xffffffffu, z, i);
           if (lane == 0) {
@@ -372,9 +372,9 @@ __global__ void __launch_bounds__(kAppendThreads)
       if (s.bad) atomicOr(p.err, kErrIndex);
       if (t >= s.q0 && t < s.q0 + s.n) {  // else: behind the last sequence, or a sequence that makes no sense
         const int pos = s.p0 + (t - s.q0);
-        const int pg = paged::page_entry(p, lo, paged::page_col(pos, p.page_size));
+        const int pg = paged::page_entry(p, lo, paged::page_col(p, pos));
         if (pg >= 0 && pg < p.n_pages)
-          at = ((int64_t)pg * p.page_size + paged::page_row(pos, p.page_size)) * row4;
+          at = ((int64_t)pg * p.page_size + paged::page_row(p, pos)) * row4;
         else
           atomicOr(p.err, kErrIndex);
       }
@@ -431,6 +431,7 @@ cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, con
 
 cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                    cudaStream_t st) {
+  if (cdtype == SPARK_BF16 && p.max_q > paged::kChunkTokens) return launch_paged_pair(p, qdtype, k, v, st);
   if (cdtype == SPARK_BF16 && p.max_q > 1) return launch_paged_chunk(p, qdtype, k, v, st);
   return launch_paged_token(p, qdtype, cdtype, k, v, st);
 }

@@ -78,6 +78,7 @@ inline paged::Args paged_args(const spark_geom* g, const spark_page_pool* pool, 
   p.max_q = b->max_q_len;
   p.n_pages = (int32_t)pool->n_pages;
   p.page_size = pool->page_size;
+  p.page_mul = paged::page_mul(pool->page_size);
   p.n_kv = g->n_kv;
   p.window = layer_class == SPARK_FULL ? 0 : g->window;
   p.scale_log2 = g->scale * 1.4426950408889634f;

@@ -27,33 +27,12 @@
 // Work is the flat list of paged.h (128-position tiles), every CTA an equal
 // share: a group cut by a share's border leaves fp32 partial states, joined
 // in CTA order by k_paged_join.
-#include <math.h>
-
-#include <type_traits>
-
-#include "launch.h"
-#include "paged_launch.h"
-#include "paged_parts.cuh"
-#include "tmem.cuh"
+#include "paged_chunk_parts.cuh"
 
 namespace spark {
 namespace {
 
-using paged::Args;
-using paged::Cursor;
-using paged::Shape;
-
-constexpr int kRows = 128;                      // rows of a group: 32 tokens x 4 heads
-constexpr int kPos = 128;                       // positions of a tile
-constexpr int kThreads = 192;
-constexpr int kSoft = 128;                      // softmax threads, one row each
-constexpr uint32_t kLineBytes = kPos * 128;     // 64 dims of 128 rows or positions
-constexpr uint32_t kSlot = 2 * kLineBytes;      // 128 dims
-constexpr uint32_t kQBytes = 4 * kLineBytes;
-constexpr uint32_t kCols = 512;
-constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O starts at 0
-constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
-constexpr int kMinTiles = 2;                    // tiles per CTA at least
+using namespace chunk;
 
 static_assert(kRows == kGroup * paged::kChunkTokens, "a row per query head of a token");
 
@@ -68,140 +47,6 @@ struct ChunkSmem {
   static constexpr uint32_t kAlloc = kBytes + 1024;  // slack to align the base (128-byte swizzle)
 };
 static_assert(ChunkSmem<true>::kAlloc <= 232448 && ChunkSmem<false>::kAlloc <= 232448, "227 KB per CTA");
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return ffma2(a, make_float2(1.f, 1.f), b); }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// eight elements of a query row, the sign of a negative scale folded in, as
-// bf16 (and the remainders, for fp32 queries)
-__device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = pack2(x[2 * i], x[2 * i + 1]);
-    const float2 f = bf16x2_to_f32x2(h[i]);
-    l[i] = pack2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-// The group's queries into shared memory: 64-dim lines of 128 rows, 16-byte
-// chunk c of row r at c ^ (r % 8) (the 128-byte swizzle).  Rows behind the
-// last token are zero.
-template <typename QT>
-__device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, bool flip, int tid) {
-  const QT* q = static_cast<const QT*>(p.q) + (int64_t)cur.j * kGroup * kHeadDim;
-  const int64_t row0 = cur.seq.q0 + cur.g.tok;
-  constexpr int kBatch = 8;  // rows in flight per warp
-  const int ch = tid & 31;
-  for (int r0 = tid >> 5; r0 < kRows; r0 += 4 * kBatch) {
-    uint4 v[kBatch][sizeof(QT) / 2];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + 4 * i;
-      const bool in = (r >> 2) < cur.g.n_tok;
-      const uint4* src = reinterpret_cast<const uint4*>(q + (row0 + (r >> 2)) * p.q_ld + (r & 3) * kHeadDim + 8 * ch);
-#pragma unroll
-      for (int k = 0; k < (int)sizeof(QT) / 2; ++k) v[i][k] = in ? __ldcg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + 4 * i;
-      const uint32_t at = (uint32_t)(ch >> 3) * kLineBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-      if constexpr (std::is_same<QT, float>::value) {
-        float x[8];
-        const float s = flip ? -1.f : 1.f;
-        const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = s * __uint_as_float(w[k]);
-        uint4 hi, lo;
-        split8(x, hi, lo);
-        *reinterpret_cast<uint4*>(q_s + at) = hi;
-        *reinterpret_cast<uint4*>(q_s + kQBytes + at) = lo;
-      } else {
-        uint4 w = v[i][0];
-        const uint32_t f = flip ? 0x80008000u : 0u;
-        w.x ^= f; w.y ^= f; w.z ^= f; w.w ^= f;
-        *reinterpret_cast<uint4*>(q_s + at) = w;
-      }
-    }
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
-}
-
-// The columns x0 .. x1 of a tile that a row sees, as one bit per column of
-// the 32 from `first`.
-__device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
-  const int a = x0 - first, b = x1 + 1 - first;  // bits [a, b)
-  const uint32_t below_b = b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1u;
-  const uint32_t below_a = a >= 32 ? 0xffffffffu : a <= 0 ? 0u : (1u << a) - 1u;
-  return below_b & ~below_a;
-}
-
-// 32 scores of a row become P = e^(scale s - ref) in bf16 (SPLIT: and the
-// remainders) over their own columns at `ts`.
-template <bool EDGE, bool SPLIT>
-__device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], float scale, float ref, uint32_t seen,
-                                      float2 (&sum)[2]) {
-  uint32_t hi[16], lo[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 t = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                           make_float2(scale, scale), make_float2(-ref, -ref));
-    float2 e = make_float2(ex2(t.x), ex2(t.y));
-    if (EDGE) {
-      e.x = ((seen >> (2 * i)) & 1u) ? e.x : 0.f;
-      e.y = ((seen >> (2 * i + 1)) & 1u) ? e.y : 0.f;
-    }
-    sum[i & 1] = fadd2(sum[i & 1], e);
-    hi[i] = pack2(e.x, e.y);
-    if (SPLIT) {
-      const float2 f = bf16x2_to_f32x2(hi[i]);
-      lo[i] = pack2(e.x - f.x, e.y - f.y);
-    }
-  }
-  tc::st16(ts, hi);
-  if (SPLIT) tc::st16(ts + 16, lo);
-}
-
-template <bool EDGE>
-__device__ __forceinline__ void max32(const uint32_t (&s)[32], uint32_t seen, float (&mx)[4]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x = !EDGE || ((seen >> (i + k)) & 1u) ? __uint_as_float(s[i + k]) : -INFINITY;
-      const float y = !EDGE || ((seen >> (i + k + 4)) & 1u) ? __uint_as_float(s[i + k + 4]) : -INFINITY;
-      mx[k] = fmaxf(mx[k], fmaxf(x, y));
-    }
-}
-
-// 32 output dims of a row
-// 32 output dims of a row
-__device__ __forceinline__ void store32(float* dst, const uint32_t (&o)[32], float inv) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 4)
-    reinterpret_cast<float4*>(dst)[i / 4] = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                                        __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-}
-__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[32], float inv) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = pack2(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
-    reinterpret_cast<uint4*>(dst)[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
 
 template <typename QT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -234,10 +79,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], kSoft);
+      mbar_init(&p_full[b], kSoft / 32);
       mbar_init(&pv_done[b], 1);
     }
-    mbar_init(q_full, kSoft);
+    mbar_init(q_full, kSoft / 32);
     mbar_init(drained, 1);
     flags[0] = 0;
     fence_mbar_init();
@@ -304,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pos, b0, b1;
         boxes(u, pos, b0, b1);
         const int b = lane % per;
-        return b >= b0 && b < b1 ? paged::page_entry(p, cur.s, paged::page_col(pos + b * box, p.page_size)) : 0;
+        return b >= b0 && b < b1 ? paged::page_entry(p, cur.s, paged::page_col(p, pos + b * box)) : 0;
       };
       int z_v = 0, v0 = 0, v1 = 0;  // the tile before
       int ahead = entry(t0);
@@ -313,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < t1) {
           int pos;
           boxes(u, pos, b0, b1);
-          z = paged::page_of(p, ahead) * p.page_size + paged::page_row(pos + (lane % per) * box, p.page_size);
+          z = paged::page_of(p, ahead) * p.page_size + paged::page_row(p, pos + (lane % per) * box);
           if (u + 1 < t1) ahead = entry(u + 1);
           slot(&tm_k, 0, z, b0, b1);
           slot(&tm_k, 1, z, b0, b1);
@@ -436,164 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---- softmax: one row per thread
-    const int quad = warp & 3, st = tid - 64;
-    const int row = quad * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const bool flip = p.scale_log2 < 0.f;
-    const float scale = fabsf(p.scale_log2);
-    QT* out = static_cast<QT*>(p.a);
-    uint32_t tile = 0;
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, flags, kWaitLimitNs));
-      tc::fence_after();
-      return ok;
-    };
-    load_queries<QT>(base, p, cur, flip, st);
-    mbar_arrive(q_full);
-    for (;;) {
-      const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
-      const paged::Group g = cur.g;
-      const int tok = row >> 2;
-      // positions the row sees; rows behind the last token take the last one's
-      const int pos_hi = cur.seq.p0 + g.tok + (tok < g.n_tok ? tok : g.n_tok - 1);
-      const int pos_lo = p.window > 0 && pos_hi + 1 > p.window ? pos_hi + 1 - p.window : 0;
-      const bool live = 8 * quad < g.n_tok;  // the warp has a row
-      const int w_hi = __shfl_sync(0xffffffffu, pos_hi, 0), w_lo = __shfl_sync(0xffffffffu, pos_lo, 31);
-      float m = -INFINITY, l = 0.f;
-      for (int64_t u = t0; u < t1; ++u, ++tile) {
-        const uint32_t buf = tile & 1;
-        if (!wait(&s_full[buf], (tile >> 1) & 1)) break;
-        if (tile >= 2 && !wait(&pv_done[buf], ((tile - 2) >> 1) & 1)) break;  // long done: S(i) came after it
-        if (live) {
-          const int pos = (g.tile0 + (int)(u - cur.begin)) * kPos;
-          const uint32_t ts = tmem + lanes + kColS + buf * kPos;
-          const bool whole = pos + kPos - 1 <= w_hi && pos >= w_lo;  // every row of the warp sees every position
-          const int x0 = pos_lo - pos, x1 = pos_hi - pos;            // columns the row sees
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          // a whole tile's scores stay in registers; a masked one (a group's
-          // last, or its first behind a window) is read twice by a short loop
-          uint32_t s0[32], s1[32], s2[32], s3[32];
-          if (whole) {
-            tc::ld32(ts, s0);
-            tc::ld32(ts + 32, s1);
-            tc::ld32(ts + 64, s2);
-            tc::ld32(ts + 96, s3);
-            tc::wait_ld(s0);
-            tc::wait_ld(s1);
-            tc::wait_ld(s2);
-            tc::wait_ld(s3);
-            max32<false>(s0, 0, mx);
-            max32<false>(s1, 0, mx);
-            max32<false>(s2, 0, mx);
-            max32<false>(s3, 0, mx);
-          } else {
-#pragma unroll 1
-            for (int ch = 0; ch < kPos; ch += 32) {
-              tc::ld32(ts + ch, s0);
-              tc::wait_ld(s0);
-              max32<true>(s0, seen32(x0, x1, ch), mx);
-            }
-          }
-          float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          mt = mt == -INFINITY ? mt : mt * scale;
-          if (u == t0) {
-            m = mt;
-          } else if (__any_sync(0xffffffffu, mt > m + kRaise)) {
-            const float mn = fmaxf(m, mt);
-            const float corr = m == -INFINITY ? 0.f : ex2(m - mn);
-            m = mn;
-            l *= corr;
-            // every earlier product is in O before it is rescaled
-            if (!wait(&pv_done[buf ^ 1], ((tile - 1) >> 1) & 1)) break;
-#pragma unroll 1
-            for (int d = 0; d < kHeadDim; d += 32) {
-              uint32_t o[32];
-              tc::ld32(tmem + lanes + d, o);
-              tc::wait_ld(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-              tc::st32(tmem + lanes + d, o);
-            }
-          }
-          const float ref = m == -INFINITY ? 0.f : m;
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          if (whole) {
-            exp32<false, kSplit>(ts, s0, scale, ref, 0, sum);
-            exp32<false, kSplit>(ts + 32, s1, scale, ref, 0, sum);
-            exp32<false, kSplit>(ts + 64, s2, scale, ref, 0, sum);
-            exp32<false, kSplit>(ts + 96, s3, scale, ref, 0, sum);
-          } else {
-#pragma unroll 1
-            for (int ch = 0; ch < kPos; ch += 32) {
-              tc::ld32(ts + ch, s0);
-              tc::wait_ld(s0);
-              exp32<true, kSplit>(ts + ch, s0, scale, ref, seen32(x0, x1, ch), sum);
-            }
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          tc::wait_st();
-        }
-        tc::fence_before();
-        mbar_arrive(&p_full[buf]);
-      }
-      if (!ok) break;
-      // Q is free (the last S is done): the next group's queries load while
-      // this one's last product runs
-      Cursor nxt = cur;
-      const bool more = cur.end < u1;
-      if (more) {
-        nxt.next(p, sh);
-        load_queries<QT>(base, p, nxt, flip, st);
-        mbar_arrive(q_full);
-      }
-      if (!wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) break;
-      const bool split = cur.begin < u0 || cur.end > u1;
-      if (live) {
-        const int64_t r = cur.seq.q0 + g.tok + tok;
-        float* part = p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) * paged::kChunkPart;
-        QT* dst = out + ((r * p.n_kv + cur.j) * kGroup + (row & 3)) * kHeadDim;
-        const float inv = 1.0f / l;
-#pragma unroll 1
-        for (int d = 0; d < kHeadDim; d += 32) {
-          uint32_t o[32];
-          tc::ld32(tmem + lanes + d, o);
-          tc::wait_ld(o);
-          if (tok < g.n_tok) {
-            if (split)
-              store32(part + row * kHeadDim + d, o, 1.0f);
-            else
-              store32(dst + d, o, inv);
-          }
-        }
-        if (split) {
-          part[kRows * kHeadDim + row] = m;
-          part[kRows * kHeadDim + kRows + row] = l;
-        }
-      }
-      tc::fence_before();  // O is read before the next group's first product (its P arrives after this)
-      if (!more) break;
-      cur = nxt;
-    }
-    if (!ok && lane == 0) {
-      if (!flags[0]) atomicOr(p.err, kErrWaitTimeout);
-      flags[0] = 1;
-    }
-    if (st == 0) {
-      // the group that begins in this share and goes on behind it, if any
-      paged::Join j = {};
-      if (ok && cur.end > u1 && cur.begin >= u0) {
-        j.row0 = cur.seq.q0 + cur.g.tok;
-        j.n_rows = 4 * cur.g.n_tok;
-        j.head = cur.j;
-        j.last = paged::cta_at(cur.end - 1, total, G);
-        j.begin = cur.begin;
-        j.total = total;
-        j.G = G;
-      }
-      p.joins[c] = j;
-    }
+    softmax_warps<QT, 1>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, s_full, pv_done, flags, warp, tid - 64,
+                         [&] { mbar_arrive(q_full); }, [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
   }
   tc::fence_before();
   __syncthreads();
@@ -601,61 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     tc::dealloc(tmem, kCols);
   }
-}
-
-// Join the partial states of the groups that a share's border cut: block
-// (share c, 8 rows of the group that begins in it and goes on), one row per
-// warp, eight dims per lane, the parts in CTA order.
-constexpr int kJoinRows = 8;
-
-template <typename QT>
-__global__ void __launch_bounds__(32 * kJoinRows) k_paged_join(const __grid_constant__ Args p) {
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinRows + warp;
-  if (row >= __ldcg(&p.joins[c].n_rows)) return;
-  const int last = __ldcg(&p.joins[c].last), G = __ldcg(&p.joins[c].G);
-  const int64_t begin = __ldcg(&p.joins[c].begin), total = __ldcg(&p.joins[c].total);
-  float M = -INFINITY, L = 0.f, O[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) O[i] = 0.f;
-  for (int q = c; q <= last; ++q) {
-    const float* part = p.part + (int64_t)paged::partial_slot(q, begin, total, G) * paged::kChunkPart;
-    const float m = __ldcg(part + kRows * kHeadDim + row), l = __ldcg(part + kRows * kHeadDim + kRows + row);
-    const float4* src = reinterpret_cast<const float4*>(part + row * kHeadDim + 8 * lane);
-    const float4 x = __ldcg(src), y = __ldcg(src + 1);
-    const float mn = fmaxf(M, m);
-    const float a = M == -INFINITY ? 0.f : exp2f(M - mn), b = m == -INFINITY ? 0.f : exp2f(m - mn);
-    M = mn;
-    L = L * a + l * b;
-    O[0] = O[0] * a + x.x * b; O[1] = O[1] * a + x.y * b; O[2] = O[2] * a + x.z * b; O[3] = O[3] * a + x.w * b;
-    O[4] = O[4] * a + y.x * b; O[5] = O[5] * a + y.y * b; O[6] = O[6] * a + y.z * b; O[7] = O[7] * a + y.w * b;
-  }
-  const float inv = 1.0f / L;
-  const int64_t r = __ldcg(&p.joins[c].row0) + (row >> 2);
-  QT* dst = static_cast<QT*>(p.a) + ((r * p.n_kv + __ldcg(&p.joins[c].head)) * kGroup + (row & 3)) * kHeadDim + 8 * lane;
-  if constexpr (std::is_same<QT, float>::value) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(O[0] * inv, O[1] * inv, O[2] * inv, O[3] * inv);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(O[4] * inv, O[5] * inv, O[6] * inv, O[7] * inv);
-  } else {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(O[0] * inv, O[1] * inv), pack2(O[2] * inv, O[3] * inv),
-                                                pack2(O[4] * inv, O[5] * inv), pack2(O[6] * inv, O[7] * inv));
-  }
-}
-
-// A pool [rows][n_kv][256] bf16 as the chunk kernel loads it: boxes of one
-// 128-byte line of `box` rows of one KV head.
-bool make_chunk_map(CUtensorMap* map, const void* base, int n_kv, int64_t rows, int box) {
-  EncodeTiledFn enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[4] = {64, (cuuint64_t)rows, 4, (cuuint64_t)n_kv};
-  const cuuint64_t strides[3] = {(cuuint64_t)n_kv * kHeadDim * 2, 128, kHeadDim * 2};
-  const cuuint32_t shape[4] = {64, (cuuint32_t)box, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, shape, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename QT>
@@ -674,7 +308,7 @@ cudaError_t launch_chunk(const Args& p, const void* k, const void* v, cudaStream
   if (grid > paged::kMaxChunkCtas) grid = paged::kMaxChunkCtas;
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), S::kAlloc, st, mk, mv, p, box);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_join<QT>, dim3(grid, kRows / kJoinRows), dim3(32 * kJoinRows), 0, st, p);
+  return launch_pdl(k_paged_join<QT, 1>, dim3(grid, kRows / kJoinRows), dim3(32 * kJoinRows), 0, st, p);
 }
 
 }  // namespace

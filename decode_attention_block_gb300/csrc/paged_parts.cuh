@@ -36,6 +36,7 @@ struct Args {
   const int32_t* seq_len;
   int32_t n_seqs, max_pages, n_tokens, max_q;
   int32_t n_pages, page_size;
+  uint64_t page_mul;  // of page_size (paged.h)
   int32_t n_kv, window;  // window 0: the whole history
   const void* q;
   int64_t q_ld;
@@ -139,6 +140,11 @@ struct Cursor {
     set_group(sh, end);
   }
 };
+
+__device__ __forceinline__ int page_col(const Args& p, int pos) { return page_col(pos, p.page_mul); }
+__device__ __forceinline__ int page_row(const Args& p, int pos) {
+  return page_row(pos, page_col(p, pos), p.page_size);
+}
 
 // The table's entry for column `col` of sequence s ...
 __device__ __forceinline__ int page_entry(const Args& p, int s, int col) {

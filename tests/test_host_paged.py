@@ -107,8 +107,14 @@ int main() {
     }
     CHECK(share_begin(total, G, 0) == 0 && share_begin(total, G, G) == total, "shares");
   }
-  for (int ps : {16, 48, 1024})
-    for (int x = 0; x < 5000; ++x) CHECK(page_col(x, ps) * ps + page_row(x, ps) == x && page_row(x, ps) < ps, "page of %d", x);
+  for (int ps = 16; ps <= 1024; ps += 16) {
+    const uint64_t m = page_mul(ps);
+    for (int i = 0; i < 30000; ++i) {
+      const int x = i < 5000 ? i : i < 10000 ? (1 << 30) - 1 - (i - 5000) : (int)(rng() >> 2);
+      const int c = page_col(x, m), r = page_row(x, c, ps);
+      CHECK(c == x / ps && r == x % ps, "page of %d at %d", x, ps);
+    }
+  }
   std::printf("%d failures\n", fails);
   return fails != 0;
 }
