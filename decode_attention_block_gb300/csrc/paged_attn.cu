@@ -431,9 +431,21 @@ cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, con
 
 cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                    cudaStream_t st) {
-  if (cdtype == SPARK_BF16 && p.max_q > paged::kChunkTokens) return launch_paged_pair(p, qdtype, k, v, st);
-  if (cdtype == SPARK_BF16 && p.max_q > 1) return launch_paged_chunk(p, qdtype, k, v, st);
-  return launch_paged_token(p, qdtype, cdtype, k, v, st);
+  // fp32 pools, and single tokens, a token at a time
+  if (cdtype != SPARK_BF16 || p.max_q == 1) return launch_paged_token(p, qdtype, cdtype, k, v, st);
+  if (p.max_q <= paged::kChunkTokens) return launch_paged_chunk(p, qdtype, k, v, st);
+  // Longer chunks take pairs of CTAs; in a mixed batch the sequences of up to
+  // 32 new tokens go to the single-CTA kernel, where they do not leave half
+  // of a pair's rows empty (32 sequences, 4 of them with chunks of ~400
+  // tokens, fp32 queries: pairs alone 311 us, single CTAs alone 230 us).
+  if (p.n_seqs == 1) return launch_paged_pair(p, qdtype, k, v, st);
+  paged::Args a = p;
+  a.from = paged::kChunkTokens + 1;
+  const cudaError_t e = launch_paged_pair(a, qdtype, k, v, st);
+  if (e != cudaSuccess) return e;
+  a.from = 1;
+  a.to = paged::kChunkTokens;
+  return launch_paged_chunk(a, qdtype, k, v, st);
 }
 
 cudaError_t launch_paged_append(const paged::Args& p, int xdtype, int cdtype, const void* k, const void* v, int64_t ld,

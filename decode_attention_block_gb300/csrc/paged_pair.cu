@@ -50,14 +50,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// this shared-memory address in rank 0
+// this shared-memory address in rank 0, and an arrival there
 __device__ __forceinline__ uint32_t in_rank0(const void* p) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
 }
+// ... releasing what this thread wrote to memory,
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// ... or without: what the barrier is about lies in tensor memory, which
+// tcgen05's own fences order (a release over the cluster took 1000 to 1400
+// cycles of a 3400-cycle tile here)
+__device__ __forceinline__ void arrive_tmem_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // a wait, bounded like every other, for what the other CTA did
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -357,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     const uint32_t q_bar = in_rank0(q_full), p_bar = in_rank0(p_full);
     softmax_warps<QT, 2>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, s_full, pv_done, flags, warp, tid - 64,
-                         [&] { arrive_at(q_bar); }, [&](uint32_t buf) { arrive_at(p_bar + 8 * buf); });
+                         [&] { arrive_at(q_bar); }, [&](uint32_t buf) { arrive_tmem_at(p_bar + 8 * buf); });
   }
   tc::fence_before();
   __syncthreads();
