@@ -113,18 +113,24 @@ SPARK_HD int32_t group_at(const Seq& s, const Shape& sh, int64_t u) {
   return lo;
 }
 
+// a / b for 0 <= a, 0 < b, by 32-bit division where both fit (a 64-bit one is
+// some hundred instructions on the GPU)
+SPARK_HD int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // CTAs that share `total` units out of at most `most`, with at least `least`
 // units each
 SPARK_HD int32_t ctas_for(int64_t total, int32_t least, int32_t most) {
-  const int64_t g = total / least;
+  const int64_t g = quotient(total, least);
   return g < 1 ? 1 : g > most ? most : (int32_t)g;
 }
 
-SPARK_HD int64_t share_begin(int64_t total, int32_t G, int32_t c) { return total * c / G; }
+SPARK_HD int64_t share_begin(int64_t total, int32_t G, int32_t c) { return quotient(total * c, G); }
 
 // the CTA that holds unit u of `total`, for G CTAs
 SPARK_HD int32_t cta_at(int64_t u, int64_t total, int32_t G) {
-  const int64_t c = ((u + 1) * G - 1) / total;
+  const int64_t c = quotient((u + 1) * G - 1, total);
   return (int32_t)(c < G - 1 ? c : G - 1);
 }
 

@@ -42,9 +42,8 @@ struct TokSmem {
   static constexpr int kO = kL + kConsumers * 16;
   static constexpr int kBars = kO + kConsumers * 4 * kHeadDim * 4;
   static constexpr int kFlags = kBars + 2 * kStages * 8;
-  static constexpr int kSums = kFlags + 16;
-  static constexpr int kPrefix = kSums + 64;
-  static constexpr int kBytes = kPrefix + 8 * (SPARK_MAX_BATCH + 2);
+  static constexpr int kPrefix = kFlags + 16;
+  static constexpr int kBytes = kPrefix + 8 * (SPARK_MAX_BATCH + 2 + kTokThreads / 32);
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 (128B swizzle)
 };
 
@@ -199,15 +198,12 @@ __global__ void __launch_bounds__(kTokThreads, MINB)
   pdl_wait();
   pdl_trigger();
   const Shape sh{1, kTile, p.window};
-  paged::work_prefix<kTokThreads>(p, sh, prefix, reinterpret_cast<int64_t*>(base + S::kSums));
-  const int64_t total = prefix[p.n_seqs];
-  if (total == 0) return;
-  const int G = paged::ctas_for(total, kMinUnits, gridDim.x), c = blockIdx.x;
-  if (c >= G) return;
-  const int64_t u0 = paged::share_begin(total, G, c), u1 = paged::share_begin(total, G, c + 1);
-
-  Cursor cur;
-  cur.seek(p, sh, prefix, u0);
+  const int c = blockIdx.x;
+  paged::Share share;
+  if (!paged::find_share<kTokThreads>(p, sh, c, kMinUnits, gridDim.x, prefix, share)) return;
+  const int64_t total = share.total, u0 = share.u0, u1 = share.u1;
+  const int G = share.G;
+  Cursor cur = share.cur;
   if (warp == kConsumers) {
     // ---- producer
     uint32_t k = 0;

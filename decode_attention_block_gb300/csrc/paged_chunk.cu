@@ -95,17 +95,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Shape sh{paged::kChunkTokens, kPos, p.window};
   // the ring is not in use yet: room for the prefix sums
   int64_t* prefix = reinterpret_cast<int64_t*>(base + S::kRing);
-  paged::work_prefix<kThreads>(p, sh, prefix, prefix + SPARK_MAX_BATCH + 2);
-  const int64_t total = prefix[p.n_seqs];
   const int c = blockIdx.x;
-  const int G = total > 0 ? paged::ctas_for(total, kMinTiles, gridDim.x) : 0;
-  if (c >= G) {
+  paged::Share share;
+  if (!paged::find_share<kThreads>(p, sh, c, kMinTiles, gridDim.x, prefix, share)) {
     if (tid == 0) p.joins[c].n_rows = 0;
     return;
   }
-  const int64_t u0 = paged::share_begin(total, G, c), u1 = paged::share_begin(total, G, c + 1);
-  Cursor cur;
-  cur.seek(p, sh, prefix, u0);
+  const int64_t total = share.total, u0 = share.u0, u1 = share.u1;
+  const int G = share.G;
+  Cursor cur = share.cur;
   if (warp == 1) tc::alloc(tmem_slot, kCols);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the prefix sums make way for TMA's writes
   tc::fence_before();

@@ -44,8 +44,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// eight elements of a query row, the sign of a negative scale folded in, as
-// bf16 (and the remainders, for fp32 queries)
+// eight elements of a query row as bf16 and the remainders
 __device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
@@ -62,7 +61,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo
 // memory: 64-dim lines of 128 rows, 16-byte chunk c of row r at c ^ (r % 8)
 // (the 128-byte swizzle).  Rows behind the last token are zero.
 template <typename QT>
-__device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, int tok0, bool flip,
+__device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, int tok0, float sign,
                                              int tid) {
   const QT* q = static_cast<const QT*>(p.q) + (int64_t)cur.j * kGroup * kHeadDim;
   const int64_t row0 = cur.seq.q0 + cur.g.tok + tok0;
@@ -84,18 +83,20 @@ __device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, 
       const uint32_t at = (uint32_t)(ch >> 3) * kLineBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
       if constexpr (std::is_same<QT, float>::value) {
         float x[8];
-        const float s = flip ? -1.f : 1.f;
         const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = s * __uint_as_float(w[k]);
+        for (int k = 0; k < 8; ++k) x[k] = sign * __uint_as_float(w[k]);
         uint4 hi, lo;
         split8(x, hi, lo);
         *reinterpret_cast<uint4*>(q_s + at) = hi;
         *reinterpret_cast<uint4*>(q_s + kQBytes + at) = lo;
       } else {
         uint4 w = v[i][0];
-        const uint32_t f = flip ? 0x80008000u : 0u;
-        w.x ^= f; w.y ^= f; w.z ^= f; w.w ^= f;
+        if (sign < 0.f) {
+          w.x ^= 0x80008000u; w.y ^= 0x80008000u; w.z ^= 0x80008000u; w.w ^= 0x80008000u;
+        } else if (sign == 0.f) {
+          w = make_uint4(0u, 0u, 0u, 0u);
+        }
         *reinterpret_cast<uint4*>(q_s + at) = w;
       }
     }
@@ -114,19 +115,14 @@ __device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
 
 // 32 scores of a row become P = e^(scale s - ref) in bf16 (SPLIT: and the
 // remainders) over their own columns at `ts`.
-template <bool EDGE, bool SPLIT>
-__device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], float scale, float ref, uint32_t seen,
-                                      float2 (&sum)[2]) {
+template <bool SPLIT>
+__device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], float scale, float ref, float2 (&sum)[2]) {
   uint32_t hi[16], lo[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float2 t = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
                            make_float2(scale, scale), make_float2(-ref, -ref));
-    float2 e = make_float2(ex2(t.x), ex2(t.y));
-    if (EDGE) {
-      e.x = ((seen >> (2 * i)) & 1u) ? e.x : 0.f;
-      e.y = ((seen >> (2 * i + 1)) & 1u) ? e.y : 0.f;
-    }
+    const float2 e = make_float2(ex2(t.x), ex2(t.y));
     sum[i & 1] = fadd2(sum[i & 1], e);
     hi[i] = pack2(e.x, e.y);
     if (SPLIT) {
@@ -138,16 +134,19 @@ __device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], floa
   if (SPLIT) tc::st16(ts + 16, lo);
 }
 
-template <bool EDGE>
-__device__ __forceinline__ void max32(const uint32_t (&s)[32], uint32_t seen, float (&mx)[4]) {
+// scores a row does not see become -inf (whatever they are: the rows of K
+// behind a sequence's end may hold anything)
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t seen) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[i] = ((seen >> i) & 1u) ? s[i] : 0xFF800000u;
+}
+
+__device__ __forceinline__ void max32(const uint32_t (&s)[32], float (&mx)[4]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 8)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x = !EDGE || ((seen >> (i + k)) & 1u) ? __uint_as_float(s[i + k]) : -INFINITY;
-      const float y = !EDGE || ((seen >> (i + k + 4)) & 1u) ? __uint_as_float(s[i + k + 4]) : -INFINITY;
-      mx[k] = fmaxf(mx[k], fmaxf(x, y));
-    }
+    for (int k = 0; k < 4; ++k)
+      mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[i + k + 4])));
 }
 
 // 32 output dims of a row
@@ -182,8 +181,10 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
   const int row = quad * 32 + lane;
   const int prow = rank * kRows + row;  // the row in a partial state
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-  const bool flip = p.scale_log2 < 0.f;
-  const float scale = fabsf(p.scale_log2);
+  // a scale of zero or below is folded into the queries: a masked score of
+  // -inf stays one
+  const float sign = p.scale_log2 < 0.f ? -1.f : p.scale_log2 > 0.f ? 1.f : 0.f;
+  const float scale = sign == 0.f ? 1.f : fabsf(p.scale_log2);
   QT* out = static_cast<QT*>(p.a);
   uint32_t tile = 0;
   bool ok = true;
@@ -193,7 +194,7 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     tc::fence_after();
     return ok;
   };
-  load_queries<QT>(q_s, p, cur, tok0, flip, st);
+  load_queries<QT>(q_s, p, cur, tok0, sign, st);
   __syncwarp();
   if (lane == 0) arrive_q();
   for (;;) {
@@ -216,30 +217,25 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         const bool whole = pos + kPos - 1 <= w_hi && pos >= w_lo;  // every row of the warp sees every position
         const int x0 = pos_lo - pos, x1 = pos_hi - pos;            // columns the row sees
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        // a whole tile's scores stay in registers; a masked one (a group's
-        // last, or its first behind a window) is read twice by a short loop
         uint32_t s0[32], s1[32], s2[32], s3[32];
-        if (whole) {
-          tc::ld32(ts, s0);
-          tc::ld32(ts + 32, s1);
-          tc::ld32(ts + 64, s2);
-          tc::ld32(ts + 96, s3);
-          tc::wait_ld(s0);
-          tc::wait_ld(s1);
-          tc::wait_ld(s2);
-          tc::wait_ld(s3);
-          max32<false>(s0, 0, mx);
-          max32<false>(s1, 0, mx);
-          max32<false>(s2, 0, mx);
-          max32<false>(s3, 0, mx);
-        } else {
-#pragma unroll 1
-          for (int ch = 0; ch < kPos; ch += 32) {
-            tc::ld32(ts + ch, s0);
-            tc::wait_ld(s0);
-            max32<true>(s0, seen32(x0, x1, ch), mx);
-          }
+        tc::ld32(ts, s0);
+        tc::ld32(ts + 32, s1);
+        tc::ld32(ts + 64, s2);
+        tc::ld32(ts + 96, s3);
+        tc::wait_ld(s0);
+        tc::wait_ld(s1);
+        tc::wait_ld(s2);
+        tc::wait_ld(s3);
+        if (!whole) {
+          mask32(s0, seen32(x0, x1, 0));
+          mask32(s1, seen32(x0, x1, 32));
+          mask32(s2, seen32(x0, x1, 64));
+          mask32(s3, seen32(x0, x1, 96));
         }
+        max32(s0, mx);
+        max32(s1, mx);
+        max32(s2, mx);
+        max32(s3, mx);
         float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         mt = mt == -INFINITY ? mt : mt * scale;
         if (u == t0) {
@@ -263,19 +259,10 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         }
         const float ref = m == -INFINITY ? 0.f : m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        if (whole) {
-          exp32<false, kSplit>(ts, s0, scale, ref, 0, sum);
-          exp32<false, kSplit>(ts + 32, s1, scale, ref, 0, sum);
-          exp32<false, kSplit>(ts + 64, s2, scale, ref, 0, sum);
-          exp32<false, kSplit>(ts + 96, s3, scale, ref, 0, sum);
-        } else {
-#pragma unroll 1
-          for (int ch = 0; ch < kPos; ch += 32) {
-            tc::ld32(ts + ch, s0);
-            tc::wait_ld(s0);
-            exp32<true, kSplit>(ts + ch, s0, scale, ref, seen32(x0, x1, ch), sum);
-          }
-        }
+        exp32<kSplit>(ts, s0, scale, ref, sum);
+        exp32<kSplit>(ts + 32, s1, scale, ref, sum);
+        exp32<kSplit>(ts + 64, s2, scale, ref, sum);
+        exp32<kSplit>(ts + 96, s3, scale, ref, sum);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::wait_st();
       }
@@ -290,7 +277,7 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     const bool more = cur.end < u1;
     if (more) {
       nxt.next(p, sh);
-      load_queries<QT>(q_s, p, nxt, tok0, flip, st);
+      load_queries<QT>(q_s, p, nxt, tok0, sign, st);
       __syncwarp();
       if (lane == 0) arrive_q();
     }
@@ -301,17 +288,23 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       float* part = p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) * (RANKS * paged::kChunkPart);
       QT* dst = out + ((r * p.n_kv + cur.j) * kGroup + (row & 3)) * kHeadDim;
       const float inv = 1.0f / l;
+      auto put = [&](int d, const uint32_t (&o)[32]) {
+        if (tok >= g.n_tok) return;
+        if (split)
+          store32(part + prow * kHeadDim + d, o, 1.0f);
+        else
+          store32(dst + d, o, inv);
+      };
+      uint32_t oa[32], ob[32];
+      tc::ld32(tmem + lanes, oa);
 #pragma unroll 1
-      for (int d = 0; d < kHeadDim; d += 32) {
-        uint32_t o[32];
-        tc::ld32(tmem + lanes + d, o);
-        tc::wait_ld(o);
-        if (tok < g.n_tok) {
-          if (split)
-            store32(part + prow * kHeadDim + d, o, 1.0f);
-          else
-            store32(dst + d, o, inv);
-        }
+      for (int d = 0; d < kHeadDim; d += 64) {
+        tc::wait_ld(oa);
+        tc::ld32(tmem + lanes + d + 32, ob);
+        put(d, oa);
+        tc::wait_ld(ob);
+        if (d + 64 < kHeadDim) tc::ld32(tmem + lanes + d + 64, oa);
+        put(d + 32, ob);
       }
       if (split) {
         part[RANKS * kRows * kHeadDim + prow] = m;
@@ -344,7 +337,8 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
 
 // Join the partial states of the groups that a share's border cut: block
 // (share c, 8 rows of the group that begins in it and goes on), one row per
-// warp, eight dims per lane, the parts in CTA order.
+// warp, eight dims per lane, the parts in CTA order, four parts' loads in
+// flight together.
 constexpr int kJoinRows = 8;
 
 template <typename QT, int RANKS>
@@ -353,27 +347,50 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_paged_join(const __grid_cons
   pdl_trigger();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * kJoinRows + warp;
-  if (row >= __ldcg(&p.joins[c].n_rows)) return;
-  const int last = __ldcg(&p.joins[c].last), G = __ldcg(&p.joins[c].G);
-  const int64_t begin = __ldcg(&p.joins[c].begin), total = __ldcg(&p.joins[c].total);
+  const paged::Join* jp = p.joins + c;
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(jp));  // row0, n_rows, head, last
+  if (row >= a.y) return;
+  const longlong2 bt = __ldcg(reinterpret_cast<const longlong2*>(jp) + 1);  // begin, total
+  const int G = __ldcg(&jp->G), last = a.w;
+  constexpr int kUnroll = 4;
   float M = -INFINITY, L = 0.f, O[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) O[i] = 0.f;
-  for (int q = c; q <= last; ++q) {
-    const float* part = p.part + (int64_t)paged::partial_slot(q, begin, total, G) * (RANKS * paged::kChunkPart);
-    const float m = __ldcg(part + RANKS * kRows * kHeadDim + row), l = __ldcg(part + RANKS * kRows * (kHeadDim + 1) + row);
-    const float4* src = reinterpret_cast<const float4*>(part + row * kHeadDim + 8 * lane);
-    const float4 x = __ldcg(src), y = __ldcg(src + 1);
-    const float mn = fmaxf(M, m);
-    const float a = M == -INFINITY ? 0.f : exp2f(M - mn), b = m == -INFINITY ? 0.f : exp2f(m - mn);
-    M = mn;
-    L = L * a + l * b;
-    O[0] = O[0] * a + x.x * b; O[1] = O[1] * a + x.y * b; O[2] = O[2] * a + x.z * b; O[3] = O[3] * a + x.w * b;
-    O[4] = O[4] * a + y.x * b; O[5] = O[5] * a + y.y * b; O[6] = O[6] * a + y.z * b; O[7] = O[7] * a + y.w * b;
+  // (the first part's slot depends on where the group begins, the others are
+  // their CTAs' first)
+  const int first = paged::partial_slot(c, bt.x, bt.y, G);
+  for (int q0 = c; q0 <= last; q0 += kUnroll) {
+    float m[kUnroll], l[kUnroll];
+    float4 x[kUnroll], y[kUnroll];
+#pragma unroll
+    for (int t = 0; t < kUnroll; ++t) {
+      m[t] = -INFINITY;
+      l[t] = 0.f;
+      x[t] = y[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q0 + t <= last) {
+        const int slot = q0 + t == c ? first : 2 * (q0 + t);
+        const float* part = p.part + (int64_t)slot * (RANKS * paged::kChunkPart);
+        m[t] = __ldcg(part + RANKS * kRows * kHeadDim + row);
+        l[t] = __ldcg(part + RANKS * kRows * (kHeadDim + 1) + row);
+        const float4* src = reinterpret_cast<const float4*>(part + row * kHeadDim + 8 * lane);
+        x[t] = __ldcg(src);
+        y[t] = __ldcg(src + 1);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kUnroll; ++t) {
+      const float mn = fmaxf(M, m[t]);
+      const float s = M == -INFINITY ? 0.f : exp2f(M - mn), r = m[t] == -INFINITY ? 0.f : exp2f(m[t] - mn);
+      M = mn;
+      L = L * s + l[t] * r;
+      O[0] = O[0] * s + x[t].x * r; O[1] = O[1] * s + x[t].y * r; O[2] = O[2] * s + x[t].z * r;
+      O[3] = O[3] * s + x[t].w * r; O[4] = O[4] * s + y[t].x * r; O[5] = O[5] * s + y[t].y * r;
+      O[6] = O[6] * s + y[t].z * r; O[7] = O[7] * s + y[t].w * r;
+    }
   }
   const float inv = 1.0f / L;
-  const int64_t r = __ldcg(&p.joins[c].row0) + (row >> 2);
-  QT* dst = static_cast<QT*>(p.a) + ((r * p.n_kv + __ldcg(&p.joins[c].head)) * kGroup + (row & 3)) * kHeadDim + 8 * lane;
+  QT* dst = static_cast<QT*>(p.a) + (((int64_t)a.x + (row >> 2)) * p.n_kv + a.z) * (kGroup * kHeadDim) +
+            (row & 3) * kHeadDim + 8 * lane;
   if constexpr (std::is_same<QT, float>::value) {
     reinterpret_cast<float4*>(dst)[0] = make_float4(O[0] * inv, O[1] * inv, O[2] * inv, O[3] * inv);
     reinterpret_cast<float4*>(dst)[1] = make_float4(O[4] * inv, O[5] * inv, O[6] * inv, O[7] * inv);
