@@ -59,23 +59,24 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo
 
 // The queries of 32 tokens of the group, from its token `tok0`, into shared
 // memory: 64-dim lines of 128 rows, 16-byte chunk c of row r at c ^ (r % 8)
-// (the 128-byte swizzle).  Rows behind the last token are zero.
+// (the 128-byte swizzle).  Rows behind the last token are zero or stay what
+// they are: their scores reach no other row, and nothing is written for them.
 template <typename QT>
 __device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, int tok0, float sign,
                                              int tid) {
   const QT* q = static_cast<const QT*>(p.q) + (int64_t)cur.j * kGroup * kHeadDim;
   const int64_t row0 = cur.seq.q0 + cur.g.tok + tok0;
   constexpr int kBatch = sizeof(QT) == 2 ? 16 : 8;  // rows in flight per warp
+  const int rows = min(kRows, 4 * (cur.g.n_tok - tok0));
   const int ch = tid & 31;
-  for (int r0 = tid >> 5; r0 < kRows; r0 += 4 * kBatch) {
+  for (int r0 = tid >> 5; r0 < rows; r0 += 4 * kBatch) {
     uint4 v[kBatch][sizeof(QT) / 2];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + 4 * i;
-      const bool in = tok0 + (r >> 2) < cur.g.n_tok;
       const uint4* src = reinterpret_cast<const uint4*>(q + (row0 + (r >> 2)) * p.q_ld + (r & 3) * kHeadDim + 8 * ch);
 #pragma unroll
-      for (int k = 0; k < (int)sizeof(QT) / 2; ++k) v[i][k] = in ? __ldcg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < (int)sizeof(QT) / 2; ++k) v[i][k] = r < rows ? __ldcg(src + k) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -237,7 +238,7 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         max32(s2, mx);
         max32(s3, mx);
         float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        mt = mt == -INFINITY ? mt : mt * scale;
+        mt = mt == -INFINITY || tok >= g.n_tok ? -INFINITY : mt * scale;
         if (u == t0) {
           m = mt;
         } else if (__any_sync(0xffffffffu, mt > m + kRaise)) {
