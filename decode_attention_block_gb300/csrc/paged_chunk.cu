@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    softmax_warps<QT, 1>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, s_full, pv_done, flags, warp, tid - 64,
+    softmax_warps<QT, 1, false>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, s_full, pv_done, flags, warp, tid - 64,
                          [&] { mbar_arrive(q_full); }, [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
   }
   tc::fence_before();
@@ -297,7 +297,7 @@ cudaError_t launch_chunk(const Args& p, const void* k, const void* v, cudaStream
   while (p.page_size % box != 0) box /= 2;
   CUtensorMap mk, mv;
   const int64_t rows = (int64_t)p.n_pages * p.page_size;
-  if (!make_chunk_map(&mk, k, p.n_kv, rows, box) || !make_chunk_map(&mv, v, p.n_kv, rows, box))
+  if (!make_chunk_map(&mk, k, p.n_kv, rows, box, 1) || !make_chunk_map(&mv, v, p.n_kv, rows, box, 1))
     return cudaErrorInvalidValue;
   auto kern = k_paged_chunk<QT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);

@@ -105,6 +105,17 @@ __device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, 
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
 }
 
+// The seen-bits of a folded tile's columns (paged_pair.cu), from those of its
+// positions: the first 8 of each 16 positions, then the last 8 of each.
+__device__ __forceinline__ void fold_seen(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x6420), b = __byte_perm(w[2], w[3], 0x6420);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7531), d = __byte_perm(w[2], w[3], 0x7531);
+  w[0] = a;
+  w[1] = b;
+  w[2] = c;
+  w[3] = d;
+}
+
 // The columns x0 .. x1 of a tile that a row sees, as one bit per column of
 // the 32 from `first`.
 __device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
@@ -172,8 +183,8 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[
 // share a group, one row per thread: scores to probabilities, the running
 // maximum and sum, the output at the group's end.  arrive_q, arrive_p: one
 // lane per warp tells the MMA warp that the queries, or the probabilities in
-// a buffer, are there.
-template <typename QT, int RANKS, typename ArriveQ, typename ArriveP>
+// a buffer, are there.  FOLD: the tiles' columns are in a folded order.
+template <typename QT, int RANKS, bool FOLD, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
                                               uint64_t* s_full, uint64_t* pv_done, volatile int* flags, int warp, int st,
@@ -228,10 +239,12 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         tc::wait_ld(s2);
         tc::wait_ld(s3);
         if (!whole) {
-          mask32(s0, seen32(x0, x1, 0));
-          mask32(s1, seen32(x0, x1, 32));
-          mask32(s2, seen32(x0, x1, 64));
-          mask32(s3, seen32(x0, x1, 96));
+          uint32_t seen[4] = {seen32(x0, x1, 0), seen32(x0, x1, 32), seen32(x0, x1, 64), seen32(x0, x1, 96)};
+          if (FOLD) fold_seen(seen);
+          mask32(s0, seen[0]);
+          mask32(s1, seen[1]);
+          mask32(s2, seen[2]);
+          mask32(s3, seen[3]);
         }
         max32(s0, mx);
         max32(s1, mx);
@@ -401,14 +414,14 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_paged_join(const __grid_cons
   }
 }
 
-// A pool [rows][n_kv][256] bf16 as the chunk kernel loads it: boxes of one
-// 128-byte line of `box` rows of one KV head.
-inline bool make_chunk_map(CUtensorMap* map, const void* base, int n_kv, int64_t rows, int box) {
+// A pool [rows][n_kv][256] bf16 as the chunk kernels load it: boxes of `lines`
+// 128-byte lines of `box` rows of one KV head.
+inline bool make_chunk_map(CUtensorMap* map, const void* base, int n_kv, int64_t rows, int box, int lines) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[4] = {64, (cuuint64_t)rows, 4, (cuuint64_t)n_kv};
   const cuuint64_t strides[3] = {(cuuint64_t)n_kv * kHeadDim * 2, 128, kHeadDim * 2};
-  const cuuint32_t shape[4] = {64, (cuuint32_t)box, 1, 1};
+  const cuuint32_t shape[4] = {64, (cuuint32_t)box, (cuuint32_t)lines, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, shape, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -101,16 +101,16 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle (mode 2 at bits 61..63,
-// version 1 at bit 46).  K-major: rows of 128 bytes, 8-row groups 1024 bytes
-// apart (bits 32..45).  MN-major: 64 elements of the M or N dimension per
-// 128-byte row, one row per K index, 8-row groups 1024 bytes apart, the next
-// 64 elements `line` bytes further (bits 16..29).
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// version 1 at bit 46).  K-major: rows of 128 bytes, 8-row groups (1024 bytes)
+// `group` bytes apart (bits 32..45).  MN-major: 64 elements of the M or N
+// dimension per 128-byte row, one row per K index, 8-row groups `group` bytes
+// apart, the next 64 elements `line` bytes further (bits 16..29).
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr, uint32_t group = 1024) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(group >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, uint32_t line) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(line >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, uint32_t line, uint32_t group = 1024) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(line >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 // Instruction descriptor of kind::f16: fp32 accumulator [4,6), bf16 A and B
