@@ -13,6 +13,7 @@ importing the binding without it raises instead of falling back to anything.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from dataclasses import dataclass, field
 
@@ -373,6 +374,9 @@ class PagedBatch(_CachedC):
                                int(self.table.shape[1]), int(self.n_tokens), int(self.max_q_len))
 
 
+_GET_C, _GET_BYTES, _GET_HEADS = operator.attrgetter("_c"), operator.itemgetter(1), operator.itemgetter(2)
+
+
 def _heads_differ(got, want) -> ValueError:
     return ValueError(f"pages of {got} (heads, dims) do not fit the geometry {want}")
 
@@ -385,12 +389,14 @@ def _pool_c(geom: SparkGeom, pool: PagePool) -> SparkPagePool:
 
 
 def _pools_c(geom: SparkGeom, pools) -> ctypes.Array:
+    built = list(map(_GET_C, pools))
+    if None in built:
+        built = [p.to_c() for p in pools]
     want = (geom.n_kv, geom.head_dim)
-    built = [p._c or p.to_c() for p in pools]
-    for _, _, heads in built:
+    for heads in set(map(_GET_HEADS, built)):
         if heads != want:
             raise _heads_differ(heads, want)
-    return (SparkPagePool * len(built)).from_buffer_copy(b"".join([b[1] for b in built]) or bytes(ctypes.sizeof(SparkPagePool)))
+    return (SparkPagePool * len(built)).from_buffer_copy(b"".join(map(_GET_BYTES, built)))
 
 
 # ---------------------------------------------------------------------------

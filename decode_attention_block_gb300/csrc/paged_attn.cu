@@ -59,6 +59,38 @@ __device__ __forceinline__ void load_q(float* q_s, const __nv_bfloat16* qg, int 
   reinterpret_cast<float4*>(dst)[1] = make_float4(c.x, c.y, f.x, f.y);
 }
 
+// The tensor-core tile's query fragments (attn_parts.cuh, MmaQ) straight from
+// global memory, all loads in flight together: column g & 3 the head, hi
+// halves for g < 4, lo halves after.  By way of shared memory the block's
+// barrier and the bank conflicts of four heads 256 bytes apart cost 1200
+// cycles more.
+__device__ __forceinline__ void load_fragments(MmaQ& Q, const float* qg, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const bool lo = g >= 4;
+  const float2* src = reinterpret_cast<const float2*>(qg + (g & 3) * kHeadDim + 2 * t);
+  float2 x[kHeadDim / 16][2];
+#pragma unroll
+  for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+    x[ks][0] = __ldcg(src + 8 * ks);
+    x[ks][1] = __ldcg(src + 8 * ks + 4);
+  }
+#pragma unroll
+  for (int ks = 0; ks < kHeadDim / 16; ++ks)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) Q.b[ks][i] = pack_bf16x2(split_part(x[ks][i].x, lo), split_part(x[ks][i].y, lo));
+}
+__device__ __forceinline__ void load_fragments(MmaQ& Q, const __nv_bfloat16* qg, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(qg + (g & 3) * kHeadDim + 2 * t);
+#pragma unroll
+  for (int ks = 0; ks < kHeadDim / 16; ++ks)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = __ldcg(src + 8 * ks + 4 * i);
+      Q.b[ks][i] = g < 4 ? w : 0u;
+    }
+}
+
 // eight output dims of one head
 __device__ __forceinline__ void store8(float* dst, const float (&o)[8], float inv) {
   reinterpret_cast<float4*>(dst)[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
@@ -110,22 +142,22 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
     P[h] = M;
     P[4 + h] = L;
   }
-  __threadfence();
   named_bar_sync(kBarMerge, kConsumerThreads);
   if (tid == 0) {
+    __threadfence();  // the block's partial, ordered before this thread by the barrier, before the ticket
     // the group's ticket is that of its first CTA, where no other split group
     // begins; every arrival counts, so the ticket is back at zero after it
     const int last = atomicAdd(&p.tickets[c_first], 1u) == (uint32_t)(c_last - c_first);
     if (last) p.tickets[c_first] = 0;
     flags[1] = last && !flags[0];
+    __threadfence();  // the ticket before the others' partials
   }
   named_bar_sync(kBarMerge, kConsumerThreads);
   if (!flags[1]) return;
-  __threadfence();
   float M2 = -INFINITY, L2 = 0.f, O2[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) O2[i] = 0.f;
-  constexpr int kBatch = 8;  // partials loaded per round trip
+  constexpr int kBatch = 12;  // partials loaded per round trip
   for (int q0 = c_first; q0 <= c_last; q0 += kBatch) {
     float mq[kBatch], lq[kBatch];
     float4 x0[kBatch], x1[kBatch];
@@ -262,12 +294,13 @@ __global__ void __launch_bounds__(kTokThreads, MINB)
     const int64_t t1 = cur.end < u1 ? cur.end : u1;
     const int64_t row = cur.seq.q0 + cur.g.tok;
     named_bar_sync(kBarConsumers, kConsumerThreads);  // the previous group's merge is done
-    load_q(q_s, q + row * p.q_ld + (int64_t)cur.j * kGroup * kHeadDim, tid);
-    named_bar_sync(kBarConsumers, kConsumerThreads);
+    const QT* qg = q + row * p.q_ld + (int64_t)cur.j * kGroup * kHeadDim;
     if constexpr (kMma) {
-      mma_q_from_smem(mq, q_s);
+      load_fragments(mq, qg, lane);
       mst.reset();
     } else {
+      load_q(q_s, qg, tid);
+      named_bar_sync(kBarConsumers, kConsumerThreads);
       st.reset();
     }
     for (int64_t u = cur.begin > u0 ? cur.begin : u0; u < t1; ++u, ++k) {
@@ -316,8 +349,12 @@ cudaError_t launch_token(const Args& p, const void* k, const void* v, cudaStream
   auto kern = k_paged_token<CT, QT, kMinB>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
   if (e != cudaSuccess) return e;
+  // two CTAs per SM, and no more than the tables' rows could give work to
+  const int64_t tiles = (int64_t)p.max_pages * (p.page_size / kTile);
+  const int64_t most = ((int64_t)p.n_seqs * p.n_kv * p.max_q * tiles + kMinUnits - 1) / kMinUnits;
   int grid = kMinB * device_sm_count();
   if (grid > paged::kMaxCtas) grid = paged::kMaxCtas;
+  if (grid > most) grid = (int)most;
   return launch_pdl(kern, dim3(grid), dim3(kTokThreads), S::kAlloc, st, mk, mv, p);
 }
 

@@ -166,7 +166,9 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
     Seq q = {0, 0, 0, false};
     if (lane < p.n_seqs) q = load_seq(p, lane);
     if (q.bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.err, kErrIndex);
-    const int64_t per_head = q.n > 0 ? units_of(q, sh) : 0;
+    // (a single token's units are its one group's)
+    const Group only = group_of(q, sh, 0);
+    const int64_t per_head = q.n == 0 ? 0 : sh.gt == 1 && p.max_q == 1 ? only.tile1 - only.tile0 : units_of(q, sh);
     int64_t run = per_head * p.n_kv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -184,7 +186,15 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
     cur.seq.n = __shfl_sync(0xffffffffu, q.n, cur.s);
     cur.seq.p0 = __shfl_sync(0xffffffffu, q.p0, cur.s);
     cur.seq.bad = false;
-    cur.seek(sh, share.u0, __shfl_sync(0xffffffffu, first, cur.s), __shfl_sync(0xffffffffu, per_head, cur.s));
+    const int64_t at = __shfl_sync(0xffffffffu, first, cur.s), each = __shfl_sync(0xffffffffu, per_head, cur.s);
+    if (sh.gt == 1 && p.max_q == 1) {
+      cur.groups = 1;
+      cur.i = 0;
+      cur.j = (int)quotient(share.u0 - at, each);
+      cur.set_group(sh, at + cur.j * each);
+    } else {
+      cur.seek(sh, share.u0, at, each);
+    }
     return true;
   }
   work_prefix<NT>(p, sh, room, room + SPARK_MAX_BATCH + 2);
