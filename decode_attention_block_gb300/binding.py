@@ -339,7 +339,7 @@ class PagePool(_CachedC):
     _c: object = field(default=None, init=False, repr=False, compare=False)
 
     def _build_c(self) -> tuple:
-        """The C struct, its bytes (for arrays of them) and (n_kv, head_dim)."""
+        """The C struct, its bytes (for arrays of them) and (n_kv, head_dim, device)."""
         dt = self.k.dtype
         if dt not in _DTYPE_CODE:
             raise TypeError(f"pages must be float32 or bfloat16, got {dt}")
@@ -347,7 +347,9 @@ class PagePool(_CachedC):
             raise ValueError("k and v must both be [n_pages, page_size, n_kv, head_dim]")
         c = SparkPagePool(_dev_ptr(self.k, "k", dt), _dev_ptr(self.v, "v", dt), int(self.k.shape[0]),
                           int(self.k.shape[1]), _DTYPE_CODE[dt])
-        return c, bytes(c), (int(self.k.shape[2]), int(self.k.shape[3]))
+        if self.v.get_device() != self.k.get_device():
+            raise ValueError("k and v must be on the same device")
+        return c, bytes(c), (int(self.k.shape[2]), int(self.k.shape[3]), self.k.get_device())
 
 
 @dataclass
@@ -377,14 +379,16 @@ class PagedBatch(_CachedC):
 _GET_C, _GET_BYTES, _GET_HEADS = operator.attrgetter("_c"), operator.itemgetter(1), operator.itemgetter(2)
 
 
-def _heads_differ(got, want) -> ValueError:
-    return ValueError(f"pages of {got} (heads, dims) do not fit the geometry {want}")
+def _pool_differs(got, want) -> ValueError:
+    return ValueError(f"pages of {got[0]} heads of {got[1]} on device {got[2]}: the geometry has {want[0]} of {want[1]}, "
+                      f"the current device is {want[2]}")
 
 
 def _pool_c(geom: SparkGeom, pool: PagePool) -> SparkPagePool:
     c, _, heads = pool.to_c()
-    if heads != (geom.n_kv, geom.head_dim):
-        raise _heads_differ(heads, (geom.n_kv, geom.head_dim))
+    want = (geom.n_kv, geom.head_dim, torch.cuda.current_device())
+    if heads != want:
+        raise _pool_differs(heads, want)
     return c
 
 
@@ -392,10 +396,10 @@ def _pools_c(geom: SparkGeom, pools) -> ctypes.Array:
     built = list(map(_GET_C, pools))
     if None in built:
         built = [p.to_c() for p in pools]
-    want = (geom.n_kv, geom.head_dim)
+    want = (geom.n_kv, geom.head_dim, torch.cuda.current_device())
     for heads in set(map(_GET_HEADS, built)):
         if heads != want:
-            raise _heads_differ(heads, want)
+            raise _pool_differs(heads, want)
     return (SparkPagePool * len(built)).from_buffer_copy(b"".join(map(_GET_BYTES, built)))
 
 

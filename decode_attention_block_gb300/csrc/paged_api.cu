@@ -39,6 +39,12 @@ int spark_paged_attention(const spark_geom* g, const void* q, int64_t q_ld, int3
   if ((s = check_paged_batch(batch, pool)) != SPARK_OK) return s;
   if ((s = check_rows(q, dtype, q_ld, (int64_t)g->n_q * kHeadDim)) != SPARK_OK) return s;
   if (!a || !aligned16(a)) return SPARK_ERR_INVALID_ARG;
+  // rows of q are read while rows of a are written
+  const int64_t es = dtype == SPARK_BF16 ? 2 : 4, width = (int64_t)g->n_q * kHeadDim;
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), a0 = reinterpret_cast<uintptr_t>(a);
+  const uintptr_t q1 = q0 + (uintptr_t)(((batch->n_tokens - 1) * q_ld + width) * es);
+  const uintptr_t a1 = a0 + (uintptr_t)(batch->n_tokens * width * es);
+  if (q0 < a1 && a0 < q1) return SPARK_ERR_INVALID_ARG;
   if ((s = check_paged_ws(workspace, workspace_bytes)) != SPARK_OK) return s;
   paged::Args p = paged_args(g, pool, layer_class, batch, workspace);
   p.q = q;

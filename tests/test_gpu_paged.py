@@ -176,6 +176,9 @@ SETS = {
     "long": [(5000, 1)],
     "long_chunk": [(2100, 70)],
     "big_chunk": [(1300, 1100), (700, 257)],
+    "edges": [(64, 64), (65, 65), (128, 33), (129, 32), (200, 63), (256, 128), (31, 31), (33, 33)],
+    "far": [(9000, 40)],     # one group over many CTAs
+    "far_short": [(9000, 6)],
 }
 
 
@@ -229,6 +232,69 @@ def test_many_sequences(B):
     seqs = [(int(c), int(min(c, n))) for c, n in zip(r.integers(0, 90, 1024), r.integers(0, 3, 1024))]
     _check_attention(B, Case(seqs, n_kv=1, page=16, seed=6), F32)
     _check_attention(B, Case(seqs, n_kv=1, page=16, seed=6), BF16, full=False, window=20)
+
+
+def test_nothing_to_do(B):
+    """Sequences without new tokens only: nothing is written, nothing reported."""
+    for max_q in (1, 20, 64):
+        case = Case([(40, 0), (0, 0)], page=16, seed=3, pad=70)
+        _check_attention_empty(B, case, max_q)
+
+
+def _check_attention_empty(B, case, max_q):
+    g = _geom(B)
+    q = torch.randn(case.n_tokens, 4096, device="cuda")
+    a = torch.full_like(q, 5.0)
+    ws = B.make_paged_workspace(g)
+    batch, pool = case.batch(B, max_q=max_q), B.PagePool(case.k, case.v)
+    B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, a, ws)
+    k0 = case.k.clone()
+    B.spark_paged_append(g, q[:, :1024], q[:, 1024:2048], pool, batch, ws)
+    assert B.spark_attn_error_word(ws) == 0
+    assert bool((a == 5.0).all()) and torch.equal(case.k.view(torch.int16), k0.view(torch.int16))
+
+
+def test_pages_far_into_a_pool(B):
+    """Page offsets beyond 2^32 bytes, in the append, the attention kernels and
+    the copies of a fork."""
+    page, n_kv, n_pages = 1024, 8, 1200                       # 4 MB a page: 4.7 GB of K and of V
+    free = torch.cuda.mem_get_info()[0]
+    if free < 14 << 30:
+        pytest.skip("needs 14 GB")
+    k = torch.empty(n_pages, page, n_kv, D, device="cuda", dtype=BF16)
+    v = torch.empty_like(k)
+    pool, g = B.PagePool(k, v), _geom(B, n_kv)
+    ws = B.make_paged_workspace(g)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    seqs = [(70, 70), (3, 3), (1100, 40)]
+    table = _i32([[1199, -1, -1], [1100, -1, -1], [1150, 1198, -1]])
+    start, lens = _i32([0, 70, 73, 113]), _i32([70, 3, 1100])
+    # the third sequence's first rows come by an append of their own
+    x = torch.randn(1060, 2 * n_kv * D, generator=gen, device="cuda").to(BF16)
+    B.spark_paged_append(g, x[:, :n_kv * D], x[:, n_kv * D:], pool,
+                         B.PagedBatch(table[2:], _i32([0, 1060]), _i32([1060]), 1060, 1060), ws)
+    y = torch.randn(113, 2 * n_kv * D, generator=gen, device="cuda").to(BF16)
+    B.spark_paged_append(g, y[:, :n_kv * D], y[:, n_kv * D:], pool, B.PagedBatch(table, start, lens, 113, 70), ws)
+    assert torch.equal(k[1199, 69].reshape(-1), y[69, :n_kv * D]) and torch.equal(v[1198, 75].reshape(-1), y[112, n_kv * D:])
+    case = Case(seqs, n_kv=n_kv, page=16, seed=2)
+    rows = [y[:70], y[70:73], torch.cat([x, y[73:]])]
+    case.rows_k = [r[:, :n_kv * D].reshape(-1, n_kv, D) for r in rows]
+    case.rows_v = [r[:, n_kv * D:].reshape(-1, n_kv, D) for r in rows]
+    q = torch.randn(113, 4 * n_kv * D, generator=gen, device="cuda").to(BF16)
+    a = torch.zeros_like(q)
+    B.spark_paged_attention(g, q, pool, B.SPARK_FULL, B.PagedBatch(table, start, lens, 113, 70), a, ws)
+    want, bound = _reference(case, q, 0, 0.0625, BF16, 2.0**-8)
+    assert ((a.double().view(want.shape) - want).abs() / bound).max().item() <= 1.0
+    one = torch.zeros(1, 4 * n_kv * D, device="cuda", dtype=BF16)      # its last token by the single-token kernel
+    B.spark_paged_attention(g, q[112:], pool, B.SPARK_FULL, B.PagedBatch(table[2:], _i32([0, 1]), _i32([1100]), 1, 1), one, ws)
+    assert ((one.double().view(1, -1, D) - want[112:]).abs() / bound[112:]).max().item() <= 1.0
+    assert B.spark_attn_error_word(ws) == 0
+    tws = B.make_pages_workspace(n_pages, 3)
+    new = torch.zeros_like(table)
+    k[0].fill_(0)
+    B.spark_pages_remap(g, [pool], table, _i32([0, 0, -1]), _i32([70, 70, 0]), _i32([70, 70, 0]), new, tws)
+    assert B.spark_attn_error_word(tws) == 0 and new.tolist() == [[1199, -1, -1], [0, -1, -1], [-1, -1, -1]]
+    assert torch.equal(k[0, :70], k[1199, :70]) and torch.equal(v[0, :70], v[1199, :70]) and not bool(k[0, 70:].any())
 
 
 def test_large_scores_and_one_dominant_row(B):
@@ -511,24 +577,34 @@ def test_remap_is_all_or_nothing(B):
 
 
 def test_remap_at_its_limits(B):
-    """1024 slots; a table wider than a block; many more pages than the plan's threads."""
+    """1024 slots; a table wider than a block; many more pages than the plan's
+    threads; both forms of the plan (pools and tables that fit one CTA's
+    shared memory, and larger ones)."""
     r = np.random.default_rng(1)
-    table = _scattered(r, r.integers(0, 33, 1024), 16, 20011, 3)
-    keep = np.array([0 if row[0] < 0 else 5 for row in table])
-    parent = np.where(keep > 0, np.arange(1024), -1)
-    _run_remap(B, table, parent.tolist(), keep.tolist(), (keep + 20).tolist(), 16, 20011, layers=1, n_kv=1)
-    wide = _scattered(r, [16 * 4000 + 3, 0], 16, 5000, 5000)
-    _run_remap(B, wide, [0, 0], [16 * 4000 + 3, 16 * 3999 + 1], [16 * 4100, 16 * 3999 + 1], 16, 5000, layers=1, n_kv=1)
+    for n_pages in (20011, 24576, 24577, 90001):
+        table = _scattered(r, r.integers(0, 33, 1024), 16, n_pages, 3)
+        keep = np.array([0 if row[0] < 0 else 5 for row in table])
+        parent = np.where(keep > 0, np.arange(1024), -1)
+        _run_remap(B, table, parent.tolist(), keep.tolist(), (keep + 20).tolist(), 16, n_pages, layers=1, n_kv=1)
+    for width in (5000, 32768, 32769):
+        wide = _scattered(r, [16 * 4000 + 3, 0], 16, 5000, width)
+        _run_remap(B, wide, [0, 0], [16 * 4000 + 3, 16 * 3999 + 1], [16 * 4100, 16 * 3999 + 1], 16, 5000, layers=1, n_kv=1)
+    # too few pages, and a bad entry, in the larger form
+    assert _run_remap(B, wide, [0, 0], [16 * 4000 + 3] * 2, [16 * 4999] * 2, 16, 5000, layers=1, n_kv=1) == 4
+    wide[0, 5] = 5000
+    assert _run_remap(B, wide, [0, 0], [16 * 4000 + 3] * 2, [16 * 4001] * 2, 16, 5000, layers=1, n_kv=1) == 2
 
 
-@pytest.mark.parametrize("seed", range(10))
+@pytest.mark.parametrize("seed", range(13))
 def test_compact(B, seed):
     r = np.random.default_rng(seed)
-    page, n_kv, layers = (16, 2, 3) if seed % 2 else (32, 1, 1)
+    page, n_kv, layers = (16, 2, 3) if seed % 2 and seed < 10 else (32 if seed < 10 else 16, 1, 1)
     n = int(r.integers(1, 40))
     lens = r.integers(0, 12 * page, n)
     need = int(sum(-(-lens // page)))
     n_pages = max(1, need + int(r.integers(0, 3 * need + 2)) * (seed != 4))
+    if seed >= 10:
+        n_pages = 30000                                         # the plan's larger form
     table = _scattered(r, lens, page, n_pages, 13)
     if n > 2 and seed % 3 == 0:
         table[1] = table[0]                                     # shared pages

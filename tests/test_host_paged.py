@@ -159,7 +159,7 @@ def _batch(B, **kw):
     return B.SparkPagedBatch(*f.values())
 
 
-def _attention(B, geom=None, q=FAKE, ld=4096, dtype=1, pool=None, cls=1, batch=None, a=FAKE, ws=FAKE, nbytes=None):
+def _attention(B, geom=None, q=FAKE, ld=4096, dtype=1, pool=None, cls=1, batch=None, a=FAKE + (1 << 30), ws=FAKE, nbytes=None):
     lib = B.load()
     g = geom or B.spark_geom_default()
     nbytes = B.spark_paged_workspace_bytes(B.spark_geom_default()) if nbytes is None else nbytes
@@ -196,6 +196,9 @@ def test_pools_and_batches_are_validated(B):
 def test_attention_arguments_are_validated(B):
     assert _attention(B, q=0) == -1 and _attention(B, q=FAKE + 8) == -1
     assert _attention(B, a=0) == -1 and _attention(B, a=FAKE + 4) == -1
+    rows = 9 * 4096 * 2                                                     # q and a do not overlap
+    assert _attention(B, a=FAKE) == -1 and _attention(B, a=FAKE + rows - 16) == -1 and _attention(B, a=FAKE - rows + 16) == -1
+    assert _attention(B, a=FAKE + rows, ws=0) == -4 and _attention(B, a=FAKE - rows, ws=0) == -4
     assert _attention(B, ld=4095) == -1 and _attention(B, ld=4100) == -1    # rows not 16-byte aligned
     assert _attention(B, ld=4098, dtype=0) == -1 and _attention(B, ld=4088) == -1
     assert _attention(B, dtype=2) == -1 and _attention(B, cls=2) == -1
