@@ -11,6 +11,12 @@
 // box per K or V tile, the page number from the table) to four consumer warps
 // holding the softmax states: the schedule and the tile of the contiguous
 // cache's decode attention (attn.cu, attn_parts.cuh).
+//
+// Measured: 64 sequences at 512-32768 (4.92 GB of rows) 0.71 ms, 6.95 TB/s,
+// 1.04 of the measured copy bandwidth; 16 at 400-3000 34 us, where the first
+// tile lands after 4 us and the merge takes 4 more; one at 700 8.2 us, all of
+// it latency (share 1.6 us, first tile 1.2, one tile a warp 1.1, merge 2.2).
+// fp32 pools run the same schedule on the CUDA cores.
 #include <math.h>
 
 #include <type_traits>
@@ -157,23 +163,24 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
   float M2 = -INFINITY, L2 = 0.f, O2[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) O2[i] = 0.f;
-  constexpr int kBatch = 12;  // partials loaded per round trip
+  constexpr int kBatch = 8;  // partials loaded per round trip
+  // (the first part's slot depends on where the group begins, the others are
+  // their CTAs' first)
+  const int first = paged::partial_slot(c_first, begin, total, G);
   for (int q0 = c_first; q0 <= c_last; q0 += kBatch) {
     float mq[kBatch], lq[kBatch];
     float4 x0[kBatch], x1[kBatch];
 #pragma unroll
     for (int t = 0; t < kBatch; ++t) {
-      if (q0 + t <= c_last) {
-        const float* Pq = p.part + (int64_t)paged::partial_slot(q0 + t, begin, total, G) * kPartFloats;
-        mq[t] = __ldcg(Pq + h);
-        lq[t] = __ldcg(Pq + 4 + h);
-        x0[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane));
-        x1[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane + 4));
-      } else {
-        mq[t] = -INFINITY;
-        lq[t] = 0.f;
-        x0[t] = x1[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      // (behind the last part the last once more, at weight 0: loads without
+      // a condition stay in flight together)
+      const int q = min(q0 + t, c_last);
+      const float* Pq = p.part + (int64_t)(q == c_first ? first : 2 * q) * kPartFloats;
+      mq[t] = __ldcg(Pq + h);
+      lq[t] = __ldcg(Pq + 4 + h);
+      x0[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane));
+      x1[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane + 4));
+      if (q0 + t > c_last) mq[t] = -INFINITY;
     }
     float mb = M2;
 #pragma unroll
@@ -377,8 +384,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 // A CTA takes up to kAppendTokens consecutive tokens: their page rows first,
 // one thread each (a binary search in q_start, then the table), then the
 // rows' words four at a time per thread, whatever rows they are of.  Bound by
-// the rows' bytes where there are many, by the chain of dependent loads where
-// there are few.
+// the rows' bytes where there are many (8370 tokens, 103 MB: 16.5 us, 6.2
+// TB/s; one CTA per token took 80 us, its dependent loads exposed), by the
+// chain of dependent loads where there are few (64 tokens: 3 us).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 16;
 constexpr int kAppendUnroll = 4;
@@ -467,11 +475,15 @@ cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype,
   // fp32 pools, and single tokens, a token at a time
   if (cdtype != SPARK_BF16 || p.max_q == 1) return launch_paged_token(p, qdtype, cdtype, k, v, st);
   if (p.max_q <= paged::kChunkTokens) return launch_paged_chunk(p, qdtype, k, v, st);
-  // Longer chunks take pairs of CTAs; in a mixed batch the sequences of up to
+  // Longer chunks take pairs of CTAs.  In a mixed batch the sequences of up to
   // 32 new tokens go to the single-CTA kernel, where they do not leave half
   // of a pair's rows empty (32 sequences, 4 of them with chunks of ~400
-  // tokens, fp32 queries: pairs alone 311 us, single CTAs alone 230 us).
-  if (p.n_seqs == 1) return launch_paged_pair(p, qdtype, k, v, st);
+  // tokens, fp32 queries: pairs alone 311 us, single CTAs alone 230 us, both
+  // 213 us).  Where the average is above half of the longest, most sequences
+  // are long, and a second kernel for the rest would mostly find nothing to
+  // do (three of 100 tokens at 800:
+  // 35 us with both, 29 us with pairs alone).
+  if (p.n_seqs == 1 || 2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q) return launch_paged_pair(p, qdtype, k, v, st);
   paged::Args a = p;
   a.from = paged::kChunkTokens + 1;
   const cudaError_t e = launch_paged_pair(a, qdtype, k, v, st);

@@ -27,6 +27,15 @@
 // Work is the flat list of paged.h (128-position tiles), every CTA an equal
 // share: a group cut by a share's border leaves fp32 partial states, joined
 // in CTA order by k_paged_join.
+//
+// This kernel takes chunks of up to 32 tokens, which are bound by the rows
+// read from HBM (32 sequences at 4096-8192, 0.82 GB: 4 tokens each 132 us,
+// 6.2 TB/s; 32 tokens 158 us, 5.3 TB/s, 658 TFLOP/s); longer ones are bound
+// by what a CTA alone takes in from L2, and go to paged_pair.cu.  What it
+// cost on the way (a chunk of 4096 tokens at 4096): 128 columns unrolled in
+// the softmax missed the instruction cache, 566 us; operands of an MMA moved
+// to uniform registers one by one, 361 -> 335; scores read twice, 335 -> 330;
+// the table's entry looked up when needed, 330 -> 309.
 #include "paged_chunk_parts.cuh"
 
 namespace spark {

@@ -378,18 +378,16 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_paged_join(const __grid_cons
     float4 x[kUnroll], y[kUnroll];
 #pragma unroll
     for (int t = 0; t < kUnroll; ++t) {
-      m[t] = -INFINITY;
-      l[t] = 0.f;
-      x[t] = y[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (q0 + t <= last) {
-        const int slot = q0 + t == c ? first : 2 * (q0 + t);
-        const float* part = p.part + (int64_t)slot * (RANKS * paged::kChunkPart);
-        m[t] = __ldcg(part + RANKS * kRows * kHeadDim + row);
-        l[t] = __ldcg(part + RANKS * kRows * (kHeadDim + 1) + row);
-        const float4* src = reinterpret_cast<const float4*>(part + row * kHeadDim + 8 * lane);
-        x[t] = __ldcg(src);
-        y[t] = __ldcg(src + 1);
-      }
+      // (behind the last part the last once more, at weight 0: loads without
+      // a condition stay in flight together)
+      const int q = min(q0 + t, last), slot = q == c ? first : 2 * q;
+      const float* part = p.part + (int64_t)slot * (RANKS * paged::kChunkPart);
+      m[t] = __ldcg(part + RANKS * kRows * kHeadDim + row);
+      l[t] = __ldcg(part + RANKS * kRows * (kHeadDim + 1) + row);
+      const float4* src = reinterpret_cast<const float4*>(part + row * kHeadDim + 8 * lane);
+      x[t] = __ldcg(src);
+      y[t] = __ldcg(src + 1);
+      if (q0 + t > last) m[t] = -INFINITY;
     }
 #pragma unroll
     for (int t = 0; t < kUnroll; ++t) {

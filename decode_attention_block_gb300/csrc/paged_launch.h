@@ -1,5 +1,5 @@
-// paged_launch.h -- host launchers of the paged cache's kernels and of the
-// token scores (internal to the library).
+// paged_launch.h -- host launchers of the paged cache's attention and append
+// kernels (internal to the library).
 #pragma once
 
 #include "paged_parts.cuh"

