@@ -312,8 +312,10 @@ __global__ void __launch_bounds__(kThreads, 4)
         top.offer(mask != 0 && at < w1 && e >= 0 && e < vocab ? make_key(y, (uint32_t)e) : 0, k, lane);
         mask &= mask - 1;
       }
-      // the list's last, once it is full (a NaN is below everything)
-      if (top.least != 0) least = fmaxf(least, key_value(top.least));
+      // the next value above the list's last, once it is full: the tiles to
+      // come have higher indices, so what equals it stays out (a row masked
+      // down to fewer than k logits would offer every -inf otherwise)
+      if (top.least != 0) least = fmaxf(least, value_of((uint32_t)(top.least >> 32) + 1));
       publish(sm, top, share, lane, warp);
     }
   }

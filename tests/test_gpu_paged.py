@@ -853,10 +853,12 @@ def test_logprobs_ties_orders_and_masks(B, dtype):
             i / v, -i / v, (i * 7919 % v) / v,                              # ascending, descending, mixed
             torch.where(i % 1000 == 999, 0.5, neg),                         # nine tokens left
             torch.where(i == 8888, 2.0, neg),                               # one left
+            torch.where((i == 8998) | (i == 8990), 0.0, torch.where(i == 4100, -0.0, neg)),  # three, equal, far apart
+            torch.where(i % 700 == 3, 1.0, 0.0),                            # thirteen above a plateau
             torch.where(i < 4000, torch.finfo(dtype).min, 1.0),             # the type's lowest value as a mask
             torch.where(i == 5, 80.0, torch.randn(v, device="cuda"))]       # all but certain
     x = torch.stack(rows).to(dtype)
-    t = _i32([8999, 0, 8999, 0, 17, 999, 0, 3, 5])
+    t = _i32([8999, 0, 8999, 0, 17, 999, 0, 4100, 3, 3, 5])
     got = _scores(B, x, t, 16)
     assert got["word"] == 0
     _check_scores(got, x, t, 16)
