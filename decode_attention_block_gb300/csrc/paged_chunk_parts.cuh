@@ -32,6 +32,14 @@ constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
 constexpr int kMinTiles = 2;                    // tiles per CTA at least
 
+// 3-D tiled TMA load global -> shared, completing on `bar` (byte count).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -57,52 +65,53 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// The queries of 32 tokens of the group, from its token `tok0`, into shared
-// memory: 64-dim lines of 128 rows, 16-byte chunk c of row r at c ^ (r % 8)
-// (the 128-byte swizzle).  Rows behind the last token are zero or stay what
-// they are: their scores reach no other row, and nothing is written for them.
-template <typename QT>
-__device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, int tok0, float sign,
-                                             int tid) {
-  const QT* q = static_cast<const QT*>(p.q) + (int64_t)cur.j * kGroup * kHeadDim;
+// fp32 queries of 32 tokens of the group, from its token `tok0`, into shared
+// memory as bf16 halves: 64-dim lines of 128 rows, 16-byte chunk c of row r at
+// c ^ (r % 8) (the 128-byte swizzle).  Rows behind the last token are zero or
+// stay what they are: their scores reach no other row, and nothing is written
+// for them.
+__device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, int tok0, int tid) {
+  const float* q = static_cast<const float*>(p.q) + (int64_t)cur.j * kGroup * kHeadDim;
   const int64_t row0 = cur.seq.q0 + cur.g.tok + tok0;
-  constexpr int kBatch = sizeof(QT) == 2 ? 16 : 8;  // rows in flight per warp
+  constexpr int kBatch = 8;  // rows in flight per warp
   const int rows = min(kRows, 4 * (cur.g.n_tok - tok0));
   const int ch = tid & 31;
   for (int r0 = tid >> 5; r0 < rows; r0 += 4 * kBatch) {
-    uint4 v[kBatch][sizeof(QT) / 2];
+    float4 v[kBatch][2];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + 4 * i;
-      const uint4* src = reinterpret_cast<const uint4*>(q + (row0 + (r >> 2)) * p.q_ld + (r & 3) * kHeadDim + 8 * ch);
+      const float4* src = reinterpret_cast<const float4*>(q + (row0 + (r >> 2)) * p.q_ld + (r & 3) * kHeadDim + 8 * ch);
 #pragma unroll
-      for (int k = 0; k < (int)sizeof(QT) / 2; ++k) v[i][k] = r < rows ? __ldcg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < 2; ++k) v[i][k] = r < rows ? __ldcg(src + k) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + 4 * i;
       const uint32_t at = (uint32_t)(ch >> 3) * kLineBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-      if constexpr (std::is_same<QT, float>::value) {
-        float x[8];
-        const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = sign * __uint_as_float(w[k]);
-        uint4 hi, lo;
-        split8(x, hi, lo);
-        *reinterpret_cast<uint4*>(q_s + at) = hi;
-        *reinterpret_cast<uint4*>(q_s + kQBytes + at) = lo;
-      } else {
-        uint4 w = v[i][0];
-        if (sign < 0.f) {
-          w.x ^= 0x80008000u; w.y ^= 0x80008000u; w.z ^= 0x80008000u; w.w ^= 0x80008000u;
-        } else if (sign == 0.f) {
-          w = make_uint4(0u, 0u, 0u, 0u);
-        }
-        *reinterpret_cast<uint4*>(q_s + at) = w;
-      }
+      const float x[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+      uint4 hi, lo;
+      split8(x, hi, lo);
+      *reinterpret_cast<uint4*>(q_s + at) = hi;
+      *reinterpret_cast<uint4*>(q_s + kQBytes + at) = lo;
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
+}
+
+// bf16 queries as TMA loads them into the same layout: a box is one 64-dim
+// line of 4 heads of 32 tokens.  Rows behind the tensor are zero, rows behind
+// the group's last token those of other tokens.
+inline bool make_query_map(CUtensorMap* map, const void* q, int64_t q_ld, int n_q, int n_tokens) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)n_q, (cuuint64_t)n_tokens};
+  const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)q_ld * 2};
+  const cuuint32_t shape[3] = {64, kGroup, paged::kChunkTokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, shape, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The seen-bits of a folded tile's columns (paged_pair.cu), from those of its
@@ -162,6 +171,12 @@ __device__ __forceinline__ void max32(const uint32_t (&s)[32], float (&mx)[4]) {
 }
 
 // 32 output dims of a row
+// scores of a negative or zero scale
+__device__ __forceinline__ void sign32(uint32_t (&s)[32], float sign) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * sign);
+}
+
 // 32 output dims of a row
 __device__ __forceinline__ void store32(float* dst, const uint32_t (&o)[32], float inv) {
 #pragma unroll
@@ -182,19 +197,23 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[
 // The four softmax warps (st: their thread, 0 .. 127) of a CTA of RANKS that
 // share a group, one row per thread: scores to probabilities, the running
 // maximum and sum, the output at the group's end.  arrive_q, arrive_p: one
-// lane per warp tells the MMA warp that the queries, or the probabilities in
-// a buffer, are there.  FOLD: the tiles' columns are in a folded order.
-template <typename QT, int RANKS, bool FOLD, typename ArriveQ, typename ArriveP>
+// lane per warp tells the MMA warp that fp32 queries (bf16 ones come by TMA),
+// or the probabilities in a buffer, are there.  FOLD: the tiles' columns are in a folded order.
+constexpr int kStageRow = 64 + 16;             // bytes of a row of an output stage: 32 bf16 dims, padding
+constexpr int kStageBytes = 32 * kStageRow;    // of a warp
+
+template <typename QT, int RANKS, bool FOLD, bool STAGE, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
-                                              uint64_t* s_full, uint64_t* pv_done, volatile int* flags, int warp, int st,
+                                              uint64_t* s_full, uint64_t* pv_done, volatile int* flags, unsigned char* stage,
+                                              int warp, int st,
                                               ArriveQ arrive_q, ArriveP arrive_p) {
   const int quad = warp & 3, lane = st & 31, tok0 = rank * paged::kChunkTokens;
   const int row = quad * 32 + lane;
   const int prow = rank * kRows + row;  // the row in a partial state
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-  // a scale of zero or below is folded into the queries: a masked score of
-  // -inf stays one
+  // a scale of zero or below is taken to the scores before they are masked: a
+  // masked one of -inf stays that
   const float sign = p.scale_log2 < 0.f ? -1.f : p.scale_log2 > 0.f ? 1.f : 0.f;
   const float scale = sign == 0.f ? 1.f : fabsf(p.scale_log2);
   QT* out = static_cast<QT*>(p.a);
@@ -206,9 +225,11 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     tc::fence_after();
     return ok;
   };
-  load_queries<QT>(q_s, p, cur, tok0, sign, st);
-  __syncwarp();
-  if (lane == 0) arrive_q();
+  if (kSplit) {
+    load_queries(q_s, p, cur, tok0, st);
+    __syncwarp();
+    if (lane == 0) arrive_q();
+  }
   for (;;) {
     const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
     const paged::Group g = cur.g;
@@ -238,6 +259,12 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         tc::wait_ld(s1);
         tc::wait_ld(s2);
         tc::wait_ld(s3);
+        if (sign != 1.f) {
+          sign32(s0, sign);
+          sign32(s1, sign);
+          sign32(s2, sign);
+          sign32(s3, sign);
+        }
         if (!whole) {
           uint32_t seen[4] = {seen32(x0, x1, 0), seen32(x0, x1, 32), seen32(x0, x1, 64), seen32(x0, x1, 96)};
           if (FOLD) fold_seen(seen);
@@ -285,15 +312,17 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       if (lane == 0) arrive_p(buf);
     }
     if (!ok) break;
-    // Q is free (the last S is done): the next group's queries load while
+    // Q is free (the last S is done): the next group's fp32 queries load while
     // this one's last product runs
     Cursor nxt = cur;
     const bool more = cur.end < u1;
     if (more) {
       nxt.next(p, sh);
-      load_queries<QT>(q_s, p, nxt, tok0, sign, st);
-      __syncwarp();
-      if (lane == 0) arrive_q();
+      if (kSplit) {
+        load_queries(q_s, p, nxt, tok0, st);
+        __syncwarp();
+        if (lane == 0) arrive_q();
+      }
     }
     if (!wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) break;
     const bool split = cur.begin < u0 || cur.end > u1;
@@ -302,12 +331,42 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       float* part = p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) * (RANKS * paged::kChunkPart);
       QT* dst = out + ((r * p.n_kv + cur.j) * kGroup + (row & 3)) * kHeadDim;
       const float inv = 1.0f / l;
+      constexpr int kAll = RANKS * kRows;
+      // A partial state is [dims / 4][row][4], then the maxima and the sums: the
+      // lanes' rows lie next to one another (row by row, 32 lines of 128 bytes
+      // per store, the output took 10000 cycles a group).
       auto put = [&](int d, const uint32_t (&o)[32]) {
-        if (tok >= g.n_tok) return;
-        if (split)
-          store32(part + prow * kHeadDim + d, o, 1.0f);
-        else
+        if (split) {
+          float4* to = reinterpret_cast<float4*>(part) + (d / 4) * kAll + prow;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            to[i * kAll] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        } else if constexpr (STAGE) {
+          // through the warp's stage, 32 rows of 64 bytes and 16 of padding: a
+          // row's dims leave next to one another
+          unsigned char* mine = stage + quad * kStageBytes;
+          uint4* at = reinterpret_cast<uint4*>(mine + lane * kStageRow);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            at[i] = make_uint4(pack2(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv),
+                               pack2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv),
+                               pack2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv),
+                               pack2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2);  // the warp's row
+            const uint4 w = *reinterpret_cast<const uint4*>(mine + rr * kStageRow + (lane & 3) * 16);
+            const int t = tok0 + 8 * quad + (rr >> 2);
+            if (t < g.n_tok)
+              *reinterpret_cast<uint4*>(out + (((cur.seq.q0 + g.tok + t) * (int64_t)p.n_kv + cur.j) * kGroup + (rr & 3)) * kHeadDim +
+                                        d + (lane & 3) * 8) = w;
+          }
+          __syncwarp();
+        } else if (tok < g.n_tok) {
           store32(dst + d, o, inv);
+        }
       };
       uint32_t oa[32], ob[32];
       tc::ld32(tmem + lanes, oa);
@@ -349,66 +408,89 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
   }
 }
 
-// Join the partial states of the groups that a share's border cut: block
-// (share c, 8 rows of the group that begins in it and goes on), one row per
-// warp, eight dims per lane, the parts in CTA order, four parts' loads in
-// flight together.
-constexpr int kJoinRows = 8;
+// Join the partial states of the groups that a share's border cut, the parts
+// in CTA order: block (share c, 32 rows of the group that begins in it and
+// goes on).  Lane r has row r, warp w the dims 4 w + 32 i, so that the reads
+// are the partial states' lines; the rows then go through shared memory to be
+// written line by line.
+constexpr int kJoinRows = 32;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinDims = kHeadDim / 4 / kJoinWarps;  // float4 of a thread
+constexpr int kJoinStride = kHeadDim + 4;             // floats of a row in shared memory
 
 template <typename QT, int RANKS>
-__global__ void __launch_bounds__(32 * kJoinRows) k_paged_join(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_constant__ Args p) {
+  __shared__ float4 rows[kJoinRows * kJoinStride / 4];
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinRows + warp;
+  const int row0 = blockIdx.y * kJoinRows, row = row0 + lane;
   const paged::Join* jp = p.joins + c;
   const int4 a = __ldcg(reinterpret_cast<const int4*>(jp));  // row0, n_rows, head, last
-  if (row >= a.y) return;
+  if (row0 >= a.y) return;
   const longlong2 bt = __ldcg(reinterpret_cast<const longlong2*>(jp) + 1);  // begin, total
   const int G = __ldcg(&jp->G), last = a.w;
-  constexpr int kUnroll = 4;
-  float M = -INFINITY, L = 0.f, O[8];
+  constexpr int kAll = RANKS * kRows;
+  constexpr int kUnroll = 2;
+  float M = -INFINITY, L = 0.f;
+  float4 O[kJoinDims];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) O[i] = 0.f;
+  for (int i = 0; i < kJoinDims; ++i) O[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   // (the first part's slot depends on where the group begins, the others are
   // their CTAs' first)
   const int first = paged::partial_slot(c, bt.x, bt.y, G);
   for (int q0 = c; q0 <= last; q0 += kUnroll) {
     float m[kUnroll], l[kUnroll];
-    float4 x[kUnroll], y[kUnroll];
+    float4 x[kUnroll][kJoinDims];
 #pragma unroll
     for (int t = 0; t < kUnroll; ++t) {
       // (behind the last part the last once more, at weight 0: loads without
       // a condition stay in flight together)
       const int q = min(q0 + t, last), slot = q == c ? first : 2 * q;
       const float* part = p.part + (int64_t)slot * (RANKS * paged::kChunkPart);
-      m[t] = __ldcg(part + RANKS * kRows * kHeadDim + row);
-      l[t] = __ldcg(part + RANKS * kRows * (kHeadDim + 1) + row);
-      const float4* src = reinterpret_cast<const float4*>(part + row * kHeadDim + 8 * lane);
-      x[t] = __ldcg(src);
-      y[t] = __ldcg(src + 1);
+      m[t] = __ldcg(part + kAll * kHeadDim + row);
+      l[t] = __ldcg(part + kAll * (kHeadDim + 1) + row);
+#pragma unroll
+      for (int i = 0; i < kJoinDims; ++i)
+        x[t][i] = __ldcg(reinterpret_cast<const float4*>(part) + (warp + kJoinWarps * i) * kAll + row);
       if (q0 + t > last) m[t] = -INFINITY;
     }
 #pragma unroll
     for (int t = 0; t < kUnroll; ++t) {
       const float mn = fmaxf(M, m[t]);
+      // (a part in which the row saw nothing holds no state)
       const float s = M == -INFINITY ? 0.f : exp2f(M - mn), r = m[t] == -INFINITY ? 0.f : exp2f(m[t] - mn);
       M = mn;
       L = L * s + l[t] * r;
-      O[0] = O[0] * s + x[t].x * r; O[1] = O[1] * s + x[t].y * r; O[2] = O[2] * s + x[t].z * r;
-      O[3] = O[3] * s + x[t].w * r; O[4] = O[4] * s + y[t].x * r; O[5] = O[5] * s + y[t].y * r;
-      O[6] = O[6] * s + y[t].z * r; O[7] = O[7] * s + y[t].w * r;
+#pragma unroll
+      for (int i = 0; i < kJoinDims; ++i)
+        if (r != 0.f || s != 1.f) {
+          O[i].x = O[i].x * s + x[t][i].x * r;
+          O[i].y = O[i].y * s + x[t][i].y * r;
+          O[i].z = O[i].z * s + x[t][i].z * r;
+          O[i].w = O[i].w * s + x[t][i].w * r;
+        }
     }
   }
   const float inv = 1.0f / L;
-  QT* dst = static_cast<QT*>(p.a) + (((int64_t)a.x + (row >> 2)) * p.n_kv + a.z) * (kGroup * kHeadDim) +
-            (row & 3) * kHeadDim + 8 * lane;
-  if constexpr (std::is_same<QT, float>::value) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(O[0] * inv, O[1] * inv, O[2] * inv, O[3] * inv);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(O[4] * inv, O[5] * inv, O[6] * inv, O[7] * inv);
-  } else {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(O[0] * inv, O[1] * inv), pack2(O[2] * inv, O[3] * inv),
-                                                pack2(O[4] * inv, O[5] * inv), pack2(O[6] * inv, O[7] * inv));
+#pragma unroll
+  for (int i = 0; i < kJoinDims; ++i)
+    rows[lane * (kJoinStride / 4) + warp + kJoinWarps * i] =
+        make_float4(O[i].x * inv, O[i].y * inv, O[i].z * inv, O[i].w * inv);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinRows / kJoinWarps; ++i) {
+    const int r = warp + kJoinWarps * i;
+    if (row0 + r >= a.y) break;
+    const float4 x = rows[r * (kJoinStride / 4) + 2 * lane], y = rows[r * (kJoinStride / 4) + 2 * lane + 1];
+    QT* dst = static_cast<QT*>(p.a) + (((int64_t)a.x + ((row0 + r) >> 2)) * p.n_kv + a.z) * (kGroup * kHeadDim) +
+              ((row0 + r) & 3) * kHeadDim + 8 * lane;
+    if constexpr (std::is_same<QT, float>::value) {
+      reinterpret_cast<float4*>(dst)[0] = x;
+      reinterpret_cast<float4*>(dst)[1] = y;
+    } else {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+    }
   }
 }
 

@@ -19,10 +19,11 @@
 // MMAs release (slots, scores, output) they release in both CTAs.
 //
 // Measured, a chunk of 4096 tokens at 4096 (4.1e11 multiply-adds x 2): bf16
-// queries 249 us, 1650 TFLOP/s, 0.85 of the measured bf16 rate; fp32 queries
-// (two MMAs for each) 455 us, 906 TFLOP/s.  A tile takes 2190 cycles against
-// 2048 of MMA, the softmax 1850 beside it; the rest is the start, about 5 us a
-// group (queries, the last product, the output) and the join (11 us).
+// queries 226 us, 1820 TFLOP/s, 0.94 of the measured bf16 rate.  A tile takes
+// 2050 cycles against 2048 of MMA, the softmax 1850 beside it; the rest is the
+// start, the first and last tile of a group (its queries come by TMA, its
+// output leaves through a stage: with both done by the softmax threads row by
+// row it was 250 us) and the join.
 #include "paged_chunk_parts.cuh"
 
 namespace spark {
@@ -37,8 +38,9 @@ constexpr uint32_t kKLine = 64 * 128;  // 64 dims of the 64 positions a CTA hold
 // of one line is 2 KB, and TMA spends about 100 cycles on a request whatever
 // its size, which bounds bf16 chunks: a chunk of 4096 tokens at 4096 with
 // pages of 16 rows took 357 us, against 246 with pages of 128.  FOLD: tiles
-// are laid out box by box instead of line by line, [box][line][16 positions][128 bytes], and a box of all the slot's lines
-// is one request (8 KB of K, 4 of V): 285 us.  The MMAs want 8-position groups a fixed stride
+// are laid out box by box instead of line by line, [box][line][16
+// positions][128 bytes], and a box of all the slot's lines is one request
+// (8 KB of K, 4 of V): 285 us.  The MMAs want 8-position groups a fixed stride
 // apart: the boxes' first halves are (8 groups, half of the tile's columns),
 // and so are their second halves.  So a folded tile's column order is: the
 // first 8 positions of each box, then the last 8 of each.  fp32 queries take twice
@@ -66,13 +68,15 @@ __device__ __forceinline__ uint32_t v_step(int ks) {
 template <bool SPLIT>
 struct PairSmem {
   static constexpr int kQ = SPLIT ? 2 : 1;
-  // one V slot more than K slots: V has a hop more to the MMA
+  // (fp32 queries leave room for three slots: V, with a hop more to the MMA,
+  // gets two; a third for bf16 ones gave nothing, and the output's stage wants room)
   static constexpr int kK = SPLIT ? 1 : 2;
-  static constexpr int kV = SPLIT ? 2 : 3;
+  static constexpr int kV = 2;
   static constexpr uint32_t kRingK = kQ * kQBytes;
   static constexpr uint32_t kRingV = kRingK + kK * kSlot;
-  static constexpr uint32_t kBars = kRingV + kV * kSlot;
-  static constexpr uint32_t kBytes = kBars + 8 * (2 * kK + 3 * kV + 8) + 32;
+  static constexpr uint32_t kStage = kRingV + kV * kSlot;  // the output's, where there is room
+  static constexpr uint32_t kBars = kStage + (SPLIT ? 0 : 4 * kStageBytes);
+  static constexpr uint32_t kBytes = kBars + 8 * (2 * kK + 3 * kV + 9) + 32;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // slack to align the base (128-byte swizzle)
 };
 static_assert(PairSmem<true>::kAlloc <= 232448 && PairSmem<false>::kAlloc <= 232448, "227 KB per CTA");
@@ -135,10 +139,19 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int c0, int c1,
+                                                 int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 template <typename QT, bool FOLD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_paged_pair(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ Args p, int box_k, int box_v) {
+                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args p, int box_k, int box_v) {
   constexpr bool kSplit = std::is_same<QT, float>::value;
   using S = PairSmem<kSplit>;
   extern __shared__ unsigned char smem_raw[];
@@ -153,7 +166,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;       // [2] rank 0: P(i) is, in both CTAs
   uint64_t* pv_done = p_full + 2;      // [2] P(i) V(i) is in O
   uint64_t* q_full = pv_done + 2;      // rank 0: the queries are there, in both CTAs
-  uint64_t* drained = q_full + 1;      // rank 0: every MMA has completed
+  uint64_t* q_empty = q_full + 1;      // bf16: the group's last S is done
+  uint64_t* drained = q_empty + 1;     // rank 0: every MMA has completed
   volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] abort
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
 
@@ -177,12 +191,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[b], 2 * kSoft / 32);
       mbar_init(&pv_done[b], 1);
     }
-    mbar_init(q_full, 2 * kSoft / 32);
+    mbar_init(q_full, kSplit ? 2 * kSoft / 32 : 1);
+    mbar_init(q_empty, 1);
     mbar_init(drained, 1);
     flags[0] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
+    if (!kSplit) prefetch_tensormap(&tm_q);
   }
   // tables, lengths, rows and queries may come from the kernel before
   pdl_wait();
@@ -209,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---- producer: K(0), then K(i), V(i - 1) for the tiles of each group
-    uint32_t kk = 0, kv = 0;
+    uint32_t kk = 0, kv = 0, item = 0;
     bool ok = true;
     const int per_k = 64 / box_k, per_v = kPos / box_v;  // boxes of a half's keys, of a tile's values
     const int bk = lane % per_k, bv = lane % per_v;      // the lane's boxes
@@ -220,6 +236,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     for (;;) {
       const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
+      if (!kSplit) {
+        // the group's queries, once the group before has its last S
+        if (!freed(q_empty, item)) break;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(q_full, 2 * kQBytes);
+        __syncwarp();
+        if (lane < 4)
+          tma_load_3d_pair(base + lane * kLineBytes, &tm_q, in_rank0(q_full), 64 * lane, kGroup * cur.j,
+                           cur.seq.q0 + cur.g.tok + rank * paged::kChunkTokens);
+        ++item;
+      }
       const int lo = cur.g.lo, hi = cur.g.hi;
       auto pos_of = [&](int64_t u) { return (cur.g.tile0 + (int)(u - cur.begin)) * kPos; };
       // whether a box of `n` positions from `x` holds a row the group reads
@@ -291,6 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0)
         for (uint32_t i = kk > (uint32_t)S::kK ? kk - S::kK : 0; i < kk; ++i)
           mbar_wait_bounded(&k_full[i % S::kK], (i / S::kK) & 1, &never, kWaitLimitNs);
+      if (rank == 0 && item > 0) mbar_wait_bounded(q_full, (item - 1) & 1, &never, kWaitLimitNs);
       for (uint32_t i = kv > (uint32_t)S::kV ? kv - S::kV : 0; i < kv; ++i)
         mbar_wait_bounded(&v_here[i % S::kV], (i / S::kV) & 1, &never, kWaitLimitNs);
     }
@@ -388,7 +415,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0 && !both(q_full, item & 1)) break;
       ++item;
       for (int i = 0; i <= n && ok; ++i) {
-        if (rank == 0 && i < n) scores(tile + i);
+        if (rank == 0 && i < n) {
+          scores(tile + i);
+          if (!kSplit && i == n - 1 && ok && one) tc::commit_both(q_empty);
+        }
         if (i > 0 && ok) {
           const int pos = pos0 + (i - 1) * kPos;
           const int r0 = lo > pos ? lo - pos : 0, r1 = hi + 1 - pos < kPos ? hi + 1 - pos : kPos;
@@ -419,7 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const uint32_t q_bar = in_rank0(q_full), p_bar = in_rank0(p_full);
-    softmax_warps<QT, 2, FOLD>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, s_full, pv_done, flags, warp, tid - 64,
+    softmax_warps<QT, 2, FOLD, !kSplit>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, s_full, pv_done, flags,
+                                        base + S::kStage, warp, tid - 64,
                          [&] { arrive_at(q_bar); }, [&](uint32_t buf) { arrive_tmem_at(p_bar + 8 * buf); });
   }
   tc::fence_before();
@@ -439,15 +470,18 @@ cudaError_t launch_pair(const Args& p, const void* k, const void* v, int box_k, 
   if (!make_chunk_map(&mk, k, p.n_kv, rows, box_k, FOLD ? 4 : 1) ||
       !make_chunk_map(&mv, v, p.n_kv, rows, box_v, FOLD ? 2 : 1))
     return cudaErrorInvalidValue;
+  CUtensorMap mq = mk;  // (unused: fp32 queries are split by the kernel)
+  if (std::is_same<QT, __nv_bfloat16>::value && !make_query_map(&mq, p.q, p.q_ld, kGroup * p.n_kv, p.n_tokens))
+    return cudaErrorInvalidValue;
   auto kern = k_paged_pair<QT, FOLD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
   if (e != cudaSuccess) return e;
   int pairs = device_sm_count() / 2;
   if (pairs > paged::kMaxChunkCtas / 2) pairs = paged::kMaxChunkCtas / 2;
   if (pairs < 1) pairs = 1;
-  e = launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), S::kAlloc, st, mk, mv, p, box_k, box_v);
+  e = launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), S::kAlloc, st, mk, mv, mq, p, box_k, box_v);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_join<QT, 2>, dim3(pairs, 2 * kRows / kJoinRows), dim3(32 * kJoinRows), 0, st, p);
+  return launch_pdl(k_paged_join<QT, 2>, dim3(pairs, 2 * kRows / kJoinRows), dim3(32 * kJoinWarps), 0, st, p);
 }
 
 }  // namespace
