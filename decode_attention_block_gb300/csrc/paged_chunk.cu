@@ -20,8 +20,8 @@
 // its own S, 32 positions at a time (hi in the first 16 of their columns, lo
 // in the others).  Shared memory: Q (64 KB, 128 KB in two halves) and a ring
 // of 32 KB slots, each 128 positions x 128 dims of K or V.  Warp 0 fills the
-// ring (TMA boxes of the part of a page inside the tile) and loads bf16
-// queries (fp32 ones are split by warps 2-5), warp 1 issues the MMAs in the
+// ring (TMA boxes of the part of a page inside the tile) and loads the
+// queries (fp32 ones are put in halves by warps 2-5), warp 1 issues the MMAs in the
 // order S(i+1), P V(i), so the tensor cores run S(i+1) while warps 2-5 turn
 // S(i) into P(i).
 //
@@ -50,10 +50,11 @@ static_assert(kRows == kGroup * paged::kChunkTokens, "a row per query head of a 
 template <bool SPLIT>
 struct ChunkSmem {
   static constexpr int kQ = SPLIT ? 2 : 1;
+  static constexpr uint32_t kQLine = kQ * kLineBytes;  // a line of the queries, with that of the remainders
   static constexpr int kSlots = SPLIT ? 3 : 5;
   static constexpr uint32_t kRing = kQ * kQBytes;
   static constexpr uint32_t kBars = kRing + kSlots * kSlot;
-  static constexpr uint32_t kBytes = kBars + 8 * (2 * kSlots + 9) + 32;
+  static constexpr uint32_t kBytes = kBars + 8 * (2 * kSlots + 10) + 32;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // slack to align the base (128-byte swizzle)
 };
 static_assert(ChunkSmem<true>::kAlloc <= 232448 && ChunkSmem<false>::kAlloc <= 232448, "227 KB per CTA");
@@ -61,7 +62,8 @@ static_assert(ChunkSmem<true>::kAlloc <= 232448 && ChunkSmem<false>::kAlloc <= 2
 template <typename QT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args p, int box) {
+                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q8,
+                  const __grid_constant__ Args p, int box) {
   constexpr bool kSplit = std::is_same<QT, float>::value;
   using S = ChunkSmem<kSplit>;
   constexpr int NS = S::kSlots;
@@ -74,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;   // [2] P(i) is
   uint64_t* pv_done = p_full + 2;  // [2] P(i) V(i) is in O (one per buffer: a thread waits for each phase, none is skipped)
   uint64_t* q_full = pv_done + 2;
-  uint64_t* q_empty = q_full + 1;  // bf16: the group's last S is done
+  uint64_t* q_raw = q_full + 1;    // fp32: they are, not yet in halves
+  uint64_t* q_empty = q_raw + 1;   // the group's last S is done
   uint64_t* drained = q_empty + 1;  // every MMA has completed
   volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] abort
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
@@ -94,13 +97,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[b], 1);
     }
     mbar_init(q_full, kSplit ? kSoft / 32 : 1);
+    mbar_init(q_raw, 1);
     mbar_init(q_empty, 1);
     mbar_init(drained, 1);
     flags[0] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
-    if (!kSplit) prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_q8);
   }
   // tables, lengths, rows and queries may come from the kernel before
   pdl_wait();
@@ -128,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- producer: K(0), then K(i), V(i - 1) for the tiles of each group
     uint32_t k = 0, item = 0;
     bool ok = true;
+    uint64_t* q_here = kSplit ? q_raw : q_full;
     const int per = kPos / box;  // boxes of a tile
     auto slot = [&](const CUtensorMap* map, int half, int z, int b0, int b1) {
       const int s = (int)(k % NS);
@@ -149,17 +155,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (;;) {
       const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
-      if (!kSplit) {
-        // the group's queries, once the group before has its last S
-        if (item > 0 && !mbar_wait_bounded(q_empty, (item - 1) & 1, flags, kWaitLimitNs)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, kQBytes);
-        __syncwarp();
-        if (lane < 4)
-          tma_load_3d(base + lane * kLineBytes, &tm_q, q_full, 64 * lane, kGroup * cur.j, cur.seq.q0 + cur.g.tok);
-        ++item;
-      }
+      // the group's queries, once the group before has its last S
+      if (item > 0 && !mbar_wait_bounded(q_empty, (item - 1) & 1, flags, kWaitLimitNs)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(q_here, query_bytes<QT>(cur.g.n_tok, 0));
+      __syncwarp();
+      load_queries<QT>(base, &tm_q, &tm_q8, cur, 0, lane,
+                       [&](const CUtensorMap* map, void* to, int head, int tok, int line) {
+                         tma_load_4d(to, map, q_here, 0, head, tok, line);
+                       });
+      ++item;
       // the boxes [b0, b1) of tile u that hold rows the group reads; the table's
       // entry for the lane's box, asked for one tile ahead
       auto boxes = [&](int64_t u, int& pos, int& b0, int& b1) {
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int never = 0;
       for (uint32_t i = k > (uint32_t)NS ? k - NS : 0; i < k; ++i)
         mbar_wait_bounded(&full[i % NS], (i / NS) & 1, &never, kWaitLimitNs);
-      if (item > 0) mbar_wait_bounded(q_full, (item - 1) & 1, &never, kWaitLimitNs);
+      if (item > 0) mbar_wait_bounded(q_here, (item - 1) & 1, &never, kWaitLimitNs);
     }
   } else if (warp == 1) {
     // ---- MMA issuer (one elected lane); the whole warp clears the rows of V tiles that
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int half = 0; half < 2; ++half, ++k) {
         const int s = (int)(k % NS);
         if (!wait(&full[s], (k / NS) & 1)) return;
-        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot), a0 = tc::desc_k_major(q_addr + 2 * half * kLineBytes);
+        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot), a0 = tc::desc_k_major(q_addr + 2 * half * S::kQLine);
         if (one) {
 #pragma unroll
           for (int line = 0; line < 2; ++line)
@@ -234,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                tc::mma_ss(d, a0 + ((part * kQBytes + line * kLineBytes) >> 4) + 2 * ks,
+                tc::mma_ss(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
                            b0 + (line * kLineBytes >> 4) + 2 * ks, kIdS, half + line + part + ks > 0);
           tc::commit(&empty[s]);
           if (half == 1) tc::commit(&s_full[i & 1]);
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++item;
       for (int i = 0; i <= n && ok; ++i) {
         if (i < n) scores(tile + i);
-        if (!kSplit && i == n - 1 && ok && one) tc::commit(q_empty);
+        if (i == n - 1 && ok && one) tc::commit(q_empty);
         if (i > 0 && ok) {
           const int pos = pos0 + (i - 1) * kPos;
           values(tile + i - 1, i == 1, lo > pos ? lo - pos : 0, hi + 1 - pos < kPos ? hi + 1 - pos : kPos);
@@ -305,9 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    softmax_warps<QT, 1, false, false>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, s_full, pv_done, flags, nullptr, warp,
-                                       tid - 64,
-                         [&] { mbar_arrive(q_full); }, [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
+    softmax_warps<QT, 1, false, false>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, q_raw, s_full, pv_done, flags, nullptr,
+                                       warp, tid - 64, [&] { mbar_arrive(q_full); }, [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
   }
   tc::fence_before();
   __syncthreads();
@@ -326,15 +331,14 @@ cudaError_t launch_chunk(const Args& p, const void* k, const void* v, cudaStream
   const int64_t rows = (int64_t)p.n_pages * p.page_size;
   if (!make_chunk_map(&mk, k, p.n_kv, rows, box, 1) || !make_chunk_map(&mv, v, p.n_kv, rows, box, 1))
     return cudaErrorInvalidValue;
-  CUtensorMap mq = mk;  // (unused: fp32 queries are split by the kernel)
-  if (std::is_same<QT, __nv_bfloat16>::value && !make_query_map(&mq, p.q, p.q_ld, kGroup * p.n_kv, p.n_tokens))
-    return cudaErrorInvalidValue;
+  CUtensorMap mq, mq8;
+  if (!make_query_maps<QT>(&mq, &mq8, p)) return cudaErrorInvalidValue;
   auto kern = k_paged_chunk<QT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
   if (e != cudaSuccess) return e;
   int grid = device_sm_count();
   if (grid > paged::kMaxChunkCtas) grid = paged::kMaxChunkCtas;
-  e = launch_pdl(kern, dim3(grid), dim3(kThreads), S::kAlloc, st, mk, mv, mq, p, box);
+  e = launch_pdl(kern, dim3(grid), dim3(kThreads), S::kAlloc, st, mk, mv, mq, mq8, p, box);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_paged_join<QT, 1>, dim3(grid, kRows / kJoinRows), dim3(32 * kJoinWarps), 0, st, p);
 }

@@ -32,15 +32,6 @@ constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
 constexpr int kMinTiles = 2;                    // tiles per CTA at least
 
-// 3-D tiled TMA load global -> shared, completing on `bar` (byte count).
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -65,53 +56,81 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// fp32 queries of 32 tokens of the group, from its token `tok0`, into shared
-// memory as bf16 halves: 64-dim lines of 128 rows, 16-byte chunk c of row r at
-// c ^ (r % 8) (the 128-byte swizzle).  Rows behind the last token are zero or
-// stay what they are: their scores reach no other row, and nothing is written
-// for them.
-__device__ __forceinline__ void load_queries(unsigned char* q_s, const Args& p, const Cursor& cur, int tok0, int tid) {
-  const float* q = static_cast<const float*>(p.q) + (int64_t)cur.j * kGroup * kHeadDim;
-  const int64_t row0 = cur.seq.q0 + cur.g.tok + tok0;
-  constexpr int kBatch = 8;  // rows in flight per warp
-  const int rows = min(kRows, 4 * (cur.g.n_tok - tok0));
-  const int ch = tid & 31;
-  for (int r0 = tid >> 5; r0 < rows; r0 += 4 * kBatch) {
-    float4 v[kBatch][2];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + 4 * i;
-      const float4* src = reinterpret_cast<const float4*>(q + (row0 + (r >> 2)) * p.q_ld + (r & 3) * kHeadDim + 8 * ch);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) v[i][k] = r < rows ? __ldcg(src + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + 4 * i;
-      const uint32_t at = (uint32_t)(ch >> 3) * kLineBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-      const float x[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-      uint4 hi, lo;
-      split8(x, hi, lo);
-      *reinterpret_cast<uint4*>(q_s + at) = hi;
-      *reinterpret_cast<uint4*>(q_s + kQBytes + at) = lo;
-    }
+// Queries in shared memory: 64-dim lines of 128 rows, 16-byte chunk c of row r
+// at c ^ (r % 8) (the 128-byte swizzle).  TMA brings them, bf16 as they are
+// used, fp32 in 32-dim lines, which the softmax warps turn into a line of bf16
+// halves and a line of remainders in the same place.  (Read by the warps 8
+// rows at a time instead, they took 5 us at the start and 3 to 6 at each later
+// group.)  More than 16 tokens come in one request of 32 with all lines, fewer
+// in requests of a line of 8.  Rows behind the group's last token are other
+// tokens', zero or what they were: their scores reach no other row, and
+// nothing is written for them.
+constexpr int kQueryBoxTokens = 8;
+constexpr int kQueryBoxes = paged::kChunkTokens / kQueryBoxTokens;
+constexpr uint32_t kQueryBox = kQueryBoxTokens * kGroup * 128;  // bytes
+template <typename QT>
+constexpr int kQueryLines = kHeadDim * sizeof(QT) / 128;
+
+// 8-token boxes of a line that hold tokens of the group, of the 32 from `tok0`
+__device__ __forceinline__ int query_boxes(int n_tok, int tok0) {
+  return min(kQueryBoxes, max(0, (n_tok - tok0 + kQueryBoxTokens - 1) / kQueryBoxTokens));
+}
+template <typename QT>
+__device__ __forceinline__ uint32_t query_bytes(int n_tok, int tok0) {
+  const int n = query_boxes(n_tok, tok0);
+  return (n > kQueryBoxes / 2 ? kQueryBoxes : n) * (kQueryLines<QT> * kQueryBox);
+}
+// a warp loads them: load(map, to, head, token, line)
+template <typename QT, typename Load>
+__device__ __forceinline__ void load_queries(unsigned char* q_s, const CUtensorMap* all, const CUtensorMap* box,
+                                             const Cursor& cur, int tok0, int lane, Load load) {
+  const int n = query_boxes(cur.g.n_tok, tok0), head = kGroup * cur.j, tok = cur.seq.q0 + cur.g.tok + tok0;
+  if (n > kQueryBoxes / 2) {
+    if (lane == 0) load(all, q_s, head, tok, 0);
+  } else {
+    const int line = lane % kQueryLines<QT>, b = lane / kQueryLines<QT>;
+    if (b < n) load(box, q_s + line * kLineBytes + b * kQueryBox, head, tok + kQueryBoxTokens * b, line);
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
 }
 
-// bf16 queries as TMA loads them into the same layout: a box is one 64-dim
-// line of 4 heads of 32 tokens.  Rows behind the tensor are zero, rows behind
-// the group's last token those of other tokens.
-inline bool make_query_map(CUtensorMap* map, const void* q, int64_t q_ld, int n_q, int n_tokens) {
+// row r of fp32 queries into halves, in place: its 256 bytes in lines 2 i and
+// 2 i + 1 become those of line i of the halves and of the remainders
+__device__ __forceinline__ void split_query(unsigned char* q_s, int i, int r) {
+  unsigned char* row = q_s + 2 * i * kLineBytes + r * 128;
+  float4 x[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    x[c] = *reinterpret_cast<const float4*>(row + (c >> 3) * kLineBytes + (((c & 7) ^ (r & 7)) << 4));
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float v[8] = {x[2 * c].x,     x[2 * c].y,     x[2 * c].z,     x[2 * c].w,
+                        x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) = hi;
+    *reinterpret_cast<uint4*>(row + kLineBytes + ((c ^ (r & 7)) << 4)) = lo;
+  }
+}
+
+// rows [token][head][256] as [line][token][head][128 bytes]
+template <typename QT>
+bool make_query_map(CUtensorMap* map, const Args& p, int tokens, int lines) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)n_q, (cuuint64_t)n_tokens};
-  const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)q_ld * 2};
-  const cuuint32_t shape[3] = {64, kGroup, paged::kChunkTokens};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, shape, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  constexpr cuuint64_t es = sizeof(QT);
+  const cuuint64_t dims[4] = {128 / es, (cuuint64_t)(kGroup * p.n_kv), (cuuint64_t)p.n_tokens, kQueryLines<QT>};
+  const cuuint64_t strides[3] = {kHeadDim * es, (cuuint64_t)p.q_ld * es, 128};
+  const cuuint32_t shape[4] = {128 / es, kGroup, (cuuint32_t)tokens, (cuuint32_t)lines};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(p.q), dims, strides, shape, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <typename QT>
+bool make_query_maps(CUtensorMap* all, CUtensorMap* box, const Args& p) {
+  return make_query_map<QT>(all, p, paged::kChunkTokens, kQueryLines<QT>) &&
+         make_query_map<QT>(box, p, kQueryBoxTokens, 1);
 }
 
 // The seen-bits of a folded tile's columns (paged_pair.cu), from those of its
@@ -197,17 +216,17 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[
 // The four softmax warps (st: their thread, 0 .. 127) of a CTA of RANKS that
 // share a group, one row per thread: scores to probabilities, the running
 // maximum and sum, the output at the group's end.  arrive_q, arrive_p: one
-// lane per warp tells the MMA warp that fp32 queries (bf16 ones come by TMA),
-// or the probabilities in a buffer, are there.  FOLD: the tiles' columns are in a folded order.
+// lane per warp tells the MMA warp that fp32 queries are in halves, or the
+// probabilities in a buffer.  FOLD: the tiles' columns are in a folded order.
+// STAGE: whole groups' outputs leave through `stage`.
 constexpr int kStageRow = 64 + 16;             // bytes of a row of an output stage: 32 bf16 dims, padding
 constexpr int kStageBytes = 32 * kStageRow;    // of a warp
 
 template <typename QT, int RANKS, bool FOLD, bool STAGE, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
-                                              uint64_t* s_full, uint64_t* pv_done, volatile int* flags, unsigned char* stage,
-                                              int warp, int st,
-                                              ArriveQ arrive_q, ArriveP arrive_p) {
+                                              uint64_t* q_raw, uint64_t* s_full, uint64_t* pv_done,
+                                              volatile int* flags, unsigned char* stage, int warp, int st, ArriveQ arrive_q, ArriveP arrive_p) {
   const int quad = warp & 3, lane = st & 31, tok0 = rank * paged::kChunkTokens;
   const int row = quad * 32 + lane;
   const int prow = rank * kRows + row;  // the row in a partial state
@@ -225,11 +244,17 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     tc::fence_after();
     return ok;
   };
-  if (kSplit) {
-    load_queries(q_s, p, cur, tok0, st);
+  // fp32 queries have landed: into halves
+  uint32_t item = 0;
+  auto split_queries = [&](const Cursor& at) {
+    if (!wait(q_raw, item++ & 1)) return;
+#pragma unroll 1
+    for (int b = 0; b < query_boxes(at.g.n_tok, tok0); ++b) split_query(q_s, quad, 32 * b + lane);  // a line per warp
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
     __syncwarp();
     if (lane == 0) arrive_q();
-  }
+  };
+  if (kSplit) split_queries(cur);
   for (;;) {
     const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
     const paged::Group g = cur.g;
@@ -312,17 +337,12 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       if (lane == 0) arrive_p(buf);
     }
     if (!ok) break;
-    // Q is free (the last S is done): the next group's fp32 queries load while
-    // this one's last product runs
+    // (the next group's fp32 queries are split while this one's last product runs)
     Cursor nxt = cur;
     const bool more = cur.end < u1;
     if (more) {
       nxt.next(p, sh);
-      if (kSplit) {
-        load_queries(q_s, p, nxt, tok0, st);
-        __syncwarp();
-        if (lane == 0) arrive_q();
-      }
+      if (kSplit) split_queries(nxt);
     }
     if (!wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) break;
     const bool split = cur.begin < u0 || cur.end > u1;

@@ -68,6 +68,7 @@ __device__ __forceinline__ uint32_t v_step(int ks) {
 template <bool SPLIT>
 struct PairSmem {
   static constexpr int kQ = SPLIT ? 2 : 1;
+  static constexpr uint32_t kQLine = kQ * kLineBytes;  // a line of the queries, with that of the remainders
   // (fp32 queries leave room for three slots: V, with a hop more to the MMA,
   // gets two; a third for bf16 ones gave nothing, and the output's stage wants room)
   static constexpr int kK = SPLIT ? 1 : 2;
@@ -76,7 +77,7 @@ struct PairSmem {
   static constexpr uint32_t kRingV = kRingK + kK * kSlot;
   static constexpr uint32_t kStage = kRingV + kV * kSlot;  // the output's, where there is room
   static constexpr uint32_t kBars = kStage + (SPLIT ? 0 : 4 * kStageBytes);
-  static constexpr uint32_t kBytes = kBars + 8 * (2 * kK + 3 * kV + 9) + 32;
+  static constexpr uint32_t kBytes = kBars + 8 * (2 * kK + 3 * kV + 10) + 32;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // slack to align the base (128-byte swizzle)
 };
 static_assert(PairSmem<true>::kAlloc <= 232448 && PairSmem<false>::kAlloc <= 232448, "227 KB per CTA");
@@ -139,19 +140,11 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int c0, int c1,
-                                                 int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 template <typename QT, bool FOLD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_paged_pair(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args p, int box_k, int box_v) {
+                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q8,
+                 const __grid_constant__ Args p, int box_k, int box_v) {
   constexpr bool kSplit = std::is_same<QT, float>::value;
   using S = PairSmem<kSplit>;
   extern __shared__ unsigned char smem_raw[];
@@ -166,7 +159,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;       // [2] rank 0: P(i) is, in both CTAs
   uint64_t* pv_done = p_full + 2;      // [2] P(i) V(i) is in O
   uint64_t* q_full = pv_done + 2;      // rank 0: the queries are there, in both CTAs
-  uint64_t* q_empty = q_full + 1;      // bf16: the group's last S is done
+  uint64_t* q_raw = q_full + 1;        // fp32: this CTA's are, not yet in halves
+  uint64_t* q_empty = q_raw + 1;       // the group's last S is done
   uint64_t* drained = q_empty + 1;     // rank 0: every MMA has completed
   volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] abort
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
@@ -192,13 +186,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[b], 1);
     }
     mbar_init(q_full, kSplit ? 2 * kSoft / 32 : 1);
+    mbar_init(q_raw, 1);
     mbar_init(q_empty, 1);
     mbar_init(drained, 1);
     flags[0] = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
-    if (!kSplit) prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_q8);
   }
   // tables, lengths, rows and queries may come from the kernel before
   pdl_wait();
@@ -236,16 +232,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     for (;;) {
       const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
-      if (!kSplit) {
-        // the group's queries, once the group before has its last S
-        if (!freed(q_empty, item)) break;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(q_full, 2 * kQBytes);
-        __syncwarp();
-        if (lane < 4)
-          tma_load_3d_pair(base + lane * kLineBytes, &tm_q, in_rank0(q_full), 64 * lane, kGroup * cur.j,
-                           cur.seq.q0 + cur.g.tok + rank * paged::kChunkTokens);
-        ++item;
+      // the group's queries, once the group before has its last S: fp32 ones on
+      // each CTA's barrier, the bytes of bf16 ones in both on that of rank 0
+      if (!freed(q_empty, item)) break;
+      const int tok0 = rank * paged::kChunkTokens;
+      if (lane == 0) {
+        if (kSplit)
+          mbar_arrive_expect_tx(q_raw, query_bytes<QT>(cur.g.n_tok, tok0));
+        else if (rank == 0)
+          mbar_arrive_expect_tx(q_full, query_bytes<QT>(cur.g.n_tok, 0) + query_bytes<QT>(cur.g.n_tok, paged::kChunkTokens));
       }
+      __syncwarp();
+      load_queries<QT>(base, &tm_q, &tm_q8, cur, tok0, lane,
+                       [&](const CUtensorMap* map, void* to, int head, int tok, int line) {
+                         if (kSplit)
+                           tma_load_4d(to, map, q_raw, 0, head, tok, line);
+                         else
+                           tma_load_4d_pair(to, map, in_rank0(q_full), 0, head, tok, line);
+                       });
+      ++item;
       const int lo = cur.g.lo, hi = cur.g.hi;
       auto pos_of = [&](int64_t u) { return (cur.g.tile0 + (int)(u - cur.begin)) * kPos; };
       // whether a box of `n` positions from `x` holds a row the group reads
@@ -317,7 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rank == 0)
         for (uint32_t i = kk > (uint32_t)S::kK ? kk - S::kK : 0; i < kk; ++i)
           mbar_wait_bounded(&k_full[i % S::kK], (i / S::kK) & 1, &never, kWaitLimitNs);
-      if (rank == 0 && item > 0) mbar_wait_bounded(q_full, (item - 1) & 1, &never, kWaitLimitNs);
+      if ((kSplit || rank == 0) && item > 0)
+        mbar_wait_bounded(kSplit ? q_raw : q_full, (item - 1) & 1, &never, kWaitLimitNs);
       for (uint32_t i = kv > (uint32_t)S::kV ? kv - S::kV : 0; i < kv; ++i)
         mbar_wait_bounded(&v_here[i % S::kV], (i / S::kV) & 1, &never, kWaitLimitNs);
     }
@@ -369,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                  tc::mma_ss2(d + h * (kPos / 2), a0 + ((part * kQBytes + line * kLineBytes) >> 4) + 2 * ks,
+                  tc::mma_ss2(d + h * (kPos / 2), a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
                               b0 + ((line * kBoxLine + h * 1024) >> 4) + 2 * ks, kIdFold, line + part + ks > 0);
         } else {
 #pragma unroll
@@ -378,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                tc::mma_ss2(d, a0 + ((part * kQBytes + line * kLineBytes) >> 4) + 2 * ks,
+                tc::mma_ss2(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
                             b0 + (line * kKLine >> 4) + 2 * ks, kIdS, line + part + ks > 0);
         }
         tc::commit_both(&k_empty[s]);
@@ -417,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i <= n && ok; ++i) {
         if (rank == 0 && i < n) {
           scores(tile + i);
-          if (!kSplit && i == n - 1 && ok && one) tc::commit_both(q_empty);
+          if (i == n - 1 && ok && one) tc::commit_both(q_empty);
         }
         if (i > 0 && ok) {
           const int pos = pos0 + (i - 1) * kPos;
@@ -449,9 +455,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const uint32_t q_bar = in_rank0(q_full), p_bar = in_rank0(p_full);
-    softmax_warps<QT, 2, FOLD, !kSplit>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, s_full, pv_done, flags,
-                                        base + S::kStage, warp, tid - 64,
-                         [&] { arrive_at(q_bar); }, [&](uint32_t buf) { arrive_tmem_at(p_bar + 8 * buf); });
+    softmax_warps<QT, 2, FOLD, !kSplit>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, q_raw, s_full, pv_done, flags,
+                                        base + S::kStage, warp, tid - 64, [&] { arrive_at(q_bar); },
+                                        [&](uint32_t buf) { arrive_tmem_at(p_bar + 8 * buf); });
   }
   tc::fence_before();
   __syncthreads();
@@ -470,16 +476,15 @@ cudaError_t launch_pair(const Args& p, const void* k, const void* v, int box_k, 
   if (!make_chunk_map(&mk, k, p.n_kv, rows, box_k, FOLD ? 4 : 1) ||
       !make_chunk_map(&mv, v, p.n_kv, rows, box_v, FOLD ? 2 : 1))
     return cudaErrorInvalidValue;
-  CUtensorMap mq = mk;  // (unused: fp32 queries are split by the kernel)
-  if (std::is_same<QT, __nv_bfloat16>::value && !make_query_map(&mq, p.q, p.q_ld, kGroup * p.n_kv, p.n_tokens))
-    return cudaErrorInvalidValue;
+  CUtensorMap mq, mq8;
+  if (!make_query_maps<QT>(&mq, &mq8, p)) return cudaErrorInvalidValue;
   auto kern = k_paged_pair<QT, FOLD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
   if (e != cudaSuccess) return e;
   int pairs = device_sm_count() / 2;
   if (pairs > paged::kMaxChunkCtas / 2) pairs = paged::kMaxChunkCtas / 2;
   if (pairs < 1) pairs = 1;
-  e = launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), S::kAlloc, st, mk, mv, mq, p, box_k, box_v);
+  e = launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), S::kAlloc, st, mk, mv, mq, mq8, p, box_k, box_v);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_paged_join<QT, 2>, dim3(pairs, 2 * kRows / kJoinRows), dim3(32 * kJoinWarps), 0, st, p);
 }
