@@ -4,11 +4,10 @@
  * attention block on a paged cache, for NVIDIA GB300 (sm_103a).  Same library
  * and conventions as spark_attn.h (device pointers owned by the caller,
  * 16-byte aligned, int32 arrays 4-byte; work enqueued on `stream`; SPARK_OK
- * or a negative spark_status; the current device is the pointers').  The
- * source pages of
- * turbospark-runtime 0.3.0 have no counterpart: its cache is one contiguous
- * slot range per sequence (src/kv_write.rs).  The attention is that of
- * spark_attn.h: query head h reads KV head h / (n_q / n_kv), scale
+ * or a negative spark_status; the current device is the pointers').  Pages
+ * have no counterpart in turbospark-runtime 0.3.0, whose cache is one
+ * contiguous slot range per sequence (src/kv_write.rs).  The attention is
+ * that of spark_attn.h: query head h reads KV head h / (n_q / n_kv), scale
  * `geom.scale`, causal over the whole history (SPARK_FULL) or the last
  * `geom.window` positions (SPARK_SLIDING).
  *
@@ -58,7 +57,8 @@ typedef struct spark_page_pool {
 /* The sequences of a call.  Sequence s brings the q_start[s + 1] - q_start[s]
  * new tokens (none is allowed) in rows q_start[s] .. q_start[s + 1] - 1 of
  * the call's q, k, v and output; they are the last of its seq_len[s]
- * positions.  Rows at or behind q_start[n_seqs] are not read or written.
+ * positions.  Rows at or behind q_start[n_seqs] are not written, and what is in
+ * them reaches no result.
  *   table    device [n_seqs][max_pages] int32.  Entries of pages that hold
  *            no position the call reads or writes may be anything.
  *   q_start  device [n_seqs + 1] int32, not decreasing, from >= 0.

@@ -227,6 +227,28 @@ def test_strided_queries_and_padded_rows(B):
         _check_attention(B, Case(SETS["mixed"], page=64, seed=4, pad=37), q_type, q_pad=2048 + 8, max_q=200)
 
 
+@pytest.mark.parametrize("q_type", [F32, BF16])
+@pytest.mark.parametrize("name", ["verify", "mixed", "edges"])
+def test_queries_of_other_sequences_do_not_matter(B, name, q_type):
+    """Rows of NaN queries (padding, and every second sequence) next to
+    others in a tile: the others' results are bit for bit what they were."""
+    case = Case(SETS[name], page=32, seed=12, pad=29)
+    g, ws = _geom(B), B.make_paged_workspace(_geom(B))
+    case.fill()
+    q = torch.randn(case.n_tokens, 4096, generator=case.g, device="cuda").to(q_type)
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    pool = B.PagePool(case.k, case.v)
+    B.spark_paged_attention(g, q, pool, B.SPARK_FULL, case.batch(B), a, ws)
+    kept = torch.zeros(case.n_tokens, dtype=torch.bool, device="cuda")
+    starts = case.q_start.tolist()
+    for s in range(0, len(case.seqs), 2):
+        kept[starts[s]:starts[s + 1]] = True
+    q[~kept] = float("nan")
+    B.spark_paged_attention(g, q, pool, B.SPARK_FULL, case.batch(B), b, ws)
+    assert B.spark_attn_error_word(ws) == 0
+    assert torch.equal(a[kept], b[kept]) and bool(torch.isfinite(a).all())
+
+
 def test_many_sequences(B):
     r = np.random.default_rng(2)
     seqs = [(int(c), int(min(c, n))) for c, n in zip(r.integers(0, 90, 1024), r.integers(0, 3, 1024))]
