@@ -475,22 +475,20 @@ cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype,
   // fp32 pools, and single tokens, a token at a time
   if (cdtype != SPARK_BF16 || p.max_q == 1) return launch_paged_token(p, qdtype, cdtype, k, v, st);
   if (p.max_q <= paged::kChunkTokens) return launch_paged_chunk(p, qdtype, k, v, st);
-  // Longer chunks take pairs of CTAs.  In a mixed batch the sequences of up to
-  // 32 new tokens go to the single-CTA kernel, where they do not leave half
-  // of a pair's rows empty (32 sequences, 4 of them with chunks of ~400
-  // tokens, fp32 queries: pairs alone 311 us, single CTAs alone 230 us, both
-  // 213 us).  Where the average is above half of the longest, most sequences
-  // are long, and a second kernel for the rest would mostly find nothing to
-  // do (three of 100 tokens at 800:
-  // 35 us with both, 29 us with pairs alone).
-  if (p.n_seqs == 1 || 2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q) return launch_paged_pair(p, qdtype, k, v, st);
-  paged::Args a = p;
-  a.from = paged::kChunkTokens + 1;
-  const cudaError_t e = launch_paged_pair(a, qdtype, k, v, st);
-  if (e != cudaSuccess) return e;
-  a.from = 1;
-  a.to = paged::kChunkTokens;
-  return launch_paged_chunk(a, qdtype, k, v, st);
+  // Longer chunks take pairs of CTAs, which read 64 tokens' rows once: where
+  // most sequences are long (the average above half of the longest: 32 of 33
+  // tokens at 4096-8192, bf16 queries, 169 us against 257 on single CTAs), or
+  // where the long ones are most of the work (above 128 tokens a sequence on
+  // average: 8 sequences, one of them with a chunk of 3100 tokens, 112 against
+  // 142 us).  In other batches the short sequences would leave most of a
+  // pair's rows empty, and single CTAs take them all (32 sequences, 4 of them
+  // with chunks of ~400 tokens: 137 against 165 us; fp32 queries 197 against
+  // 245).  Each kind on the kernel that suits it, one after the other, came
+  // to 155 and 200 us there, and to twice as long for 8 sequences with one
+  // chunk of 100: the two kernels' starts and ends add up.
+  const int64_t T = p.n_tokens, S = p.n_seqs;
+  if (2 * T > S * p.max_q || T > 128 * S) return launch_paged_pair(p, qdtype, k, v, st);
+  return launch_paged_chunk(p, qdtype, k, v, st);
 }
 
 cudaError_t launch_paged_append(const paged::Args& p, int xdtype, int cdtype, const void* k, const void* v, int64_t ld,

@@ -76,8 +76,6 @@ inline paged::Args paged_args(const spark_geom* g, const spark_page_pool* pool, 
   p.max_pages = b->max_pages;
   p.n_tokens = b->n_tokens;
   p.max_q = b->max_q_len;
-  p.from = 0;
-  p.to = b->max_q_len;
   p.n_pages = (int32_t)pool->n_pages;
   p.page_size = pool->page_size;
   p.page_mul = paged::page_mul(pool->page_size);

@@ -30,9 +30,10 @@
 // in CTA order by k_paged_join.
 //
 // This kernel takes chunks of up to 32 tokens, which are bound by the rows
-// read from HBM (32 sequences at 4096-8192, 0.82 GB: 4 tokens each 132 us,
-// 6.2 TB/s; 32 tokens 158 us, 5.3 TB/s, 658 TFLOP/s); longer ones are bound
-// by what a CTA alone takes in from L2, and go to paged_pair.cu.  What it
+// read from HBM (32 sequences at 4096-8192, 0.82 GB, bf16 queries: 4 tokens
+// each 136 us, 6.0 TB/s; 32 tokens 147 us, 5.6 TB/s, 707 TFLOP/s), and batches
+// with few longer ones; many longer ones are bound by what a CTA alone takes
+// in from L2, and go to paged_pair.cu.  What it
 // cost on the way (a chunk of 4096 tokens at 4096): 128 columns unrolled in
 // the softmax missed the instruction cache, 566 us; operands of an MMA moved
 // to uniform registers one by one, 361 -> 335; scores read twice, 335 -> 330;

@@ -1,5 +1,5 @@
 // paged_pair.cu -- the chunk attention of paged_chunk.cu on pairs of CTAs, for
-// chunks of more than 32 tokens.
+// batches of mostly long chunks.
 //
 // A pair (a cluster of 2) takes a group of 64 consecutive tokens of one
 // sequence with one KV head: 256 rows, 128 in each CTA, one MMA of M = 256
@@ -19,7 +19,8 @@
 // MMAs release (slots, scores, output) they release in both CTAs.
 //
 // Measured, a chunk of 4096 tokens at 4096 (4.1e11 multiply-adds x 2): bf16
-// queries 226 us, 1820 TFLOP/s, 0.94 of the measured bf16 rate.  A tile takes
+// queries 226 to 236 us on several GPUs, 1740 to 1820 TFLOP/s, 0.90 to 0.94 of
+// the measured bf16 rate; fp32 queries (two MMAs for each) 430 us.  A tile takes
 // 2050 cycles against 2048 of MMA, the softmax 1850 beside it; the rest is the
 // start, the first and last tile of a group (its queries come by TMA, its
 // output leaves through a stage: with both done by the softmax threads row by
@@ -40,12 +41,12 @@ constexpr uint32_t kKLine = 64 * 128;  // 64 dims of the 64 positions a CTA hold
 // pages of 16 rows took 357 us, against 246 with pages of 128.  FOLD: tiles
 // are laid out box by box instead of line by line, [box][line][16
 // positions][128 bytes], and a box of all the slot's lines is one request
-// (8 KB of K, 4 of V): 285 us.  The MMAs want 8-position groups a fixed stride
-// apart: the boxes' first halves are (8 groups, half of the tile's columns),
-// and so are their second halves.  So a folded tile's column order is: the
-// first 8 positions of each box, then the last 8 of each.  fp32 queries take twice
-// the MMA time, which half-width MMAs lengthen: 484 us unfolded, 494 folded,
-// so they stay unfolded, as do the single-CTA kernel's shorter chunks.
+// (8 KB of K, 4 of V): 270 us against 235.  The MMAs want 8-position groups a
+// fixed stride apart: the boxes' first halves are (8 groups, half of the
+// tile's columns), and so are their second halves.  So a folded tile's column
+// order is: the first 8 positions of each box, then the last 8 of each.  fp32
+// queries take twice the MMA time, which half-width MMAs lengthen: 484 us
+// unfolded, 494 folded, so they stay unfolded, as does the single-CTA kernel.
 constexpr uint32_t kBoxLine = 16 * 128;  // a line of a box
 
 // byte offset of 16-byte chunk `ch` of row r of line `line` in a V slot

@@ -35,7 +35,6 @@ struct Args {
   const int32_t* q_start;
   const int32_t* seq_len;
   int32_t n_seqs, max_pages, n_tokens, max_q;
-  int32_t from, to;  // a launch takes the sequences of from .. to new tokens
   int32_t n_pages, page_size;
   uint64_t page_mul;  // of page_size (paged.h)
   int32_t n_kv, window;  // window 0: the whole history
@@ -52,10 +51,8 @@ struct Args {
 #if defined(__CUDACC__)
 
 __device__ __forceinline__ Seq load_seq(const Args& p, int s) {
-  Seq q = seq_of(__ldcg(p.q_start + s), __ldcg(p.q_start + s + 1), __ldcg(p.seq_len + s), p.n_tokens, p.max_q,
-                 (int64_t)p.max_pages * p.page_size);
-  if (q.n < p.from || q.n > p.to) q.n = 0;
-  return q;
+  return seq_of(__ldcg(p.q_start + s), __ldcg(p.q_start + s + 1), __ldcg(p.seq_len + s), p.n_tokens, p.max_q,
+                (int64_t)p.max_pages * p.page_size);
 }
 
 // prefix[s] = units of the sequences before s (all KV heads), s <= n_seqs, in

@@ -110,8 +110,8 @@ int spark_paged_append(const spark_geom* g, const void* k, const void* v, int64_
  * Rows that no token of the sequence attends to may hold anything, NaN
  * included; a row that one of its new tokens attends to is expected finite
  * (a non-finite V row may reach every new token of its sequence).
- * max_q_len chooses the kernels (1: single tokens; up to 32; more), not the
- * results beyond rounding: give the true bound.
+ * max_q_len, with n_tokens and n_seqs, chooses the kernel, not the results
+ * beyond rounding: give the true bound.
  * workspace and errors as spark_paged_append. */
 int spark_paged_attention(const spark_geom* g, const void* q, int64_t q_ld, int32_t dtype,
                           const spark_page_pool* pool, int32_t layer_class, const spark_paged_batch* batch,

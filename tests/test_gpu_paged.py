@@ -176,6 +176,8 @@ SETS = {
     "long": [(5000, 1)],
     "long_chunk": [(2100, 70)],
     "big_chunk": [(1300, 1100), (700, 257)],
+    # mostly long: more than half of the longest on average
+    "pairs": [(400, 90), (0, 0), (260, 130), (77, 64), (530, 103), (640, 31), (65, 65), (900, 129)],
     "edges": [(64, 64), (65, 65), (128, 33), (129, 32), (200, 63), (256, 128), (31, 31), (33, 33)],
     "far": [(9000, 40)],     # one group over many CTAs
     "far_short": [(9000, 6)],
@@ -198,14 +200,14 @@ def test_attention_f32_pool(B, name, full, q_type):
 
 
 @pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 256, 1024])
-@pytest.mark.parametrize("name", ["decode", "mixed"])
+@pytest.mark.parametrize("name", ["decode", "mixed", "pairs"])
 def test_page_sizes(B, page, name):
     _check_attention(B, Case(SETS[name], page=page, seed=page), BF16)
     _check_attention(B, Case(SETS[name], page=page, seed=page + 1), F32, full=False, window=130)
 
 
 @pytest.mark.parametrize("n_kv", [1, 2, 3, 5, 8])
-@pytest.mark.parametrize("name", ["decode", "mixed"])
+@pytest.mark.parametrize("name", ["decode", "mixed", "pairs"])
 def test_head_counts(B, n_kv, name):
     _check_attention(B, Case(SETS[name], n_kv=n_kv, page=32, seed=n_kv), BF16)
     _check_attention(B, Case(SETS[name], n_kv=n_kv, page=32, seed=n_kv), F32)
@@ -213,22 +215,27 @@ def test_head_counts(B, n_kv, name):
 
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 127, 128, 129, 100000])
 @pytest.mark.parametrize("q_type", [F32, BF16])
-def test_windows(B, window, q_type):
-    _check_attention(B, Case(SETS["mixed"], page=16, seed=window), q_type, full=False, window=window)
+@pytest.mark.parametrize("name", ["mixed", "pairs"])
+def test_windows(B, name, window, q_type):
+    _check_attention(B, Case(SETS[name], page=16, seed=window), q_type, full=False, window=window)
+    _check_attention(B, Case(SETS[name], page=128, seed=window), q_type, full=False, window=window)
 
 
 @pytest.mark.parametrize("scale", [0.0, 0.01, 0.25, -0.0625])
-def test_scales(B, scale):
-    _check_attention(B, Case(SETS["mixed"], page=64, seed=9), F32, scale=scale)
+@pytest.mark.parametrize("name", ["mixed", "pairs"])
+def test_scales(B, name, scale):
+    _check_attention(B, Case(SETS[name], page=64, seed=9), F32, scale=scale)
+    _check_attention(B, Case(SETS[name], page=64, seed=9), BF16, scale=scale)
 
 
 def test_strided_queries_and_padded_rows(B):
     for q_type in (F32, BF16):
         _check_attention(B, Case(SETS["mixed"], page=64, seed=4, pad=37), q_type, q_pad=2048 + 8, max_q=200)
+        _check_attention(B, Case(SETS["pairs"], page=64, seed=4, pad=37), q_type, q_pad=2048 + 8)
 
 
 @pytest.mark.parametrize("q_type", [F32, BF16])
-@pytest.mark.parametrize("name", ["verify", "mixed", "edges"])
+@pytest.mark.parametrize("name", ["verify", "mixed", "edges", "pairs"])
 def test_queries_of_other_sequences_do_not_matter(B, name, q_type):
     """Rows of NaN queries (padding, and every second sequence) next to
     others in a tile: the others' results are bit for bit what they were."""
@@ -344,12 +351,12 @@ def test_repeated_and_unordered_calls_agree(B):
     g = _geom(B)
     ws = B.make_paged_workspace(g)
     runs = []
-    for name in ("decode", "big_chunk", "mixed", "long"):
+    for name in ("decode", "big_chunk", "mixed", "long", "pairs"):
         case = Case(SETS[name], page=64, seed=1)
         case.fill()
         q = torch.randn(case.n_tokens, 4096, generator=case.g, device="cuda")
         runs.append((case, q, torch.zeros_like(q), torch.zeros_like(q)))
-    for which, order in ((2, (0, 1, 2, 3)), (3, (3, 1, 0, 2))):
+    for which, order in ((2, (0, 1, 2, 3, 4)), (3, (4, 3, 1, 0, 2))):
         for i in order:
             case, q = runs[i][:2]
             B.spark_paged_attention(g, q, B.PagePool(case.k, case.v), B.SPARK_FULL, case.batch(B), runs[i][which], ws)
@@ -390,6 +397,59 @@ def test_bad_entries_raise_the_error_word(B):
     # a sequence whose length makes no sense leaves the others' results alone
     good, bad = run(lambda c: None)[2], run(put("seq_len", 0, 1))[2]
     assert bool((bad[:3] == 0).all())
+
+
+@pytest.mark.parametrize("q_type", [F32, BF16])
+@pytest.mark.parametrize("page", [16, 64])
+def test_bad_pages_under_long_chunks(B, page, q_type):
+    """Entries outside the pool under a chunk that pairs of CTAs take: reported,
+    and the other sequence's results are what they were."""
+    case = Case([(200, 90), (130, 70)], page=page, seed=15)
+    case.fill()
+    g, ws, pool = _geom(B), B.make_paged_workspace(_geom(B)), B.PagePool(case.k, case.v)
+    q = torch.randn(160, 4096, generator=case.g, device="cuda").to(q_type)
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    B.spark_paged_attention(g, q, pool, B.SPARK_FULL, case.batch(B), a, ws)
+    assert B.spark_attn_error_word(ws) == 0
+    keep = case.table.clone()
+    for entry in (-1, case.k.shape[0], 2**31 - 1, -2**31):
+        case.table.copy_(keep)
+        case.table[0, 1] = entry
+        b.zero_()
+        B.spark_paged_attention(g, q, pool, B.SPARK_FULL, case.batch(B), b, ws)
+        assert B.spark_attn_error_word(ws) == 2
+        assert torch.equal(a[90:], b[90:])
+        B.spark_attn_workspace_init(ws)
+
+
+@pytest.mark.parametrize("q_type", [F32, BF16])
+def test_captured_long_chunks_replay_with_new_lengths(B, q_type):
+    g = _geom(B)
+    case = Case([(300, 130), (200, 70)], page=16, seed=16)
+    case.fill()
+    pool, ws = B.PagePool(case.k, case.v), B.make_paged_workspace(g)
+    q = torch.randn(200, 4096, generator=case.g, device="cuda").to(q_type)
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    batch = case.batch(B)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, a, ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, a, ws)
+    for lens, new in (((300, 200), (130, 70)), ((33, 199), (33, 1)), ((290, 2), (0, 2)), ((129, 64), (128, 64))):
+        case.seq_len.copy_(_i32(lens))
+        case.q_start.copy_(_i32([0, new[0], sum(new)]))
+        a.fill_(3.0)
+        b.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, b, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and bool((a[sum(new):] == 3.0).all())
+    assert B.spark_attn_error_word(ws) == 0
 
 
 def test_captured_calls_replay_with_new_lengths(B):
