@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint64_t* q_here = kSplit ? q_raw : q_full;
     const int per = kPos / box;  // boxes of a tile
+    const uint64_t once = policy_once(), again = policy_again();
     auto slot = [&](const CUtensorMap* map, int half, int z, int b0, int b1) {
       const int s = (int)(k % NS);
       const uint32_t r = k / NS;
@@ -149,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < 2 * per) {
         const int b = lane % per, line = lane / per;
         if (b >= b0 && b < b1)
-          tma_load_4d(base + S::kRing + s * kSlot + line * kLineBytes + b * box * 128, map, &full[s], 0, z,
-                      2 * half + line, cur.j);
+          tma_load_rows(base + S::kRing + s * kSlot + line * kLineBytes + b * box * 128, map, &full[s], z,
+                        2 * half + line, cur.j, cur.groups == 1 ? once : again);
       }
       ++k;
     };

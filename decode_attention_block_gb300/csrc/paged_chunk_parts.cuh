@@ -32,6 +32,29 @@ constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
 constexpr int kMinTiles = 2;                    // tiles per CTA at least
 
+// L2 policies of the pool's rows.  A sequence of one group reads its rows
+// once: they make room first, or they would drive out the rows of longer
+// chunks, which every group of the sequence reads, up to a whole call later.
+__device__ __forceinline__ uint64_t policy_once() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_again() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+// a TMA load of a box of rows under a policy
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2, int c3,
+                                              uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
