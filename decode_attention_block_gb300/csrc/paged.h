@@ -5,9 +5,12 @@
 // Attention work is a flat list of units.  A group is up to `gt` consecutive
 // new tokens of one sequence with one KV head; it reads the cache rows of the
 // union of its tokens' windows in tiles of `tile` positions aligned to
-// multiples of `tile`, and each (group, tile) is one unit.  The list is
-// ordered by sequence, KV head, group, tile.  The CTAs of a launch take equal
-// contiguous shares of it: CTA c of G the units [total c / G, total (c+1) / G).
+// multiples of `tile`, and each (group, tile) is one unit.  A group costs more
+// than its tiles (its queries, its output): `lead` units before its first tile
+// stand for that.  The list is ordered by sequence, KV head, group, tile.  The
+// CTAs of a launch take equal contiguous shares of it: CTA c of G the units
+// [total c / G, total (c+1) / G); one whose share ends in a group's lead
+// leaves the group to the next.
 #pragma once
 
 #include <stdint.h>
@@ -62,6 +65,7 @@ struct Shape {
   int32_t gt;      // tokens of a group
   int32_t tile;    // positions of a tile (a multiple of gt)
   int32_t window;  // 0: the whole history
+  int32_t lead = 0;  // units before a group's tiles
 };
 
 SPARK_HD int32_t groups_of(const Seq& s, const Shape& sh) { return (s.n + sh.gt - 1) / sh.gt; }
@@ -86,12 +90,12 @@ SPARK_HD Group group_of(const Seq& s, const Shape& sh, int32_t i) {
   return g;
 }
 
-// units of the first x groups of a sequence, one KV head
+// units of the first x groups of a sequence, one KV head, their leads included
 SPARK_HD int64_t units_before(const Seq& s, const Shape& sh, int32_t x) {
   if (x <= 0) return 0;
   const int32_t groups = groups_of(s, sh);
   const int32_t whole = x < groups ? x : groups - 1;  // groups of exactly gt tokens among them
-  int64_t u = floor_sum((int64_t)s.p0 + sh.gt - 1, whole, sh.gt, sh.tile) + whole;
+  int64_t u = floor_sum((int64_t)s.p0 + sh.gt - 1, whole, sh.gt, sh.tile) + whole + (int64_t)sh.lead * x;
   if (x == groups) u += (int64_t)(s.p0 + s.n - 1) / sh.tile + 1;
   if (sh.window > 0) {
     const int64_t c = (int64_t)s.p0 + 1 - sh.window;

@@ -30,7 +30,7 @@ constexpr uint32_t kQBytes = 4 * kLineBytes;
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O starts at 0
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
-constexpr int kMinTiles = 2;                    // tiles per CTA at least
+constexpr int kMinTiles = 2;                    // units per CTA at least
 
 // L2 policies of the pool's rows.  A sequence of one group reads its rows
 // once: they make room first, or they would drive out the rows of longer
@@ -220,12 +220,6 @@ __device__ __forceinline__ void sign32(uint32_t (&s)[32], float sign) {
 }
 
 // 32 output dims of a row
-__device__ __forceinline__ void store32(float* dst, const uint32_t (&o)[32], float inv) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 4)
-    reinterpret_cast<float4*>(dst)[i / 4] = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                                        __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-}
 __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[32], float inv) {
 #pragma unroll
   for (int i = 0; i < 32; i += 8) {
@@ -362,11 +356,8 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     if (!ok) break;
     // (the next group's fp32 queries are split while this one's last product runs)
     Cursor nxt = cur;
-    const bool more = cur.end < u1;
-    if (more) {
-      nxt.next(p, sh);
-      if (kSplit) split_queries(nxt);
-    }
+    const bool more = nxt.advance(p, sh, u1);
+    if (kSplit && more) split_queries(nxt);
     if (!wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) break;
     const bool split = cur.begin < u0 || cur.end > u1;
     if (live) {
@@ -407,20 +398,51 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
                                         d + (lane & 3) * 8) = w;
           }
           __syncwarp();
-        } else if (tok < g.n_tok) {
-          store32(dst + d, o, inv);
+        } else if constexpr (!kSplit) {
+          if (tok < g.n_tok) store32(dst + d, o, inv);
         }
       };
       uint32_t oa[32], ob[32];
-      tc::ld32(tmem + lanes, oa);
+      if (kSplit && !split) {
+        // whole rows of fp32: four lanes write 32 bytes of a row at a time
+        auto at = [&](int x) { return tmem + lanes + ((uint32_t)(x >> 2) << 20) + (x & 3) * 64; };
+        auto rows = [&](int x, const uint32_t (&o)[32]) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = 16 * (x >> 2) + 8 * i + (lane >> 2);  // the warp's row
+            const float iv = __shfl_sync(0xffffffffu, inv, rr);
+            const int t = tok0 + 8 * quad + (rr >> 2);
+            float* to = static_cast<float*>(p.a) +
+                        (((cur.seq.q0 + g.tok + t) * (int64_t)p.n_kv + cur.j) * kGroup + (rr & 3)) * kHeadDim +
+                        (x & 3) * 64 + 2 * (lane & 3);
+            if (t < g.n_tok)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<float2*>(to + 8 * k) =
+                    make_float2(__uint_as_float(o[4 * k + 2 * i]) * iv, __uint_as_float(o[4 * k + 2 * i + 1]) * iv);
+          }
+        };
+        tc::ld16x64(at(0), oa);
 #pragma unroll 1
-      for (int d = 0; d < kHeadDim; d += 64) {
-        tc::wait_ld(oa);
-        tc::ld32(tmem + lanes + d + 32, ob);
-        put(d, oa);
-        tc::wait_ld(ob);
-        if (d + 64 < kHeadDim) tc::ld32(tmem + lanes + d + 64, oa);
-        put(d + 32, ob);
+        for (int x = 0; x < 8; x += 2) {
+          tc::wait_ld(oa);
+          tc::ld16x64(at(x + 1), ob);
+          rows(x, oa);
+          tc::wait_ld(ob);
+          if (x + 2 < 8) tc::ld16x64(at(x + 2), oa);
+          rows(x + 1, ob);
+        }
+      } else {
+        tc::ld32(tmem + lanes, oa);
+#pragma unroll 1
+        for (int d = 0; d < kHeadDim; d += 64) {
+          tc::wait_ld(oa);
+          tc::ld32(tmem + lanes + d + 32, ob);
+          put(d, oa);
+          tc::wait_ld(ob);
+          if (d + 64 < kHeadDim) tc::ld32(tmem + lanes + d + 64, oa);
+          put(d + 32, ob);
+        }
       }
       if (split) {
         part[RANKS * kRows * kHeadDim + prow] = m;

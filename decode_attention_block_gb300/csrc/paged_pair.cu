@@ -74,6 +74,11 @@ struct PairSmem {
   // gets two; a third for bf16 ones gave nothing, and the output's stage wants room)
   static constexpr int kK = SPLIT ? 1 : 2;
   static constexpr int kV = 2;
+  // A group's cost beyond its tiles, in tiles.  Four chunks of 258 to 517
+  // tokens, fp32 queries: 92 us at 0, 82, 73 and 70 at 1, 2 and 3, 73 at 4;
+  // bf16 ones 55.7, 49.5, 45.3, 44.7 and 44.9 (a chunk of 4096 230 us at 0,
+  // 229 at 2, 231 at 3).
+  static constexpr int kLead = SPLIT ? 3 : 2;
   static constexpr uint32_t kRingK = kQ * kQBytes;
   static constexpr uint32_t kRingV = kRingK + kK * kSlot;
   static constexpr uint32_t kStage = kRingV + kV * kSlot;  // the output's, where there is room
@@ -200,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // tables, lengths, rows and queries may come from the kernel before
   pdl_wait();
   pdl_trigger();
-  const Shape sh{kPairTokens, kPos, p.window};
+  const Shape sh{kPairTokens, kPos, p.window, S::kLead};
   // the rings are not in use yet: room for the prefix sums
   int64_t* prefix = reinterpret_cast<int64_t*>(base + S::kRingK);
   const int c = blockIdx.x >> 1;
@@ -310,8 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         z_v = z;
         pos_v = pos;
       }
-      if (!ok || cur.end >= u1) break;
-      cur.next(p, sh);
+      if (!ok || !cur.advance(p, sh, u1)) break;
     }
     if (!ok && lane == 0) {
       if (!flags[0]) atomicOr(p.err, kErrWaitTimeout);
@@ -438,8 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       tile += n;
-      if (!ok || __shfl_sync(0xffffffffu, (int)(cur.end >= u1), 0)) break;
-      cur.next(p, sh);
+      if (!ok || !__shfl_sync(0xffffffffu, (int)cur.advance(p, sh, u1), 0)) break;
     }
     if (one) {
       if (!ok) {

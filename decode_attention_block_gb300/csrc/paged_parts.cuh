@@ -101,12 +101,12 @@ struct Cursor {
   int groups;       // groups of the sequence
   Seq seq;
   Group g;
-  int64_t begin, end;  // the group's units in the list
+  int64_t begin, end;  // the units of the group's tiles in the list
 
   __device__ __forceinline__ void set_group(const Shape& sh, int64_t at) {
     g = group_of(seq, sh, i);
-    begin = at;
-    end = at + (g.tile1 - g.tile0);
+    begin = at + sh.lead;
+    end = begin + (g.tile1 - g.tile0);
   }
   // the group that holds unit u, in sequence `s`, `seq`, whose units begin at
   // `first`, per_head for each KV head
@@ -132,10 +132,17 @@ struct Cursor {
     }
     set_group(sh, end);
   }
+  // the next group, if it has a tile before unit u1
+  __device__ __forceinline__ bool advance(const Args& p, const Shape& sh, int64_t u1) {
+    if (end >= u1) return false;
+    next(p, sh);
+    return begin < u1;
+  }
 };
 
 // A CTA's share of the list: the units [u0, u1) of `total`, shared by G CTAs,
-// and the group it begins with.  Empty (c >= G): no more is set.
+// and the group it begins with.  Without a tile (c >= G, or a share that is
+// all lead): no more is set.
 struct Share {
   int64_t total, u0, u1;
   int G;
@@ -192,7 +199,7 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
     } else {
       cur.seek(sh, share.u0, at, each);
     }
-    return true;
+    return cur.begin < share.u1;
   }
   work_prefix<NT>(p, sh, room, room + SPARK_MAX_BATCH + 2);
   share.total = room[p.n_seqs];
@@ -205,7 +212,7 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
   cur.s = lo;
   cur.seq = load_seq(p, lo);
   cur.seek(sh, share.u0, room[lo], (room[lo + 1] - room[lo]) / p.n_kv);
-  return true;
+  return cur.begin < share.u1;
 }
 
 __device__ __forceinline__ int page_col(const Args& p, int pos) { return page_col(pos, p.page_mul); }

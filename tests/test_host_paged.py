@@ -59,7 +59,7 @@ int main() {
   // groups and their tiles, at the edges of tiles and windows
   std::mt19937 rng(1);
   const Shape shapes[] = {{1, 16, 0}, {1, 16, 1}, {1, 16, 5}, {1, 16, 512}, {32, 128, 0}, {32, 128, 7}, {32, 128, 512},
-                          {32, 128, INT32_MAX}, {64, 128, 0}, {64, 128, 100}};
+                          {32, 128, INT32_MAX}, {64, 128, 0}, {64, 128, 100}, {32, 128, 0, 3}, {64, 128, 100, 1}};
   for (const Shape& sh : shapes)
     for (int it = 0; it < 400; ++it) {
       Seq s{0, 1 + (int)(rng() % 200), (int)(rng() % 1500), false};
@@ -75,7 +75,7 @@ int main() {
         }
         CHECK(g.lo == lo && g.hi == hi && g.tok == i * sh.gt && g.tok + g.n_tok <= s.n, "group %d", i);
         CHECK(g.tile0 == lo / sh.tile && g.tile1 == hi / sh.tile + 1, "tiles of group %d", i);
-        for (int k = g.tile0; k < g.tile1; ++k, ++u) CHECK(group_at(s, sh, u) == i, "group_at");
+        for (int k = g.tile0 - sh.lead; k < g.tile1; ++k, ++u) CHECK(group_at(s, sh, u) == i, "group_at");
       }
       CHECK(units_of(s, sh) == u, "units_of");
     }
@@ -85,14 +85,14 @@ int main() {
   // shares, tickets and partial slots
   for (int it = 0; it < 300; ++it) {
     std::vector<int64_t> begin{0};
-    const int groups = 1 + rng() % 30;
-    for (int i = 0; i < groups; ++i) begin.push_back(begin.back() + 1 + rng() % (it % 3 ? 9 : 300));
+    const int groups = 1 + rng() % 30, lead = it % 4;
+    for (int i = 0; i < groups; ++i) begin.push_back(begin.back() + lead + 1 + rng() % (it % 3 ? 9 : 300));
     const int64_t total = begin.back();
     const int G = ctas_for(total, 1 + rng() % 6, 1 + rng() % 40);
     CHECK(G >= 1 && G <= total, "ctas_for");
     std::set<int> slots, tickets;
     for (int i = 0; i < groups; ++i) {
-      const int64_t b = begin[i], e = begin[i + 1];
+      const int64_t b = begin[i] + lead, e = begin[i + 1];
       const int c0 = cta_at(b, total, G), c1 = cta_at(e - 1, total, G);
       for (int c = 0; c < G; ++c) {
         const int64_t u0 = share_begin(total, G, c), u1 = share_begin(total, G, c + 1);
