@@ -148,15 +148,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       const int n = b1 - b0;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * n * box) * 128u);
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(n * box) * 256u);
       __syncwarp();
-      // lane: (line of the half, box); z is the row of the lane's box
-      if (lane < 2 * per) {
-        const int b = lane % per, line = lane / per;
-        if (b >= b0 && b < b1)
-          tma_load_rows(base + S::kRing + s * kSlot + line * kLineBytes + b * box * 128, map, &full[s], z,
-                        2 * half + line, cur.j, cur.groups == 1 ? once : again);
-      }
+      // a lane per box, its two lines at once; z is the box's row
+      if (lane >= b0 && lane < b1)
+        tma_load_rows(base + S::kRing + s * kSlot + lane * (box / 8) * kGroupBytes<2>, map, &full[s], z, 2 * half, cur.j,
+                      cur.groups == 1 ? once : again);
       ++k;
     };
     for (;;) {
@@ -182,8 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto entry = [&](int64_t u) {
         int pos, b0, b1;
         boxes(u, pos, b0, b1);
-        const int b = lane % per;
-        return b >= b0 && b < b1 ? paged::page_entry(p, cur.s, paged::page_col(p, pos + b * box)) : 0;
+        return lane >= b0 && lane < b1 ? paged::page_entry(p, cur.s, paged::page_col(p, pos + lane * box)) : 0;
       };
       int z_v = 0, v0 = 0, v1 = 0;  // the tile before
       int ahead = entry(t0);
@@ -192,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < t1) {
           int pos;
           boxes(u, pos, b0, b1);
-          z = paged::page_of(p, ahead) * p.page_size + paged::page_row(p, pos + (lane % per) * box);
+          z = paged::page_of(p, ahead) * p.page_size + paged::page_row(p, pos + lane * box);
           if (u + 1 < t1) ahead = entry(u + 1);
           slot(&tm_k, 0, z, b0, b1);
           slot(&tm_k, 1, z, b0, b1);
@@ -237,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int half = 0; half < 2; ++half, ++k) {
         const int s = (int)(k % NS);
         if (!wait(&full[s], (k / NS) & 1)) return;
-        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot), a0 = tc::desc_k_major(q_addr + 2 * half * S::kQLine);
+        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot, kGroupBytes<2>), a0 = tc::desc_k_major(q_addr + 2 * half * S::kQLine);
         if (one) {
 #pragma unroll
           for (int line = 0; line < 2; ++line)
@@ -246,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 tc::mma_ss(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
-                           b0 + (line * kLineBytes >> 4) + 2 * ks, kIdS, half + line + part + ks > 0);
+                           b0 + (line * kAtom >> 4) + 2 * ks, kIdS, half + line + part + ks > 0);
           tc::commit(&empty[s]);
           if (half == 1) tc::commit(&s_full[i & 1]);
         }
@@ -261,23 +257,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = (int)(k % NS);
         if (!wait(&full[s], (k / NS) & 1)) return;
         if (r0 > 0 || r1 < kPos) {
-          unsigned char* v = base + S::kRing + s * kSlot;
-          // 16 lanes clear a row's two lines
-          for (int r = lane >> 4; r < kPos; r += 2)
-            if (r < r0 || r >= r1)
-              *reinterpret_cast<uint4*>(v + ((lane >> 3) & 1) * kLineBytes + r * 128 + (lane & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          clear_rows(base + S::kRing + s * kSlot, r0, r1, lane);
           __syncwarp();
         }
-        const uint64_t b0 = tc::desc_mn_major(ring + s * kSlot, kLineBytes);
+        const uint64_t b0 = tc::desc_mn_major(ring + s * kSlot, kAtom, kGroupBytes<2>);
         const uint32_t d = tmem + half * 128;
         if (one) {
 #pragma unroll
           for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
             for (int ks = 0; ks < kPos / 16; ++ks)  // 16 positions: two 8-row groups, eight columns of P
-              tc::mma_ts(d, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b0 + ks * (2048 >> 4), kIdO,
+              tc::mma_ts(d, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b0 + ks * (2 * kGroupBytes<2> >> 4), kIdO,
                          !first || part + ks > 0);
           tc::commit(&empty[s]);
           if (half == 1) tc::commit(&pv_done[i & 1]);
@@ -315,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    softmax_warps<QT, 1, false, false>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, q_raw, s_full, pv_done, flags, nullptr,
+    softmax_warps<QT, 1, false>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, q_raw, s_full, pv_done, flags, nullptr,
                                        warp, tid - 64, [&] { mbar_arrive(q_full); }, [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
   }
   tc::fence_before();
@@ -333,7 +323,7 @@ cudaError_t launch_chunk(const Args& p, const void* k, const void* v, cudaStream
   while (p.page_size % box != 0) box /= 2;
   CUtensorMap mk, mv;
   const int64_t rows = (int64_t)p.n_pages * p.page_size;
-  if (!make_chunk_map(&mk, k, p.n_kv, rows, box, 1) || !make_chunk_map(&mv, v, p.n_kv, rows, box, 1))
+  if (!make_chunk_map(&mk, k, p.n_kv, rows, box, 2) || !make_chunk_map(&mv, v, p.n_kv, rows, box, 2))
     return cudaErrorInvalidValue;
   CUtensorMap mq, mq8;
   if (!make_query_maps<QT>(&mq, &mq8, p)) return cudaErrorInvalidValue;

@@ -27,6 +27,16 @@ constexpr int kSoft = 128;                      // softmax threads, one row each
 constexpr uint32_t kLineBytes = kPos * 128;     // 64 dims of 128 rows or positions
 constexpr uint32_t kSlot = 2 * kLineBytes;      // 128 dims
 constexpr uint32_t kQBytes = 4 * kLineBytes;
+// K and V lie in a slot as groups of 8 rows, each group line by line: [row /
+// 8][line][8 rows][128 bytes].  So one TMA box holds all the slot's lines of
+// its rows, and groups and lines are a fixed stride apart, as an MMA's operand
+// wants them.  TMA spends about 100 cycles on a request whatever its size:
+// line by line, pages of 16 rows bound a tile by its 64 requests (a mixed
+// batch of 32, bf16 queries: 135 against 107 us; a chunk of 4096 345 against
+// 240), and longer pages gained nothing (109 and 225 us either way).
+constexpr uint32_t kAtom = 8 * 128;
+template <int LINES>  // of a slot
+constexpr uint32_t kGroupBytes = LINES * kAtom;
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O starts at 0
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
@@ -45,14 +55,33 @@ __device__ __forceinline__ uint64_t policy_again() {
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-// a TMA load of a box of rows under a policy
-__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2, int c3,
-                                              uint64_t policy) {
+// A TMA load of a box of rows from row `row` (a multiple of 8), lines `line` ..,
+// of a head, under a policy.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int row, int line,
+                                              int head, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(line), "r"(row >> 3), "r"(head), "l"(policy)
       : "memory");
+}
+
+// A warp clears the rows outside [r0, r1) of a slot of two lines of 128 rows.
+// (Kept small: a loop over the rows, unrolled, cost a mixed batch 18 of 123
+// us, the MMA warp's code missing the instruction cache.)
+__device__ __forceinline__ void clear_rows(unsigned char* v, int r0, int r1, int lane) {
+#pragma unroll 1
+  for (int g = 0; g < kPos / 8; ++g) {
+    if (8 * g >= r0 && 8 * g + 8 <= r1) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * (i & 1) + (lane >> 3);
+      if (8 * g + r < r0 || 8 * g + r >= r1)
+        *reinterpret_cast<uint4*>(v + g * kGroupBytes<2> + (i >> 1) * kAtom + r * 128 + (lane & 7) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -156,17 +185,6 @@ bool make_query_maps(CUtensorMap* all, CUtensorMap* box, const Args& p) {
          make_query_map<QT>(box, p, kQueryBoxTokens, 1);
 }
 
-// The seen-bits of a folded tile's columns (paged_pair.cu), from those of its
-// positions: the first 8 of each 16 positions, then the last 8 of each.
-__device__ __forceinline__ void fold_seen(uint32_t (&w)[4]) {
-  const uint32_t a = __byte_perm(w[0], w[1], 0x6420), b = __byte_perm(w[2], w[3], 0x6420);
-  const uint32_t c = __byte_perm(w[0], w[1], 0x7531), d = __byte_perm(w[2], w[3], 0x7531);
-  w[0] = a;
-  w[1] = b;
-  w[2] = c;
-  w[3] = d;
-}
-
 // The columns x0 .. x1 of a tile that a row sees, as one bit per column of
 // the 32 from `first`.
 __device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
@@ -234,12 +252,12 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[
 // share a group, one row per thread: scores to probabilities, the running
 // maximum and sum, the output at the group's end.  arrive_q, arrive_p: one
 // lane per warp tells the MMA warp that fp32 queries are in halves, or the
-// probabilities in a buffer.  FOLD: the tiles' columns are in a folded order.
+// probabilities in a buffer.
 // STAGE: whole groups' outputs leave through `stage`.
 constexpr int kStageRow = 64 + 16;             // bytes of a row of an output stage: 32 bf16 dims, padding
 constexpr int kStageBytes = 32 * kStageRow;    // of a warp
 
-template <typename QT, int RANKS, bool FOLD, bool STAGE, typename ArriveQ, typename ArriveP>
+template <typename QT, int RANKS, bool STAGE, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
                                               uint64_t* q_raw, uint64_t* s_full, uint64_t* pv_done,
@@ -309,7 +327,6 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         }
         if (!whole) {
           uint32_t seen[4] = {seen32(x0, x1, 0), seen32(x0, x1, 32), seen32(x0, x1, 64), seen32(x0, x1, 96)};
-          if (FOLD) fold_seen(seen);
           mask32(s0, seen[0]);
           mask32(s1, seen[1]);
           mask32(s2, seen[2]);
@@ -560,15 +577,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_con
 }
 
 // A pool [rows][n_kv][256] bf16 as the chunk kernels load it: boxes of `lines`
-// 128-byte lines of `box` rows of one KV head.
+// lines of `box` rows of one KV head (kAtom's layout).  Its dimensions are a
+// line's elements, the row of a group, the line, the group, the head.
 inline bool make_chunk_map(CUtensorMap* map, const void* base, int n_kv, int64_t rows, int box, int lines) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {64, (cuuint64_t)rows, 4, (cuuint64_t)n_kv};
-  const cuuint64_t strides[3] = {(cuuint64_t)n_kv * kHeadDim * 2, 128, kHeadDim * 2};
-  const cuuint32_t shape[4] = {64, (cuuint32_t)box, (cuuint32_t)lines, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, shape, estr,
+  const cuuint64_t row = (cuuint64_t)n_kv * kHeadDim * 2;
+  const cuuint64_t dims[5] = {64, 8, 4, (cuuint64_t)rows / 8, (cuuint64_t)n_kv};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, kHeadDim * 2};
+  const cuuint32_t shape[5] = {64, 8, (cuuint32_t)lines, (cuuint32_t)box / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, shape, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -19,8 +19,8 @@
 // MMAs release (slots, scores, output) they release in both CTAs.
 //
 // Measured, a chunk of 4096 tokens at 4096 (4.1e11 multiply-adds x 2): bf16
-// queries 226 to 236 us on several GPUs, 1740 to 1820 TFLOP/s, 0.90 to 0.94 of
-// the measured bf16 rate; fp32 queries (two MMAs for each) 430 us.  A tile takes
+// queries 224 us, 1840 TFLOP/s, 0.95 of the measured bf16 rate (240 us on
+// pages of 16 rows); fp32 queries (two MMAs for each) 410 us.  A tile takes
 // 2050 cycles against 2048 of MMA, the softmax 1850 beside it; the rest is the
 // start, the first and last tile of a group (its queries come by TMA, its
 // output leaves through a stage: with both done by the softmax threads row by
@@ -33,39 +33,6 @@ namespace {
 using namespace chunk;
 
 constexpr int kPairTokens = 2 * paged::kChunkTokens;
-constexpr uint32_t kKLine = 64 * 128;  // 64 dims of the 64 positions a CTA holds the keys of
-
-// Pages of 16 rows (or an odd multiple) come in boxes of 16 positions.  A box
-// of one line is 2 KB, and TMA spends about 100 cycles on a request whatever
-// its size, which bounds bf16 chunks: a chunk of 4096 tokens at 4096 with
-// pages of 16 rows took 357 us, against 246 with pages of 128.  FOLD: tiles
-// are laid out box by box instead of line by line, [box][line][16
-// positions][128 bytes], and a box of all the slot's lines is one request
-// (8 KB of K, 4 of V): 270 us against 235.  The MMAs want 8-position groups a
-// fixed stride apart: the boxes' first halves are (8 groups, half of the
-// tile's columns), and so are their second halves.  So a folded tile's column
-// order is: the first 8 positions of each box, then the last 8 of each.  fp32
-// queries take twice the MMA time, which half-width MMAs lengthen: 484 us
-// unfolded, 494 folded, so they stay unfolded, as does the single-CTA kernel.
-constexpr uint32_t kBoxLine = 16 * 128;  // a line of a box
-
-// byte offset of 16-byte chunk `ch` of row r of line `line` in a V slot
-template <bool FOLD>
-__device__ __forceinline__ uint32_t v_chunk(int r, int line, int ch) {
-  return (FOLD ? (uint32_t)(r >> 4) * (2 * kBoxLine) + line * kBoxLine + (r & 15) * 128 : line * kLineBytes + r * 128) +
-         ch * 16;
-}
-// the descriptor of a V slot, and the offset (descriptor units) of its step of
-// 16 positions (two groups of 8)
-template <bool FOLD>
-__device__ __forceinline__ uint64_t v_desc(uint32_t slot) {
-  return FOLD ? tc::desc_mn_major(slot, kBoxLine, 2 * kBoxLine) : tc::desc_mn_major(slot, kLineBytes);
-}
-template <bool FOLD>
-__device__ __forceinline__ uint32_t v_step(int ks) {
-  return (FOLD ? (uint32_t)(ks & 3) * (4 * kBoxLine) + (ks >> 2) * 1024 : (uint32_t)ks * 2048) >> 4;
-}
-
 template <bool SPLIT>
 struct PairSmem {
   static constexpr int kQ = SPLIT ? 2 : 1;
@@ -146,7 +113,17 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-template <typename QT, bool FOLD>
+// ... a box of rows (tma_load_rows)
+__device__ __forceinline__ void tma_load_rows_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int row,
+                                                   int line, int head, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(0), "r"(line), "r"(row >> 3), "r"(head), "l"(policy)
+      : "memory");
+}
+
+template <typename QT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_paged_pair(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q8,
@@ -231,6 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int per_k = 64 / box_k, per_v = kPos / box_v;  // boxes of a half's keys, of a tile's values
     const int bk = lane % per_k, bv = lane % per_v;      // the lane's boxes
+    const uint64_t once = policy_once(), again = policy_again();
     auto freed = [&](uint64_t* bar, uint32_t use) {
       if (ok && use > 0 && !mbar_wait_bounded(bar, (use - 1) & 1, flags, kWaitLimitNs)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
@@ -288,13 +266,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(&k_full[s], (uint32_t)(n * box_k) * 512u);
             __syncwarp();
           }
-          if (FOLD) {
-            if (lane < per_k && wanted(xk, box_k))
-              tma_load_4d_pair(base + S::kRingK + s * kSlot + bk * (4 * kBoxLine), &tm_k, in_rank0(&k_full[s]), 0, zk, 0,
-                               cur.j);
-          } else if (lane < 4 * per_k && wanted(xk, box_k))
-            tma_load_4d_pair(base + S::kRingK + s * kSlot + (lane / per_k) * kKLine + bk * box_k * 128, &tm_k,
-                             in_rank0(&k_full[s]), 0, zk, lane / per_k, cur.j);
+          if (lane < per_k && wanted(xk, box_k))
+            tma_load_rows_pair(base + S::kRingK + s * kSlot + lane * (box_k / 8) * kGroupBytes<4>, &tm_k,
+                               in_rank0(&k_full[s]), zk, 0, cur.j, cur.groups == 1 ? once : again);
           ++kk;
         }
         if (u > t0) {
@@ -304,12 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int b = 0; b < per_v; ++b) n += wanted(pos_v + b * box_v, box_v);
           if (lane == 0) mbar_arrive_expect_tx(&v_here[s], (uint32_t)(n * box_v) * 256u);
           __syncwarp();
-          if (FOLD) {
-            if (lane < per_v && wanted(pos_v + bv * box_v, box_v))
-              tma_load_4d(base + S::kRingV + s * kSlot + bv * (2 * kBoxLine), &tm_v, &v_here[s], 0, z_v, 2 * rank, cur.j);
-          } else if (lane < 2 * per_v && wanted(pos_v + bv * box_v, box_v))
-            tma_load_4d(base + S::kRingV + s * kSlot + (lane / per_v) * kLineBytes + bv * box_v * 128, &tm_v, &v_here[s],
-                        0, z_v, 2 * rank + lane / per_v, cur.j);
+          if (lane < per_v && wanted(pos_v + lane * box_v, box_v))
+            tma_load_rows(base + S::kRingV + s * kSlot + lane * (box_v / 8) * kGroupBytes<2>, &tm_v, &v_here[s], z_v,
+                          2 * rank, cur.j, cur.groups == 1 ? once : again);
           ++kv;
         }
         z_v = z;
@@ -337,7 +308,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the rows of V tiles that no token of the group sees (their P is 0, but
     // they may hold anything)
     constexpr uint32_t kIdS = tc::idesc(2 * kRows, kPos, false), kIdO = tc::idesc(2 * kRows, kHeadDim, true);
-    constexpr uint32_t kIdFold = tc::idesc(2 * kRows, kPos / 2, false);
     const uint32_t q_addr = smem_u32(base), ring_k = smem_u32(base + S::kRingK), ring_v = smem_u32(base + S::kRingV);
     uint32_t kk = 0, kv = 0, tile = 0, item = 0;
     bool ok = true;
@@ -352,15 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int s = (int)(kv % S::kV);
       ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&v_here[s], (kv / S::kV) & 1, flags, kWaitLimitNs));
       if (!ok) return false;
-      if (r0 > 0 || r1 < kPos) {
-        unsigned char* v = base + S::kRingV + s * kSlot;
-        // 16 lanes clear a row's two lines
-        for (int r = lane >> 4; r < kPos; r += 2)
-          if (r < r0 || r >= r1)
-            *reinterpret_cast<uint4*>(v + v_chunk<FOLD>(r, (lane >> 3) & 1, lane & 7)) =
-                make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
+      if (r0 > 0 || r1 < kPos) clear_rows(base + S::kRingV + s * kSlot, r0, r1, lane);
       __syncwarp();
       return true;
     };
@@ -369,29 +331,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int s = (int)(kk % S::kK);
       if (!both(&k_full[s], (kk / S::kK) & 1)) return;
       const uint64_t a0 = tc::desc_k_major(q_addr);
-      const uint64_t b0 = tc::desc_k_major(ring_k + s * kSlot, FOLD ? 4 * kBoxLine : 1024);
+      const uint64_t b0 = tc::desc_k_major(ring_k + s * kSlot, kGroupBytes<4>);
       if (one) {
-        if (FOLD) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h)  // the boxes' first and second halves
 #pragma unroll
-            for (int line = 0; line < 4; ++line)
+        for (int line = 0; line < 4; ++line)
 #pragma unroll
-              for (int part = 0; part < S::kQ; ++part)
+          for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  tc::mma_ss2(d + h * (kPos / 2), a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
-                              b0 + ((line * kBoxLine + h * 1024) >> 4) + 2 * ks, kIdFold, line + part + ks > 0);
-        } else {
-#pragma unroll
-          for (int line = 0; line < 4; ++line)
-#pragma unroll
-            for (int part = 0; part < S::kQ; ++part)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                tc::mma_ss2(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
-                            b0 + (line * kKLine >> 4) + 2 * ks, kIdS, line + part + ks > 0);
-        }
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_ss2(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
+                          b0 + (line * kAtom >> 4) + 2 * ks, kIdS, line + part + ks > 0);
         tc::commit_both(&k_empty[s]);
         tc::commit_both(&s_full[i & 1]);
       }
@@ -404,13 +353,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!values_here(r0, r1)) return;
       if (!both(&v_peer[s], (kv / S::kV) & 1)) return;
       if (!both(&p_full[i & 1], (i >> 1) & 1)) return;
-      const uint64_t b0 = v_desc<FOLD>(ring_v + s * kSlot);
+      const uint64_t b0 = tc::desc_mn_major(ring_v + s * kSlot, kAtom, kGroupBytes<2>);
       if (one) {
 #pragma unroll
         for (int part = 0; part < S::kQ; ++part)
 #pragma unroll
           for (int ks = 0; ks < kPos / 16; ++ks)  // 16 positions: two 8-row groups, eight columns of P
-            tc::mma_ts2(tmem, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b0 + v_step<FOLD>(ks), kIdO,
+            tc::mma_ts2(tmem, a + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, b0 + ks * (2 * kGroupBytes<2> >> 4), kIdO,
                         !first || part + ks > 0);
         tc::commit_both(&v_empty[s]);
         tc::commit_both(&pv_done[i & 1]);
@@ -459,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const uint32_t q_bar = in_rank0(q_full), p_bar = in_rank0(p_full);
-    softmax_warps<QT, 2, FOLD, !kSplit>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, q_raw, s_full, pv_done, flags,
+    softmax_warps<QT, 2, !kSplit>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, q_raw, s_full, pv_done, flags,
                                         base + S::kStage, warp, tid - 64, [&] { arrive_at(q_bar); },
                                         [&](uint32_t buf) { arrive_tmem_at(p_bar + 8 * buf); });
   }
@@ -472,17 +421,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename QT, bool FOLD>
+template <typename QT>
 cudaError_t launch_pair(const Args& p, const void* k, const void* v, int box_k, int box_v, cudaStream_t st) {
   using S = PairSmem<std::is_same<QT, float>::value>;
   CUtensorMap mk, mv;
   const int64_t rows = (int64_t)p.n_pages * p.page_size;
-  if (!make_chunk_map(&mk, k, p.n_kv, rows, box_k, FOLD ? 4 : 1) ||
-      !make_chunk_map(&mv, v, p.n_kv, rows, box_v, FOLD ? 2 : 1))
+  if (!make_chunk_map(&mk, k, p.n_kv, rows, box_k, 4) ||
+      !make_chunk_map(&mv, v, p.n_kv, rows, box_v, 2))
     return cudaErrorInvalidValue;
   CUtensorMap mq, mq8;
   if (!make_query_maps<QT>(&mq, &mq8, p)) return cudaErrorInvalidValue;
-  auto kern = k_paged_pair<QT, FOLD>;
+  auto kern = k_paged_pair<QT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
   if (e != cudaSuccess) return e;
   int pairs = device_sm_count() / 2;
@@ -499,9 +448,8 @@ cudaError_t launch_paged_pair(const paged::Args& p, int qdtype, const void* k, c
   int box_v = kPos;  // the largest boxes that divide a tile's values, a half's keys, and a page
   while (p.page_size % box_v != 0) box_v /= 2;
   const int box_k = box_v < 64 ? box_v : 64;
-  if (qdtype != SPARK_BF16) return launch_pair<float, false>(p, k, v, box_k, box_v, st);
-  return box_v == 16 ? launch_pair<__nv_bfloat16, true>(p, k, v, box_k, box_v, st)
-                     : launch_pair<__nv_bfloat16, false>(p, k, v, box_k, box_v, st);
+  return qdtype == SPARK_BF16 ? launch_pair<__nv_bfloat16>(p, k, v, box_k, box_v, st)
+                              : launch_pair<float>(p, k, v, box_k, box_v, st);
 }
 
 }  // namespace spark
