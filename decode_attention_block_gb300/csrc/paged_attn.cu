@@ -477,15 +477,14 @@ cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype,
   if (p.max_q <= paged::kChunkTokens) return launch_paged_chunk(p, qdtype, k, v, st);
   // Longer chunks take pairs of CTAs, which read 64 tokens' rows once: where
   // most sequences are long (the average above half of the longest: 32 of 33
-  // tokens at 4096-8192, bf16 queries, 169 us against 257 on single CTAs), or
+  // tokens at 4096-8192, bf16 queries, 166 us against 261 on single CTAs), or
   // where the long ones are most of the work (above 128 tokens a sequence on
-  // average: 8 sequences, one of them with a chunk of 3100 tokens, 112 against
-  // 142 us).  In other batches the short sequences would leave most of a
+  // average: 16 sequences, 3 of them with chunks of ~3000 tokens, 402 against
+  // 446 us).  In other batches the short sequences would leave most of a
   // pair's rows empty, and single CTAs take them all (32 sequences, 4 of them
-  // with chunks of ~400 tokens: 137 against 165 us; fp32 queries 197 against
-  // 245).  Each kind on the kernel that suits it, one after the other, came
-  // to 155 and 200 us there, and to twice as long for 8 sequences with one
-  // chunk of 100: the two kernels' starts and ends add up.
+  // with chunks of ~400 tokens: 107 against 118 us; fp32 queries 132 against
+  // 172).  Each kind on the kernel that suits it, one after the other, was
+  // slower than either: the two kernels' starts and ends add up.
   const int64_t T = p.n_tokens, S = p.n_seqs;
   if (2 * T > S * p.max_q || T > 128 * S) return launch_paged_pair(p, qdtype, k, v, st);
   return launch_paged_chunk(p, qdtype, k, v, st);

@@ -31,13 +31,14 @@
 //
 // This kernel takes chunks of up to 32 tokens, which are bound by the rows
 // read from HBM (32 sequences at 4096-8192, 0.82 GB, bf16 queries: 4 tokens
-// each 136 us, 6.0 TB/s; 32 tokens 147 us, 5.6 TB/s, 707 TFLOP/s), and batches
-// with few longer ones; many longer ones are bound by what a CTA alone takes
-// in from L2, and go to paged_pair.cu.  What it
-// cost on the way (a chunk of 4096 tokens at 4096): 128 columns unrolled in
-// the softmax missed the instruction cache, 566 us; operands of an MMA moved
-// to uniform registers one by one, 361 -> 335; scores read twice, 335 -> 330;
-// the table's entry looked up when needed, 330 -> 309.
+// each 132 us, 6.2 TB/s; 32 tokens 147 us, 5.6 TB/s, 707 TFLOP/s), and batches
+// with few longer ones (32 sequences, 4 of them with chunks of ~400 tokens:
+// 107 us; 133 us for fp32 queries, whose MMAs alone take 80); many longer ones
+// are bound by what a CTA alone takes in from L2, and go to paged_pair.cu.
+// What it cost on the way (a chunk of 4096 tokens at 4096): 128 columns
+// unrolled in the softmax missed the instruction cache, 566 us; operands of an
+// MMA moved to uniform registers one by one, 361 -> 335; scores read twice,
+// 335 -> 330; the table's entry looked up when needed, 330 -> 309.
 #include "paged_chunk_parts.cuh"
 
 namespace spark {
@@ -53,9 +54,9 @@ struct ChunkSmem {
   static constexpr int kQ = SPLIT ? 2 : 1;
   static constexpr uint32_t kQLine = kQ * kLineBytes;  // a line of the queries, with that of the remainders
   static constexpr int kSlots = SPLIT ? 3 : 5;
-  // A group's cost beyond its tiles, in tiles.  A mixed batch of 32, fp32
-  // queries: 195 us at 0, 160, 154 and 157 at 1, 2 and 3; bf16 ones 137 at 0
-  // and 136, 141 and 144.
+  // A group's cost beyond its tiles, in tiles.  A mixed batch of 32 (pages of
+  // 16 rows line by line), fp32 queries: 195 us at 0, 160, 154 and 157 at 1, 2
+  // and 3; bf16 ones 137 at 0 and 136, 141 and 144.
   static constexpr int kLead = SPLIT ? 2 : 1;
   static constexpr uint32_t kRing = kQ * kQBytes;
   static constexpr uint32_t kBars = kRing + kSlots * kSlot;
