@@ -10,8 +10,9 @@ namespace spark {
 namespace score {
 
 constexpr int kMaxParts = 64;       // parts a row is split into at most
-constexpr int kMaxSplit = 2048;     // (row, part) pairs of a split call at most
+constexpr int kMaxSplit = 256;      // (row, part) pairs of a split call at most
 constexpr int kPartElems = 4096;    // elements of a part at least: one tile
+constexpr int kSplitElems = 65536;  // of a row that is split
 
 // what one part of a row leaves for the join
 struct alignas(16) Part {
@@ -24,15 +25,17 @@ constexpr size_t kTickets = 256;    // uint32 [kMaxSplit], zero between launches
 constexpr size_t kParts = kTickets + 4 * kMaxSplit;
 constexpr size_t kTotal = kParts + sizeof(Part) * kMaxSplit;
 
-// Parts per row: enough CTAs for the GPU (about two an SM) where the rows
-// alone are too few.
-inline int parts_for(int n_rows, int vocab, int sms) {
-  int64_t c = (2 * (int64_t)sms + n_rows - 1) / n_rows;
-  const int64_t most = vocab / kPartElems;
-  if (c > most) c = most;
+// Parts per row.  A part's list of alternatives and the join cost more than the
+// CTAs gain where there are many: one row of 131072 with 20 alternatives takes
+// 22 us whole, 14 in 8 parts and 10.8 in 32; 32 rows 25, 18 and 22; 100 rows 26
+// whole and 28 in two; 511 rows 57 and 72.  Rows of 32001 take 12 us whole and
+// 10.4 in 8 parts at best, and longer as soon as there are 48 of them.
+inline int parts_for(int n_rows, int vocab) {
+  if (vocab < kSplitElems) return 1;
+  int c = kMaxSplit / n_rows;
+  if (c > vocab / kPartElems) c = vocab / kPartElems;
   if (c > kMaxParts) c = kMaxParts;
-  if (c * n_rows > kMaxSplit) c = kMaxSplit / n_rows;
-  return c < 1 ? 1 : (int)c;
+  return c < 1 ? 1 : c;
 }
 
 }  // namespace score

@@ -902,7 +902,10 @@ def _check_scores(got, logits, targets, k):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("n,vocab,k", [(1, 1, 1), (1, 1, 0), (3, 2, 2), (2, 31, 31), (5, 257, 5), (1, 4097, 20),
                                        (7, 8191, 32), (64, 1000, 1), (1, 131072, 20), (2, 131071, 32), (33, 50001, 5),
-                                       (700, 5003, 3), (1, 262144, 0), (2100, 64, 4)])
+                                       (700, 5003, 3), (1, 262144, 0), (2100, 64, 4),
+                                       # rows in parts: 65536 and up
+                                       (1, 65535, 20), (3, 65536, 32), (5, 65539, 1), (33, 70001, 6), (128, 66000, 9),
+                                       (129, 65537, 2), (1, 1000003, 32)])
 def test_logprobs(B, n, vocab, k, dtype):
     g = torch.Generator(device="cuda").manual_seed(n + vocab)
     x = (torch.randn(n, vocab, generator=g, device="cuda") * 3).to(dtype)
@@ -913,30 +916,31 @@ def test_logprobs(B, n, vocab, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("ld,off", [(5007, 0), (5008, 3), (5001, 1), (6000, 7)])
-def test_logprobs_strides_and_alignment(B, ld, off, dtype):
+@pytest.mark.parametrize("ld,off,vocab", [(5007, 0, 5000), (5008, 3, 5000), (5001, 1, 5000), (6000, 7, 5000),
+                                          (70009, 0, 70001), (70001, 1, 69999), (66000, 5, 65536)])
+def test_logprobs_strides_and_alignment(B, ld, off, vocab, dtype):
     x = (torch.randn(9, ld, device="cuda") * 2).to(dtype)
-    v = x[:, off:off + 5000]
+    v = x[:, off:off + vocab]
     t = torch.arange(9, dtype=torch.int32, device="cuda") * 500
     x[:, :off] = float("inf")                       # outside the rows: never looked at
-    x[:, off + 5000:] = float("nan")
+    x[:, off + vocab:] = float("nan")
     got = _scores(B, v, t, 7)
     assert got["word"] == 0
     _check_scores(got, v, t, 7)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_logprobs_ties_orders_and_masks(B, dtype):
-    v = 9000
+@pytest.mark.parametrize("v", [9000, 81000])
+def test_logprobs_ties_orders_and_masks(B, v, dtype):
     i = torch.arange(v, device="cuda", dtype=F32)
     neg = torch.full((v,), -float("inf"), device="cuda")
     rows = [torch.zeros(v, device="cuda"),                                  # all equal: the lowest indices
             -torch.zeros(v, device="cuda") + torch.where(i % 2 == 0, 0.0, -0.0),  # -0 and 0 are equal
             i / v, -i / v, (i * 7919 % v) / v,                              # ascending, descending, mixed
-            torch.where(i % 1000 == 999, 0.5, neg),                         # nine tokens left
+            torch.where(i % (v // 9) == 999, 0.5, neg),                     # nine tokens left
             torch.where(i == 8888, 2.0, neg),                               # one left
             torch.where((i == 8998) | (i == 8990), 0.0, torch.where(i == 4100, -0.0, neg)),  # three, equal, far apart
-            torch.where(i % 700 == 3, 1.0, 0.0),                            # thirteen above a plateau
+            torch.where(i % (7 * v // 90) == 3, 1.0, 0.0),                  # thirteen above a plateau
             torch.where(i < 4000, torch.finfo(dtype).min, 1.0),             # the type's lowest value as a mask
             torch.where(i == 5, 80.0, torch.randn(v, device="cuda"))]       # all but certain
     x = torch.stack(rows).to(dtype)
@@ -948,8 +952,8 @@ def test_logprobs_ties_orders_and_masks(B, dtype):
     assert abs(got["entropy"][0].item() - np.log(v)) < 1e-5
 
 
-def test_logprobs_rows_without_a_distribution(B):
-    v = 6000
+@pytest.mark.parametrize("v", [6000, 66001])
+def test_logprobs_rows_without_a_distribution(B, v):
     base = torch.randn(v, device="cuda")
     inf, nan = float("inf"), float("nan")
     x = torch.stack([base] * 5)
@@ -973,7 +977,7 @@ def test_logprobs_rows_without_a_distribution(B):
 def test_logprobs_captured_on_a_shared_workspace(B):
     ws = B.make_logprobs_workspace(4, 3)
     outs, graphs, ins = [], [], []
-    for n, v in ((1, 50000), (4, 9000)):
+    for n, v in ((1, 100000), (4, 70000)):
         x = torch.randn(n, v, device="cuda")
         t = torch.zeros(n, dtype=torch.int32, device="cuda")
         o = [torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"),
