@@ -107,13 +107,25 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&o)[8], 
                                               pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
 }
 
+// The CTAs of a group, first and last, the slots of this CTA's partial state
+// and of the first's (the others' are their CTAs' first).
+struct Parts {
+  int first, last, slot, slot0;
+  __device__ __forceinline__ Parts(int64_t begin, int64_t end, int64_t total, int G, int c)
+      : first(paged::cta_at(begin, total, G)),
+        last(paged::cta_at(end - 1, total, G)),
+        slot(paged::partial_slot(c, begin, total, G)),
+        slot0(paged::partial_slot(first, begin, total, G)) {}
+};
+
 // The group's state from the consumer warps' states in `sm`: finished if
-// whole, else this CTA's partial; the last of the group's CTAs c_first ..
-// c_last to arrive merges them in CTA order.  Warp h takes query head h, lane
-// l its dims [8 l, 8 l + 8).
+// whole, else this CTA's partial; the last of the group's CTAs to arrive
+// merges them in CTA order.  Warp h takes query head h, lane l its dims
+// [8 l, 8 l + 8).  (The parts are worked out before the tiles arrive: their
+// divisions took up to 2000 cycles here.)
 template <typename QT>
 __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* flags, const Args& p, QT* a_head0,
-                                             int64_t begin, int64_t end, int64_t total, int G, int c) {
+                                             const Parts& parts) {
   const int tid = threadIdx.x, h = tid >> 5, lane = tid & 31;
   named_bar_sync(kBarConsumers, kConsumerThreads);
   float M = -INFINITY;
@@ -135,12 +147,12 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
     O[6] = fmaf(x1.z, scl, O[6]); O[7] = fmaf(x1.w, scl, O[7]);
   }
   QT* dst = a_head0 + h * kHeadDim + 8 * lane;
-  const int c_first = paged::cta_at(begin, total, G), c_last = paged::cta_at(end - 1, total, G);
+  const int c_first = parts.first, c_last = parts.last;
   if (c_first == c_last) {
     if (!flags[0]) store8(dst, O, 1.0f / L);
     return;
   }
-  float* P = p.part + (int64_t)paged::partial_slot(c, begin, total, G) * kPartFloats;
+  float* P = p.part + (int64_t)parts.slot * kPartFloats;
   float4* po = reinterpret_cast<float4*>(P + 8 + h * kHeadDim + 8 * lane);
   po[0] = make_float4(O[0], O[1], O[2], O[3]);
   po[1] = make_float4(O[4], O[5], O[6], O[7]);
@@ -156,7 +168,7 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
     const int last = atomicAdd(&p.tickets[c_first], 1u) == (uint32_t)(c_last - c_first);
     if (last) p.tickets[c_first] = 0;
     flags[1] = last && !flags[0];
-    __threadfence();  // the ticket before the others' partials
+    if (last) __threadfence();  // the ticket before the others' partials
   }
   named_bar_sync(kBarMerge, kConsumerThreads);
   if (!flags[1]) return;
@@ -164,9 +176,6 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
 #pragma unroll
   for (int i = 0; i < 8; ++i) O2[i] = 0.f;
   constexpr int kBatch = 8;  // partials loaded per round trip
-  // (the first part's slot depends on where the group begins, the others are
-  // their CTAs' first)
-  const int first = paged::partial_slot(c_first, begin, total, G);
   for (int q0 = c_first; q0 <= c_last; q0 += kBatch) {
     float mq[kBatch], lq[kBatch];
     float4 x0[kBatch], x1[kBatch];
@@ -175,7 +184,7 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
       // (behind the last part the last once more, at weight 0: loads without
       // a condition stay in flight together)
       const int q = min(q0 + t, c_last);
-      const float* Pq = p.part + (int64_t)(q == c_first ? first : 2 * q) * kPartFloats;
+      const float* Pq = p.part + (int64_t)(q == c_first ? parts.slot0 : 2 * q) * kPartFloats;
       mq[t] = __ldcg(Pq + h);
       lq[t] = __ldcg(Pq + 4 + h);
       x0[t] = __ldcg(reinterpret_cast<const float4*>(Pq + 8 + h * kHeadDim + 8 * lane));
@@ -310,6 +319,7 @@ __global__ void __launch_bounds__(kTokThreads, MINB)
       named_bar_sync(kBarConsumers, kConsumerThreads);
       st.reset();
     }
+    const Parts parts(cur.begin, cur.end, total, G, c);
     for (int64_t u = cur.begin > u0 ? cur.begin : u0; u < t1; ++u, ++k) {
       if ((int)(k % kConsumers) != warp) continue;
       const int s = (int)(k % kStages);
@@ -338,7 +348,7 @@ __global__ void __launch_bounds__(kTokThreads, MINB)
       attn_store_state_mma(mst, msm);
     else
       attn_store_state(st, msm);
-    finish_group(msm, flags, p, a + (row * p.n_kv + cur.j) * kGroup * kHeadDim, cur.begin, cur.end, total, G, c);
+    finish_group(msm, flags, p, a + (row * p.n_kv + cur.j) * kGroup * kHeadDim, parts);
     if (cur.end >= u1) break;
     cur.next(p, sh);
   }
