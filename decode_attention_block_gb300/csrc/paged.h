@@ -13,6 +13,7 @@
 // leaves the group to the next.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #if defined(__CUDACC__)
@@ -123,11 +124,19 @@ SPARK_HD int64_t quotient(int64_t a, int64_t b) {
   return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// CTAs that share `total` units out of at most `most`, with at least `least`
-// units each
-SPARK_HD int32_t ctas_for(int64_t total, int32_t least, int32_t most) {
-  const int64_t g = quotient(total, least);
-  return g < 1 ? 1 : g > most ? most : (int32_t)g;
+// CTAs that share `total` units of `groups` groups (0 < groups <= total) out of
+// at most `most`: a whole number of parts a group, so that where groups are
+// alike no CTA meets two of them.  A part has at least `least` units, and a
+// group of U units at most sqrt(spread U) parts: more would cost more to merge
+// than they save.
+SPARK_HD int32_t ctas_for(int64_t total, int64_t groups, int32_t least, float spread, int32_t most) {
+  if (groups >= most) return most;
+  const int64_t units = quotient(total, groups);
+  int64_t parts = quotient(units, least);
+  const int64_t cap = (int64_t)sqrtf(spread * (float)units);
+  if (parts > cap) parts = cap;
+  if (parts < 1) parts = 1;
+  return groups * parts > most ? most : (int32_t)(groups * parts);
 }
 
 SPARK_HD int64_t share_begin(int64_t total, int32_t G, int32_t c) { return quotient(total * c, G); }

@@ -49,7 +49,7 @@ struct TokSmem {
   static constexpr int kBars = kO + kConsumers * 4 * kHeadDim * 4;
   static constexpr int kFlags = kBars + 2 * kStages * 8;
   static constexpr int kPrefix = kFlags + 16;
-  static constexpr int kBytes = kPrefix + 8 * (SPARK_MAX_BATCH + 2 + kTokThreads / 32);
+  static constexpr int kBytes = kPrefix + 8 * (SPARK_MAX_BATCH + 2 + kTokThreads / 16);
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 (128B swizzle)
 };
 
@@ -367,8 +367,8 @@ cudaError_t launch_token(const Args& p, const void* k, const void* v, cudaStream
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
   if (e != cudaSuccess) return e;
   // two CTAs per SM, and no more than the tables' rows could give work to
-  const int64_t tiles = (int64_t)p.max_pages * (p.page_size / kTile);
-  const int64_t most = ((int64_t)p.n_seqs * p.n_kv * p.max_q * tiles + kMinUnits - 1) / kMinUnits;
+  const int64_t parts = ((int64_t)p.max_pages * (p.page_size / kTile) + kMinUnits - 1) / kMinUnits;
+  const int64_t most = (int64_t)p.n_seqs * p.n_kv * p.max_q * parts;
   int grid = kMinB * device_sm_count();
   if (grid > paged::kMaxCtas) grid = paged::kMaxCtas;
   if (grid > most) grid = (int)most;

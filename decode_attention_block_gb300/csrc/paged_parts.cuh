@@ -57,13 +57,15 @@ __device__ __forceinline__ Seq load_seq(const Args& p, int s) {
 
 // prefix[s] = units of the sequences before s (all KV heads), s <= n_seqs, in
 // shared memory; every thread of the block calls this and `sums` has room for
-// one value per warp.  CTA 0 reports sequences that make no sense.
+// two values per warp.  Returns the number of groups.  CTA 0 reports sequences
+// that make no sense.
 template <int NT>
-__device__ __forceinline__ void work_prefix(const Args& p, const Shape& sh, int64_t* prefix, int64_t* sums) {
+__device__ __forceinline__ int64_t work_prefix(const Args& p, const Shape& sh, int64_t* prefix, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kPer = (SPARK_MAX_BATCH + NT - 1) / NT;
   const int per = (p.n_seqs + NT - 1) / NT;
   int64_t u[kPer], mine = 0;
+  int groups = 0;  // (a call's tokens are at most 2^17)
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int s = tid * per + i;
@@ -72,6 +74,7 @@ __device__ __forceinline__ void work_prefix(const Args& p, const Shape& sh, int6
       const Seq q = load_seq(p, s);
       if (q.bad && blockIdx.x == 0) atomicOr(p.err, kErrIndex);
       if (q.n > 0) u[i] = (int64_t)p.n_kv * units_of(q, sh);
+      groups += groups_of(q, sh);
     }
     mine += u[i];
   }
@@ -82,7 +85,11 @@ __device__ __forceinline__ void work_prefix(const Args& p, const Shape& sh, int6
     if (lane >= o) run += up;
   }
   if (lane == 31) sums[warp] = run;
+  groups = __reduce_add_sync(0xffffffffu, groups);
+  if (lane == 0) sums[NT / 32 + warp] = groups;
   __syncthreads();
+  int64_t all = 0;
+  for (int w = 0; w < NT / 32; ++w) all += sums[NT / 32 + w];
   int64_t before = run - mine;
   for (int w = 0; w < warp; ++w) before += sums[w];
 #pragma unroll
@@ -93,6 +100,7 @@ __device__ __forceinline__ void work_prefix(const Args& p, const Shape& sh, int6
     if (i < per && s == p.n_seqs - 1) prefix[p.n_seqs] = before;
   }
   __syncthreads();
+  return all * p.n_kv;
 }
 
 // A walk over the groups a share of the work list meets.
@@ -140,6 +148,13 @@ struct Cursor {
   }
 };
 
+// What a group of U units is split into at most is sqrt(kSpread U) parts.  One
+// token at 12000 with one KV head: 33 us with as many parts as there are CTAs,
+// 19.1 at 2.5, 19.8 at 5, 21.6 at 10; at 700 9.2 at 5, 10.0 at 2.5.  And a
+// whole number of parts a group: one token at 100 with 4 KV heads took 12.9 us
+// on 7 CTAs that met two groups each, 7.6 on one a group.
+constexpr float kSpread = 4.f;
+
 // A CTA's share of the list: the units [u0, u1) of `total`, shared by G CTAs,
 // and the group it begins with.  Without a tile (c >= G, or a share that is
 // all lead): no more is set.
@@ -147,8 +162,8 @@ struct Share {
   int64_t total, u0, u1;
   int G;
   Cursor cur;
-  __device__ __forceinline__ bool cut(int c, int least, int most) {
-    G = total > 0 ? ctas_for(total, least, most) : 0;
+  __device__ __forceinline__ bool cut(int c, int64_t groups, int least, int most) {
+    G = total > 0 ? ctas_for(total, groups, least, kSpread, most) : 0;
     if (c >= G) return false;
     u0 = share_begin(total, G, c);
     u1 = share_begin(total, G, c + 1);
@@ -157,7 +172,7 @@ struct Share {
 };
 
 // Every thread of the block calls this, with room for SPARK_MAX_BATCH + 2 +
-// NT / 32 values in shared memory; the block is in step afterwards.  Up to 32
+// NT / 16 values in shared memory; the block is in step afterwards.  Up to 32
 // sequences (the common decode and prefill calls) each warp keeps one per
 // lane and finds its share without another thread: 900 cycles against 4000
 // by way of the prefix sums in shared memory.
@@ -181,7 +196,9 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
     }
     const int64_t first = run - per_head * p.n_kv;
     share.total = __shfl_sync(0xffffffffu, run, 31);
-    const bool any = share.cut(c, least, most);
+    const int groups = sh.gt == 1 && p.max_q == 1 ? __popc(__ballot_sync(0xffffffffu, q.n != 0))
+                                                  : __reduce_add_sync(0xffffffffu, groups_of(q, sh));
+    const bool any = share.cut(c, (int64_t)groups * p.n_kv, least, most);
     __syncthreads();
     if (!any) return false;
     // the last sequence that begins at or before u0 (one without units shares its beginning with the next)
@@ -201,9 +218,9 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
     }
     return cur.begin < share.u1;
   }
-  work_prefix<NT>(p, sh, room, room + SPARK_MAX_BATCH + 2);
+  const int64_t groups = work_prefix<NT>(p, sh, room, room + SPARK_MAX_BATCH + 2);
   share.total = room[p.n_seqs];
-  if (!share.cut(c, least, most)) return false;
+  if (!share.cut(c, groups, least, most)) return false;
   int lo = 0, hi = p.n_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

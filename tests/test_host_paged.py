@@ -88,8 +88,16 @@ int main() {
     const int groups = 1 + rng() % 30, lead = it % 4;
     for (int i = 0; i < groups; ++i) begin.push_back(begin.back() + lead + 1 + rng() % (it % 3 ? 9 : 300));
     const int64_t total = begin.back();
-    const int G = ctas_for(total, 1 + rng() % 6, 1 + rng() % 40);
-    CHECK(G >= 1 && G <= total, "ctas_for");
+    const int least = 1 + rng() % 6, most = 1 + rng() % 40;
+    const float spread = 0.5f + rng() % 8;
+    const int G = ctas_for(total, groups, least, spread, most);
+    CHECK(G >= 1 && G <= total && G <= most, "ctas_for");
+    // groups alike, as many CTAs as they want: a whole number each
+    const int units = 1 + rng() % 900, H = ctas_for((int64_t)units * groups, groups, least, spread, 1 << 20);
+    CHECK(H % groups == 0 && (H == groups || (H / groups * least <= units && (float)(H / groups) * (H / groups) <= spread * units)),
+          "parts of groups alike");
+    for (int i = 0; i <= groups; ++i)
+      CHECK(share_begin((int64_t)units * groups, H, i * (H / groups)) == (int64_t)i * units, "shares of groups alike");
     std::set<int> slots, tickets;
     for (int i = 0; i < groups; ++i) {
       const int64_t b = begin[i] + lead, e = begin[i + 1];
