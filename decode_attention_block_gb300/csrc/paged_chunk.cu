@@ -46,6 +46,10 @@ namespace {
 
 using namespace chunk;
 
+// Units per CTA at least (one sequence of 8 tokens at 1000, bf16 queries: 13.6
+// us at 1, 14.6 at 2; one of 4 at 500 13.1 and 14.4).
+constexpr int kMinUnits = 1;
+
 static_assert(kRows == kGroup * paged::kChunkTokens, "a row per query head of a token");
 
 // Q halves and ring slots: 224 KB either way
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* prefix = reinterpret_cast<int64_t*>(base + S::kRing);
   const int c = blockIdx.x;
   paged::Share share;
-  if (!paged::find_share<kThreads>(p, sh, c, kMinTiles, gridDim.x, prefix, share)) {
+  if (!paged::find_share<kThreads>(p, sh, c, kMinUnits, gridDim.x, prefix, share)) {
     if (tid == 0) p.joins[c].n_rows = 0;
     return;
   }

@@ -40,7 +40,6 @@ constexpr uint32_t kGroupBytes = LINES * kAtom;
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O starts at 0
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
-constexpr int kMinTiles = 2;                    // units per CTA at least
 
 // L2 policies of the pool's rows.  A sequence of one group reads its rows
 // once: they make room first, or they would drive out the rows of longer

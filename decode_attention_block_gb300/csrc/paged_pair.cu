@@ -33,6 +33,10 @@ namespace {
 using namespace chunk;
 
 constexpr int kPairTokens = 2 * paged::kChunkTokens;
+// Units per pair at least (one sequence of 48 tokens at 1000, bf16 queries: 15.7
+// us at 2, 16.9 at 1, 18.2 at 3).
+constexpr int kMinUnits = 2;
+
 template <bool SPLIT>
 struct PairSmem {
   static constexpr int kQ = SPLIT ? 2 : 1;
@@ -187,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int64_t* prefix = reinterpret_cast<int64_t*>(base + S::kRingK);
   const int c = blockIdx.x >> 1;
   paged::Share share;
-  if (!paged::find_share<kThreads>(p, sh, c, kMinTiles, gridDim.x >> 1, prefix, share)) {  // both CTAs of the pair
+  if (!paged::find_share<kThreads>(p, sh, c, kMinUnits, gridDim.x >> 1, prefix, share)) {  // both CTAs of the pair
     if (tid == 0 && rank == 0) p.joins[c].n_rows = 0;
     return;
   }
