@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int half = 0; half < 2; ++half, ++k) {
         const int s = (int)(k % NS);
         if (!wait(&full[s], (k / NS) & 1)) return;
-        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot, kGroupBytes<2>), a0 = tc::desc_k_major(q_addr + 2 * half * S::kQLine);
+        const uint64_t b0 = tc::desc_k_major(ring + s * kSlot, kGroupBytes<2>);
+        const uint64_t a0 = tc::desc_k_major(q_addr + 2 * half * S::kQLine);
         if (one) {
 #pragma unroll
           for (int line = 0; line < 2; ++line)
@@ -311,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     softmax_warps<QT, 1, false>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, q_raw, s_full, pv_done, flags, nullptr,
-                                       warp, tid - 64, [&] { mbar_arrive(q_full); }, [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
+                                warp, tid - 64, [&] { mbar_arrive(q_full); },
+                                [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
   }
   tc::fence_before();
   __syncthreads();

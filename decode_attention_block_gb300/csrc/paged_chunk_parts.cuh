@@ -261,7 +261,8 @@ template <typename QT, int RANKS, bool STAGE, typename ArriveQ, typename ArriveP
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
                                               uint64_t* q_raw, uint64_t* s_full, uint64_t* pv_done,
-                                              volatile int* flags, unsigned char* stage, int warp, int st, ArriveQ arrive_q, ArriveP arrive_p) {
+                                              volatile int* flags, unsigned char* stage, int warp, int st,
+                                              ArriveQ arrive_q, ArriveP arrive_p) {
   const int quad = warp & 3, lane = st & 31, tok0 = rank * paged::kChunkTokens;
   const int row = quad * 32 + lane;
   const int prow = rank * kRows + row;  // the row in a partial state
@@ -411,8 +412,9 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
             const uint4 w = *reinterpret_cast<const uint4*>(mine + rr * kStageRow + (lane & 3) * 16);
             const int t = tok0 + 8 * quad + (rr >> 2);
             if (t < g.n_tok)
-              *reinterpret_cast<uint4*>(out + (((cur.seq.q0 + g.tok + t) * (int64_t)p.n_kv + cur.j) * kGroup + (rr & 3)) * kHeadDim +
-                                        d + (lane & 3) * 8) = w;
+              *reinterpret_cast<uint4*>(
+                  out + (((cur.seq.q0 + g.tok + t) * (int64_t)p.n_kv + cur.j) * kGroup + (rr & 3)) * kHeadDim + d +
+                  (lane & 3) * 8) = w;
           }
           __syncwarp();
         } else if constexpr (!kSplit) {
@@ -494,7 +496,8 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
 // in CTA order: block (share c, 32 rows of the group that begins in it and
 // goes on).  Lane r has row r, warp w the dims 4 w + 32 i, so that the reads
 // are the partial states' lines; the rows then go through shared memory to be
-// written line by line.
+// written line by line.  Bound by the states' bytes, 40 MB for a chunk of 4096
+// tokens on 76 pairs: 11 us from HBM, less where they are still in L2.
 constexpr int kJoinRows = 32;
 constexpr int kJoinWarps = 8;
 constexpr int kJoinDims = kHeadDim / 4 / kJoinWarps;  // float4 of a thread
