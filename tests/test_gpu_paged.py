@@ -399,6 +399,30 @@ def test_bad_entries_raise_the_error_word(B):
     assert bool((bad[:3] == 0).all())
 
 
+def test_calls_at_once_on_their_own_workspaces(B):
+    """Streams side by side, each with its workspace and its kind of batch:
+    the results of the same calls one after another."""
+    g = _geom(B)
+    runs = []
+    for i, (name, q_type) in enumerate((("decode", F32), ("mixed", F32), ("pairs", BF16), ("big_chunk", F32),
+                                        ("verify", BF16), ("long", BF16))):
+        case = Case(SETS[name], page=(16, 64)[i % 2], seed=20 + i)
+        case.fill()
+        q = torch.randn(case.n_tokens, 4096, generator=case.g, device="cuda").to(q_type)
+        ws = B.make_paged_workspace(g)
+        want, got = torch.zeros_like(q), torch.zeros_like(q)
+        runs.append((q, B.PagePool(case.k, case.v), case.batch(B), want, got, ws, torch.cuda.Stream(), case))
+    for q, pool, batch, want, _, ws, _, _ in runs:
+        B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, want, ws)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, pool, batch, _, got, ws, st, _ in runs:
+            B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, got, ws, stream=st)
+    torch.cuda.synchronize()
+    for _, _, _, want, got, ws, _, _ in runs:
+        assert B.spark_attn_error_word(ws) == 0 and torch.equal(want, got)
+
+
 @pytest.mark.parametrize("q_type", [F32, BF16])
 @pytest.mark.parametrize("page", [16, 64])
 def test_bad_pages_under_long_chunks(B, page, q_type):
