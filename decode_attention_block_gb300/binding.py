@@ -13,7 +13,6 @@ importing the binding without it raises instead of falling back to anything.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
 from dataclasses import dataclass, field
 
@@ -202,12 +201,15 @@ def declared_symbols() -> list[str]:
 # the current stream's handle without building a torch.cuda.Stream around it
 # (0.2 us a call instead of 3)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device without asking whether CUDA is initialised: a call's
+# tensors have done that
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -322,11 +324,13 @@ def _rows(t: torch.Tensor, name: str) -> tuple:
     are contiguous but may lie apart (a slice of a fused projection's output)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPE_CODE:
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must be a matrix with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], _DTYPE_CODE[t.dtype]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1], code
 
 
 @dataclass
@@ -376,7 +380,6 @@ class PagedBatch(_CachedC):
                                int(self.table.shape[1]), int(self.n_tokens), int(self.max_q_len))
 
 
-_GET_C, _GET_BYTES, _GET_HEADS = operator.attrgetter("_c"), operator.itemgetter(1), operator.itemgetter(2)
 
 
 def _pool_differs(got, want) -> ValueError:
@@ -386,21 +389,21 @@ def _pool_differs(got, want) -> ValueError:
 
 def _pool_c(geom: SparkGeom, pool: PagePool) -> SparkPagePool:
     c, _, heads = pool.to_c()
-    want = (geom.n_kv, geom.head_dim, torch.cuda.current_device())
+    want = (geom.n_kv, geom.head_dim, _current_device())
     if heads != want:
         raise _pool_differs(heads, want)
     return c
 
 
 def _pools_c(geom: SparkGeom, pools) -> ctypes.Array:
-    built = list(map(_GET_C, pools))
+    built = [p._c for p in pools]
     if None in built:
         built = [p.to_c() for p in pools]
-    want = (geom.n_kv, geom.head_dim, torch.cuda.current_device())
-    for heads in set(map(_GET_HEADS, built)):
+    want = (geom.n_kv, geom.head_dim, _current_device())
+    for heads in {b[2] for b in built}:
         if heads != want:
             raise _pool_differs(heads, want)
-    return (SparkPagePool * len(built)).from_buffer_copy(b"".join(map(_GET_BYTES, built)))
+    return (SparkPagePool * len(built)).from_buffer_copy(b"".join([b[1] for b in built]))
 
 
 # ---------------------------------------------------------------------------
@@ -612,7 +615,7 @@ def spark_paged_append(geom: SparkGeom, k: torch.Tensor, v: torch.Tensor, pool: 
         raise ValueError("k and v must have the same dtype and row stride")
     pc, bc = _pool_c(geom, pool), batch.to_c()
     _check(load().spark_paged_append(ctypes.byref(geom), kp, vp, ld, dt, ctypes.byref(pc), ctypes.byref(bc),
-                                     _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+                                     _dev_ptr(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_paged_append")
 
 
@@ -626,7 +629,7 @@ def spark_paged_attention(geom: SparkGeom, q: torch.Tensor, pool: PagePool, laye
     pc, bc = _pool_c(geom, pool), batch.to_c()
     _check(load().spark_paged_attention(ctypes.byref(geom), qp, ld, dt, ctypes.byref(pc), int(layer_class),
                                         ctypes.byref(bc), _dev_ptr(a, "a", q.dtype), _dev_ptr(ws, "workspace"),
-                                        ws.numel() * ws.element_size(), _stream(stream)), "spark_paged_attention")
+                                        ws.nbytes, _stream(stream)), "spark_paged_attention")
 
 
 def spark_attn_paged(geom: SparkGeom, h: torch.Tensor, weights: LayerWeights, pool: PagePool, layer_class: int,
@@ -640,8 +643,8 @@ def spark_attn_paged(geom: SparkGeom, h: torch.Tensor, weights: LayerWeights, po
     _check(load().spark_attn_paged(ctypes.byref(geom), _dev_ptr(h, "h", torch.float32), ctypes.byref(wc),
                                    ctypes.byref(pc), int(layer_class), ctypes.byref(bc), _positions(positions),
                                    _dev_ptr(out, "out", torch.float32), _dev_ptr(ws, "workspace"),
-                                   ws.numel() * ws.element_size(), _dev_ptr(paged_ws, "paged workspace"),
-                                   paged_ws.numel() * paged_ws.element_size(), _stream(stream)), "spark_attn_paged")
+                                   ws.nbytes, _dev_ptr(paged_ws, "paged workspace"),
+                                   paged_ws.nbytes, _stream(stream)), "spark_attn_paged")
 
 
 def spark_pages_workspace_bytes(n_pages: int, n_slots: int) -> int:
@@ -667,7 +670,7 @@ def spark_pages_remap(geom: SparkGeom, pools, table: torch.Tensor, parent: torch
                                     n, int(table.shape[1]), _dev_ptr(parent, "parent", i32),
                                     _dev_ptr(keep_len, "keep_len", i32), _dev_ptr(new_len, "new_len", i32),
                                     _dev_ptr(new_table, "new_table", i32), _dev_ptr(ws, "workspace"),
-                                    ws.numel() * ws.element_size(), _stream(stream)), "spark_pages_remap")
+                                    ws.nbytes, _stream(stream)), "spark_pages_remap")
 
 
 def spark_pages_compact(geom: SparkGeom, pools, table: torch.Tensor, new_table: torch.Tensor, n_live: torch.Tensor,
@@ -680,7 +683,7 @@ def spark_pages_compact(geom: SparkGeom, pools, table: torch.Tensor, new_table: 
     _check(load().spark_pages_compact(ctypes.byref(geom), _pools_c(geom, pools), len(pools),
                                       _dev_ptr(table, "table", i32), int(table.shape[0]), int(table.shape[1]),
                                       _dev_ptr(new_table, "new_table", i32), _dev_ptr(n_live, "n_live", i32),
-                                      _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+                                      _dev_ptr(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_pages_compact")
 
 
@@ -711,7 +714,7 @@ def spark_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, logprob: t
                                        _dev_ptr(entropy, "entropy", torch.float32),
                                        _dev_ptr(top_ids, "top_ids", torch.int32) if k else None,
                                        _dev_ptr(top_logprobs, "top_logprobs", torch.float32) if k else None,
-                                       _dev_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+                                       _dev_ptr(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_token_logprobs")
 
 
