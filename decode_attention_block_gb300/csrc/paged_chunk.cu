@@ -341,7 +341,7 @@ cudaError_t launch_chunk(const Args& p, const void* k, const void* v, cudaStream
   if (grid > paged::kMaxChunkCtas) grid = paged::kMaxChunkCtas;
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), S::kAlloc, st, mk, mv, mq, mq8, p, box);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_join<QT, 1>, dim3(grid, kRows / kJoinRows), dim3(32 * kJoinWarps), 0, st, p);
+  return launch_pdl(k_paged_join<QT, 1>, dim3(grid, kRows / kJoinRows, kJoinSplit), dim3(32 * kJoinWarps), 0, st, p);
 }
 
 }  // namespace

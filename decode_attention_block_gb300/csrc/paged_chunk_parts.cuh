@@ -494,14 +494,22 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
 
 // Join the partial states of the groups that a share's border cut, the parts
 // in CTA order: block (share c, 32 rows of the group that begins in it and
-// goes on).  Lane r has row r, warp w the dims 4 w + 32 i, so that the reads
-// are the partial states' lines; the rows then go through shared memory to be
-// written line by line.  Bound by the states' bytes, 40 MB for a chunk of 4096
-// tokens on 76 pairs: 11 us from HBM, less where they are still in L2.
+// goes on, 256 / kJoinSplit dims).  Lane r has row r, warp w the dims 4 w + 32
+// i, so that the reads are the partial states' lines; the rows then go through
+// shared memory to be written line by line.  Bound by what an SM takes in from
+// L2 where a few groups have many parts (one sequence of 8 tokens at 12000: 26.7
+// us with whole rows to a block, 25.0 with halves, 24.1 with quarters, but one
+// of 48 at 300 13.8, 14.2 and 15.5), by the states' bytes where there are many
+// groups (40 MB for a chunk of 4096 tokens on 76 pairs).  Four parts at a time
+// read the last one more often than they hide: 228 against 224 us there.
 constexpr int kJoinRows = 32;
 constexpr int kJoinWarps = 8;
-constexpr int kJoinDims = kHeadDim / 4 / kJoinWarps;  // float4 of a thread
-constexpr int kJoinStride = kHeadDim + 4;             // floats of a row in shared memory
+constexpr int kJoinParts = 2;                         // loaded at a time
+constexpr int kJoinSplit = 2;                         // blocks that share a row
+constexpr int kJoinWidth = kHeadDim / kJoinSplit;     // dims of a block
+constexpr int kJoinDims = kJoinWidth / 4 / kJoinWarps;  // float4 of a thread
+constexpr int kJoinStride = kJoinWidth + 4;           // floats of a row in shared memory
+static_assert(kJoinDims >= 1, "a float4 a thread at least");
 
 template <typename QT, int RANKS>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_constant__ Args p) {
@@ -509,14 +517,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_con
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.y * kJoinRows, row = row0 + lane;
+  const int row0 = blockIdx.y * kJoinRows, row = row0 + lane, d0 = blockIdx.z * kJoinWidth;
   const paged::Join* jp = p.joins + c;
   const int4 a = __ldcg(reinterpret_cast<const int4*>(jp));  // row0, n_rows, head, last
   if (row0 >= a.y) return;
   const longlong2 bt = __ldcg(reinterpret_cast<const longlong2*>(jp) + 1);  // begin, total
   const int G = __ldcg(&jp->G), last = a.w;
   constexpr int kAll = RANKS * kRows;
-  constexpr int kUnroll = 2;
   float M = -INFINITY, L = 0.f;
   float4 O[kJoinDims];
 #pragma unroll
@@ -524,11 +531,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_con
   // (the first part's slot depends on where the group begins, the others are
   // their CTAs' first)
   const int first = paged::partial_slot(c, bt.x, bt.y, G);
-  for (int q0 = c; q0 <= last; q0 += kUnroll) {
-    float m[kUnroll], l[kUnroll];
-    float4 x[kUnroll][kJoinDims];
+#pragma unroll 1
+  for (int q0 = c; q0 <= last; q0 += kJoinParts) {
+    float m[kJoinParts], l[kJoinParts];
+    float4 x[kJoinParts][kJoinDims];
 #pragma unroll
-    for (int t = 0; t < kUnroll; ++t) {
+    for (int t = 0; t < kJoinParts; ++t) {
       // (behind the last part the last once more, at weight 0: loads without
       // a condition stay in flight together)
       const int q = min(q0 + t, last), slot = q == c ? first : 2 * q;
@@ -537,11 +545,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_con
       l[t] = __ldcg(part + kAll * (kHeadDim + 1) + row);
 #pragma unroll
       for (int i = 0; i < kJoinDims; ++i)
-        x[t][i] = __ldcg(reinterpret_cast<const float4*>(part) + (warp + kJoinWarps * i) * kAll + row);
+        x[t][i] = __ldcg(reinterpret_cast<const float4*>(part) + (d0 / 4 + warp + kJoinWarps * i) * kAll + row);
       if (q0 + t > last) m[t] = -INFINITY;
     }
 #pragma unroll
-    for (int t = 0; t < kUnroll; ++t) {
+    for (int t = 0; t < kJoinParts; ++t) {
       const float mn = fmaxf(M, m[t]);
       // (a part in which the row saw nothing holds no state)
       const float s = M == -INFINITY ? 0.f : exp2f(M - mn), r = m[t] == -INFINITY ? 0.f : exp2f(m[t] - mn);
@@ -563,13 +571,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_con
     rows[lane * (kJoinStride / 4) + warp + kJoinWarps * i] =
         make_float4(O[i].x * inv, O[i].y * inv, O[i].z * inv, O[i].w * inv);
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kJoinRows / kJoinWarps; ++i) {
-    const int r = warp + kJoinWarps * i;
+  // 8 dims a thread
+  constexpr int kThreadsRow = kJoinWidth / 8;
+  for (int e = threadIdx.x; e < kJoinRows * kThreadsRow; e += 32 * kJoinWarps) {
+    const int r = e / kThreadsRow, d = 8 * (e % kThreadsRow);
     if (row0 + r >= a.y) break;
-    const float4 x = rows[r * (kJoinStride / 4) + 2 * lane], y = rows[r * (kJoinStride / 4) + 2 * lane + 1];
+    const float4 x = rows[r * (kJoinStride / 4) + d / 4], y = rows[r * (kJoinStride / 4) + d / 4 + 1];
     QT* dst = static_cast<QT*>(p.a) + (((int64_t)a.x + ((row0 + r) >> 2)) * p.n_kv + a.z) * (kGroup * kHeadDim) +
-              ((row0 + r) & 3) * kHeadDim + 8 * lane;
+              ((row0 + r) & 3) * kHeadDim + d0 + d;
     if constexpr (std::is_same<QT, float>::value) {
       reinterpret_cast<float4*>(dst)[0] = x;
       reinterpret_cast<float4*>(dst)[1] = y;

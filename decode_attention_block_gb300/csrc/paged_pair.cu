@@ -443,7 +443,7 @@ cudaError_t launch_pair(const Args& p, const void* k, const void* v, int box_k, 
   if (pairs < 1) pairs = 1;
   e = launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), S::kAlloc, st, mk, mv, mq, mq8, p, box_k, box_v);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_join<QT, 2>, dim3(pairs, 2 * kRows / kJoinRows), dim3(32 * kJoinWarps), 0, st, p);
+  return launch_pdl(k_paged_join<QT, 2>, dim3(pairs, 2 * kRows / kJoinRows, kJoinSplit), dim3(32 * kJoinWarps), 0, st, p);
 }
 
 }  // namespace
