@@ -10,7 +10,7 @@ namespace spark {
 cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                    cudaStream_t st);
 
-// The same, token by token (any pool type).
+// The same for single tokens (any pool type).
 cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                cudaStream_t st);
 

@@ -185,7 +185,8 @@ __device__ __forceinline__ bool find_share(const Args& p, const Shape& sh, int c
     Seq q = {0, 0, 0, false};
     if (lane < p.n_seqs) q = load_seq(p, lane);
     if (q.bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.err, kErrIndex);
-    // (a single token's units are its one group's)
+    // (a single token's units are its one group's; groups of one are of calls
+    // with max_q 1, but not asked for that the compiler spills registers here)
     const Group only = group_of(q, sh, 0);
     const int64_t per_head = q.n == 0 ? 0 : sh.gt == 1 && p.max_q == 1 ? only.tile1 - only.tile0 : units_of(q, sh);
     int64_t run = per_head * p.n_kv;

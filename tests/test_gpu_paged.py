@@ -193,10 +193,19 @@ def test_attention_bf16_pool(B, name, full, q_type):
 
 
 @pytest.mark.parametrize("q_type", [F32, BF16])
-@pytest.mark.parametrize("name", ["one", "decode", "verify", "chunk_at", "mixed"])
+@pytest.mark.parametrize("name", ["one", "two", "decode", "verify", "chunk", "chunk_at", "mixed", "pairs", "edges",
+                                  "long_chunk", "far_short"])
 @pytest.mark.parametrize("full", [True, False])
 def test_attention_f32_pool(B, name, full, q_type):
     _check_attention(B, Case(SETS[name], page=32, dtype=F32, seed=3), q_type, full, window=64)
+
+
+@pytest.mark.parametrize("n_kv,page", [(1, 16), (3, 48), (5, 80), (8, 256)])
+@pytest.mark.parametrize("window", [0, 1, 9, 17, 300])
+def test_f32_pool_heads_pages_windows(B, n_kv, page, window):
+    for q_type in (F32, BF16):
+        _check_attention(B, Case(SETS["mixed"], n_kv=n_kv, page=page, dtype=F32, seed=page, pad=5), q_type, window == 0,
+                         window=window or 512, q_pad=8)
 
 
 @pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 256, 1024])
@@ -405,8 +414,8 @@ def test_calls_at_once_on_their_own_workspaces(B):
     g = _geom(B)
     runs = []
     for i, (name, q_type) in enumerate((("decode", F32), ("mixed", F32), ("pairs", BF16), ("big_chunk", F32),
-                                        ("verify", BF16), ("long", BF16))):
-        case = Case(SETS[name], page=(16, 64)[i % 2], seed=20 + i)
+                                        ("verify", BF16), ("long", BF16), ("edges", F32))):
+        case = Case(SETS[name], page=(16, 64)[i % 2], dtype=F32 if name == "edges" else BF16, seed=20 + i)
         case.fill()
         q = torch.randn(case.n_tokens, 4096, generator=case.g, device="cuda").to(q_type)
         ws = B.make_paged_workspace(g)
@@ -423,12 +432,12 @@ def test_calls_at_once_on_their_own_workspaces(B):
         assert B.spark_attn_error_word(ws) == 0 and torch.equal(want, got)
 
 
-@pytest.mark.parametrize("q_type", [F32, BF16])
+@pytest.mark.parametrize("q_type,dtype", [(F32, BF16), (BF16, BF16), (BF16, F32)])
 @pytest.mark.parametrize("page", [16, 64])
-def test_bad_pages_under_long_chunks(B, page, q_type):
-    """Entries outside the pool under a chunk that pairs of CTAs take: reported,
-    and the other sequence's results are what they were."""
-    case = Case([(200, 90), (130, 70)], page=page, seed=15)
+def test_bad_pages_under_long_chunks(B, page, q_type, dtype):
+    """Entries outside the pool under long chunks: reported, and the other
+    sequence's results are what they were."""
+    case = Case([(200, 90), (130, 70)], page=page, dtype=dtype, seed=15)
     case.fill()
     g, ws, pool = _geom(B), B.make_paged_workspace(_geom(B)), B.PagePool(case.k, case.v)
     q = torch.randn(160, 4096, generator=case.g, device="cuda").to(q_type)
@@ -446,10 +455,10 @@ def test_bad_pages_under_long_chunks(B, page, q_type):
         B.spark_attn_workspace_init(ws)
 
 
-@pytest.mark.parametrize("q_type", [F32, BF16])
-def test_captured_long_chunks_replay_with_new_lengths(B, q_type):
+@pytest.mark.parametrize("q_type,dtype", [(F32, BF16), (BF16, BF16), (F32, F32)])
+def test_captured_long_chunks_replay_with_new_lengths(B, q_type, dtype):
     g = _geom(B)
-    case = Case([(300, 130), (200, 70)], page=16, seed=16)
+    case = Case([(300, 130), (200, 70)], page=16, dtype=dtype, seed=16)
     case.fill()
     pool, ws = B.PagePool(case.k, case.v), B.make_paged_workspace(g)
     q = torch.randn(200, 4096, generator=case.g, device="cuda").to(q_type)
