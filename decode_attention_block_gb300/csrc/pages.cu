@@ -44,6 +44,10 @@ struct PlanSmem {
   int copy[SPARK_MAX_BATCH];  // its index among the copies, or -1
 };
 
+// bytes of pages' words (4096 pages) that fit beside it without asking for more
+constexpr size_t kPlanDefault = 32 * 1024;
+static_assert(kPlanDefault + sizeof(PlanSmem) + 1024 <= 48 * 1024, "shared memory of a block by default");
+
 // exclusive sum over the block's threads; `total` gets the block's sum
 __device__ __forceinline__ long long block_scan(long long v, PlanSmem& sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -348,7 +352,9 @@ template <int CTAS>
 cudaError_t launch_plan(bool remap, const PlanArgs& p, cudaStream_t st) {
   auto kern = remap ? k_pages_remap<CTAS> : k_pages_compact<CTAS>;
   const size_t smem = CTAS == 1 ? 2 * sizeof(int32_t) * (size_t)p.n_pages : 0;
-  if (smem > 48 * 1024) {
+  // without the attribute the pages' words and the plan's own shared memory
+  // have 48 KB together
+  if (smem > kPlanDefault) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * sizeof(int32_t) * kSmallPages));
     if (e != cudaSuccess) return e;

@@ -1,0 +1,61 @@
+"""The paged cache's operators where their forms meet: pools around the sizes
+at which a plan's shared memory needs more than the default, batches of more
+sequences than a warp has lanes, sequences that no row of an append belongs
+to, the block in a replayed graph.  References, bounds and their derivation:
+``test_gpu_paged.py``."""
+
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from decode_attention_block_gb300 import synth
+from test_gpu_paged import B, BF16, D, F32, SETS, Case, _check_attention, _geom, _i32, _pools, _run_remap, _scattered  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+# ---------------------------------------------------------------------------
+# page plans
+# ---------------------------------------------------------------------------
+
+def _run_compact(B, table, page, n_pages):
+    live = np.unique(table[table >= 0])
+    m = len(live)
+    src, dst = live[live >= m], np.setdiff1d(np.arange(m), live)
+    to = np.arange(n_pages)
+    to[src] = dst
+    x, pools = _pools(B, 1, n_pages, page, 1, BF16, n_pages)
+    after = x.clone()
+    after[:, :, torch.tensor(dst, device="cuda")] = x[:, :, torch.tensor(src, device="cuda")]
+    ws = B.make_pages_workspace(n_pages, len(table))
+    out, n_live = _i32(table), torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.spark_pages_compact(_geom(B, 1), pools, out, out, n_live, ws)
+    assert B.spark_attn_error_word(ws) == 0 and int(n_live) == m
+    assert np.array_equal(out.cpu().numpy(), np.where(table >= 0, to[table], -1))
+    assert torch.equal(x, after)
+
+
+def plans_of(sizes):
+    """Remap and compact on pools of these sizes."""
+    from decode_attention_block_gb300 import binding as B
+    r = np.random.default_rng(7)
+    for n_pages in sizes:
+        lens = r.integers(0, 400, 20)
+        table = _scattered(r, lens, 16, n_pages, 30)
+        _run_remap(B, table, list(range(20)), lens.tolist(), (lens + 17).tolist(), 16, n_pages, layers=1, n_kv=1)
+        _run_compact(B, table, 16, n_pages)
+
+
+@pytest.mark.parametrize("sizes", [(4095, 4096, 4097), (5080, 5086, 5087, 5088, 5500), (6143, 6144, 6145)])
+def test_plans_around_the_default_shared_memory(B, sizes):
+    """In a process of their own: what one call raises for a kernel stays
+    raised for the calls after it."""
+    code = f"import sys; sys.path[:0] = [{HERE!r}, {os.path.dirname(HERE)!r}]; import test_gpu_paged_limits as t; t.plans_of({sizes!r})"
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
