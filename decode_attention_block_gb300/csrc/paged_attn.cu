@@ -649,7 +649,6 @@ __global__ void __launch_bounds__(kAppendThreads)
         if (__ldcg(p.q_start + mid) <= t) lo = mid; else hi = mid - 1;
       }
       const paged::Seq s = paged::load_seq(p, lo);
-      if (s.bad) atomicOr(p.err, kErrIndex);
       if (t >= s.q0 && t < s.q0 + s.n) {  // else: behind the last sequence, or a sequence that makes no sense
         const int pos = s.p0 + (t - s.q0);
         const int pg = paged::page_entry(p, lo, paged::page_col(p, pos));
@@ -661,6 +660,11 @@ __global__ void __launch_bounds__(kAppendThreads)
     }
     to[threadIdx.x] = at;
   }
+  // every sequence is looked at, also one that no token's search ends in, by
+  // the threads that have no token first
+  for (int s = blockIdx.x * kAppendThreads + kAppendThreads - 1 - (int)threadIdx.x; s < p.n_seqs;
+       s += gridDim.x * kAppendThreads)
+    if (paged::load_seq(p, s).bad) atomicOr(p.err, kErrIndex);
   __syncthreads();
   const int words = per * row4;
   for (int w0 = threadIdx.x; w0 < words; w0 += kAppendThreads * kAppendUnroll) {

@@ -59,3 +59,34 @@ def test_plans_around_the_default_shared_memory(B, sizes):
     code = f"import sys; sys.path[:0] = [{HERE!r}, {os.path.dirname(HERE)!r}]; import test_gpu_paged_limits as t; t.plans_of({sizes!r})"
     res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stderr[-2000:]
+
+
+# ---------------------------------------------------------------------------
+# appends
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("start", [(0, 6, 4, 4), (0, 6, 6, 9), (0, 6, 6, 5), (0, 6, -1, -1), (0, 2, 6, 2**31 - 1)])
+def test_append_reports_sequences_that_no_row_belongs_to(B, start):
+    """Starts that decrease or pass the rows of the call are reported by the
+    append too, where the search of no row ends in them."""
+    case = Case([(100, 6), (40, 0), (50, 0)], page=16, seed=5)
+    case.q_start = _i32(start)
+    g, ws, pool = _geom(B), B.make_paged_workspace(_geom(B)), B.PagePool(case.k, case.v)
+    kv = torch.ones(6, 1024, device="cuda")
+    B.spark_paged_append(g, kv, kv, pool, case.batch(B, n_tokens=6, max_q=6), ws)
+    assert B.spark_attn_error_word(ws) == 2
+    case.q_start = _i32((0, 6, 6, 6))
+    B.spark_paged_append(g, kv, kv, pool, case.batch(B, n_tokens=6, max_q=6), ws)
+    assert B.spark_attn_error_word(ws) == 0
+
+
+def test_append_reports_one_sequence_of_many(B):
+    """1024 sequences, one of them with an end behind the rows of the call."""
+    case = Case([(3, 1)] * 1024, n_kv=1, page=16, seed=5)
+    g, ws, pool = _geom(B, 1), B.make_paged_workspace(_geom(B, 1)), B.PagePool(case.k, case.v)
+    kv = torch.ones(1024, D, device="cuda")
+    B.spark_paged_append(g, kv, kv, pool, case.batch(B), ws)
+    assert B.spark_attn_error_word(ws) == 0
+    case.q_start[1023:] = _i32([1024, 1025])          # the last but one takes the last row
+    B.spark_paged_append(g, kv, kv, pool, case.batch(B, max_q=2), ws)
+    assert B.spark_attn_error_word(ws) == 2
