@@ -226,6 +226,24 @@ def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
     return t.data_ptr()
 
 
+def _not_here(t, name: str) -> Exception:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return TypeError(f"{name} must be a CUDA tensor")
+    return ValueError(f"{name} is on device {t.get_device()}, the current device is {_current_device()}")
+
+
+def _here(t: torch.Tensor, name: str, dtype=None) -> int:
+    """As _dev_ptr, of a tensor on the current device: the call goes to its
+    stream, and its memory alone the kernels are sure to reach."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != _current_device():
+        raise _not_here(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
 def _check(status: int, where: str) -> None:
     if status != SPARK_OK:
         raise SparkError(status, where)
@@ -320,10 +338,11 @@ class MlpWeights(_CachedC):
 
 
 def _rows(t: torch.Tensor, name: str) -> tuple:
-    """Address, row stride (elements) and dtype code of a matrix whose rows
-    are contiguous but may lie apart (a slice of a fused projection's output)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    """Address, row stride (elements) and dtype code of a matrix on the current
+    device whose rows are contiguous but may lie apart (a slice of a fused
+    projection's output)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != _current_device():
+        raise _not_here(t, name)
     code = _DTYPE_CODE.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
@@ -370,16 +389,26 @@ class PagedBatch(_CachedC):
     max_q_len: int
     _c: object = field(default=None, init=False, repr=False, compare=False)
 
-    def _build_c(self) -> SparkPagedBatch:
+    def _build_c(self) -> tuple:
+        """The C struct and the device its arrays are on."""
         if self.table.dim() != 2 or self.q_start.shape != (self.table.shape[0] + 1,) or \
                 self.seq_len.shape != (self.table.shape[0],):
             raise ValueError("table must be [n_seqs, max_pages], q_start [n_seqs + 1], seq_len [n_seqs]")
-        return SparkPagedBatch(_dev_ptr(self.table, "table", torch.int32),
-                               _dev_ptr(self.q_start, "q_start", torch.int32),
-                               _dev_ptr(self.seq_len, "seq_len", torch.int32), int(self.table.shape[0]),
-                               int(self.table.shape[1]), int(self.n_tokens), int(self.max_q_len))
+        c = SparkPagedBatch(_dev_ptr(self.table, "table", torch.int32),
+                            _dev_ptr(self.q_start, "q_start", torch.int32),
+                            _dev_ptr(self.seq_len, "seq_len", torch.int32), int(self.table.shape[0]),
+                            int(self.table.shape[1]), int(self.n_tokens), int(self.max_q_len))
+        device = self.table.get_device()
+        if self.q_start.get_device() != device or self.seq_len.get_device() != device:
+            raise ValueError("table, q_start and seq_len must be on the same device")
+        return c, device
 
 
+def _batch_c(batch: PagedBatch) -> SparkPagedBatch:
+    c, device = batch.to_c()
+    if device != _current_device():
+        raise _not_here(batch.table, "the batch's table")
+    return c
 
 
 def _pool_differs(got, want) -> ValueError:
@@ -613,9 +642,9 @@ def spark_paged_append(geom: SparkGeom, k: torch.Tensor, v: torch.Tensor, pool: 
         raise ValueError(f"k and v must be [n_tokens, {kv_dim}]")
     if vdt != dt or vld != ld:
         raise ValueError("k and v must have the same dtype and row stride")
-    pc, bc = _pool_c(geom, pool), batch.to_c()
+    pc, bc = _pool_c(geom, pool), _batch_c(batch)
     _check(load().spark_paged_append(ctypes.byref(geom), kp, vp, ld, dt, ctypes.byref(pc), ctypes.byref(bc),
-                                     _dev_ptr(ws, "workspace"), ws.nbytes, _stream(stream)),
+                                     _here(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_paged_append")
 
 
@@ -626,9 +655,9 @@ def spark_paged_attention(geom: SparkGeom, q: torch.Tensor, pool: PagePool, laye
     qp, ld, dt = _rows(q, "q")
     if q.shape != (batch.n_tokens, geom.n_q * geom.head_dim) or a.shape != q.shape:
         raise ValueError(f"q and a must be [n_tokens, {geom.n_q * geom.head_dim}]")
-    pc, bc = _pool_c(geom, pool), batch.to_c()
+    pc, bc = _pool_c(geom, pool), _batch_c(batch)
     _check(load().spark_paged_attention(ctypes.byref(geom), qp, ld, dt, ctypes.byref(pc), int(layer_class),
-                                        ctypes.byref(bc), _dev_ptr(a, "a", q.dtype), _dev_ptr(ws, "workspace"),
+                                        ctypes.byref(bc), _here(a, "a", q.dtype), _here(ws, "workspace"),
                                         ws.nbytes, _stream(stream)), "spark_paged_attention")
 
 
@@ -639,11 +668,14 @@ def spark_attn_paged(geom: SparkGeom, h: torch.Tensor, weights: LayerWeights, po
     out [n_tokens, hidden]; positions: each row's rope position (host)."""
     if h.shape != (batch.n_tokens, geom.hidden) or out.shape != h.shape or len(positions) != batch.n_tokens:
         raise ValueError("h and out must be [n_tokens, hidden], with one position per row")
-    wc, pc, bc = weights.to_c(), _pool_c(geom, pool), batch.to_c()
-    _check(load().spark_attn_paged(ctypes.byref(geom), _dev_ptr(h, "h", torch.float32), ctypes.byref(wc),
+    wc, pc, bc = weights.to_c(), _pool_c(geom, pool), _batch_c(batch)
+    for name in ("norm_w", "qkv_w", "g_w", "o_w"):
+        if getattr(weights, name).get_device() != _current_device():
+            raise _not_here(getattr(weights, name), name)
+    _check(load().spark_attn_paged(ctypes.byref(geom), _here(h, "h", torch.float32), ctypes.byref(wc),
                                    ctypes.byref(pc), int(layer_class), ctypes.byref(bc), _positions(positions),
-                                   _dev_ptr(out, "out", torch.float32), _dev_ptr(ws, "workspace"),
-                                   ws.nbytes, _dev_ptr(paged_ws, "paged workspace"),
+                                   _here(out, "out", torch.float32), _here(ws, "workspace"),
+                                   ws.nbytes, _here(paged_ws, "paged workspace"),
                                    paged_ws.nbytes, _stream(stream)), "spark_attn_paged")
 
 
@@ -666,10 +698,10 @@ def spark_pages_remap(geom: SparkGeom, pools, table: torch.Tensor, parent: torch
     if table.dim() != 2 or new_table.shape != table.shape or not parent.shape == keep_len.shape == new_len.shape == (n,):
         raise ValueError("table and new_table must be [n_slots, max_pages], the lists [n_slots]")
     i32 = torch.int32
-    _check(load().spark_pages_remap(ctypes.byref(geom), _pools_c(geom, pools), len(pools), _dev_ptr(table, "table", i32),
-                                    n, int(table.shape[1]), _dev_ptr(parent, "parent", i32),
-                                    _dev_ptr(keep_len, "keep_len", i32), _dev_ptr(new_len, "new_len", i32),
-                                    _dev_ptr(new_table, "new_table", i32), _dev_ptr(ws, "workspace"),
+    _check(load().spark_pages_remap(ctypes.byref(geom), _pools_c(geom, pools), len(pools), _here(table, "table", i32),
+                                    n, int(table.shape[1]), _here(parent, "parent", i32),
+                                    _here(keep_len, "keep_len", i32), _here(new_len, "new_len", i32),
+                                    _here(new_table, "new_table", i32), _here(ws, "workspace"),
                                     ws.nbytes, _stream(stream)), "spark_pages_remap")
 
 
@@ -681,9 +713,9 @@ def spark_pages_compact(geom: SparkGeom, pools, table: torch.Tensor, new_table: 
         raise ValueError("table and new_table must be [n_slots, max_pages], n_live one element")
     i32 = torch.int32
     _check(load().spark_pages_compact(ctypes.byref(geom), _pools_c(geom, pools), len(pools),
-                                      _dev_ptr(table, "table", i32), int(table.shape[0]), int(table.shape[1]),
-                                      _dev_ptr(new_table, "new_table", i32), _dev_ptr(n_live, "n_live", i32),
-                                      _dev_ptr(ws, "workspace"), ws.nbytes, _stream(stream)),
+                                      _here(table, "table", i32), int(table.shape[0]), int(table.shape[1]),
+                                      _here(new_table, "new_table", i32), _here(n_live, "n_live", i32),
+                                      _here(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_pages_compact")
 
 
@@ -709,12 +741,12 @@ def spark_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, logprob: t
         raise ValueError("targets, logprob and entropy must be [n]")
     if k and (top_ids.shape != (n, k) or top_logprobs.shape != (n, k)):
         raise ValueError("top_ids and top_logprobs must be [n, k]")
-    _check(load().spark_token_logprobs(lp, ld, dt, n, vocab, _dev_ptr(targets, "targets", torch.int32), k,
-                                       _dev_ptr(logprob, "logprob", torch.float32),
-                                       _dev_ptr(entropy, "entropy", torch.float32),
-                                       _dev_ptr(top_ids, "top_ids", torch.int32) if k else None,
-                                       _dev_ptr(top_logprobs, "top_logprobs", torch.float32) if k else None,
-                                       _dev_ptr(ws, "workspace"), ws.nbytes, _stream(stream)),
+    _check(load().spark_token_logprobs(lp, ld, dt, n, vocab, _here(targets, "targets", torch.int32), k,
+                                       _here(logprob, "logprob", torch.float32),
+                                       _here(entropy, "entropy", torch.float32),
+                                       _here(top_ids, "top_ids", torch.int32) if k else None,
+                                       _here(top_logprobs, "top_logprobs", torch.float32) if k else None,
+                                       _here(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_token_logprobs")
 
 
