@@ -665,7 +665,8 @@ def spark_attn_paged(geom: SparkGeom, h: torch.Tensor, weights: LayerWeights, po
                      batch: PagedBatch, positions, out: torch.Tensor, ws: torch.Tensor, paged_ws: torch.Tensor,
                      stream=None) -> None:
     """The attention block for the batch's new tokens on a paged cache: h,
-    out [n_tokens, hidden]; positions: each row's rope position (host)."""
+    out [n_tokens, hidden]; positions: each row's rope position (host; a
+    captured call keeps those of its capture, whatever the lengths become)."""
     if h.shape != (batch.n_tokens, geom.hidden) or out.shape != h.shape or len(positions) != batch.n_tokens:
         raise ValueError("h and out must be [n_tokens, hidden], with one position per row")
     wc, pc, bc = weights.to_c(), _pool_c(geom, pool), _batch_c(batch)

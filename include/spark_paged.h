@@ -16,11 +16,11 @@
  * table[s][x / page_size], row x % page_size.
  *
  * Page tables, starts and lengths are DEVICE arrays, read when the work
- * runs, so a captured call replays with new lengths.  What the host cannot
- * see the kernels check: an entry out of range raises bit 2 of the
- * workspace's error word (spark_attn_error_word), no memory outside the
- * buffers is read or written, and the results of the sequence it belongs to
- * are unspecified.
+ * runs, so a captured call replays with new lengths (spark_attn_paged with
+ * the rope positions of its capture, see there).  What the host cannot see
+ * the kernels check: an entry out of range raises bit 2 of the workspace's
+ * error word (spark_attn_error_word), no memory outside the buffers is read
+ * or written, and the results of the sequence it belongs to are unspecified.
  *
  * A workspace serves one call at a time: calls that share one are ordered on
  * a stream, captured graphs that share one do not run at once.  After an
@@ -123,8 +123,12 @@ int spark_paged_attention(const spark_geom* g, const void* q, int64_t q_ld, int3
  *   h          [n_tokens][hidden] fp32 device; out the same, may equal h.
  *   positions  [n_tokens] HOST int32: the rope position of each row (they
  *              are the call's only host array; the rows of the cache follow
- *              seq_len alone).  Rows behind q_start[n_seqs] take any
- *              position >= 0, and their out rows are unspecified.
+ *              seq_len alone).  They are read during the call, as
+ *              spark_attn_decode's are: a captured call replays with the
+ *              positions of its capture whatever seq_len says by then, so a
+ *              graph of it serves a step again, not the next token.
+ *              Rows behind q_start[n_seqs] take any position >= 0, and their
+ *              out rows are unspecified.
  *   n_tokens   1 .. SPARK_MAX_BATCH here.
  *   workspace  >= spark_attn_workspace_bytes(g, n_tokens), as for
  *              spark_attn_decode; paged_workspace as for

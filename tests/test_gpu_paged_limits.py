@@ -90,3 +90,55 @@ def test_append_reports_one_sequence_of_many(B):
     case.q_start[1023:] = _i32([1024, 1025])          # the last but one takes the last row
     B.spark_paged_append(g, kv, kv, pool, case.batch(B, max_q=2), ws)
     assert B.spark_attn_error_word(ws) == 2
+
+
+# ---------------------------------------------------------------------------
+# the block in a graph
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("is_full", [True, False])
+def test_a_captured_block_replays_with_new_lengths_and_its_own_positions(B, is_full):
+    """Tables, starts, lengths and rows are read at the replay, the rope
+    positions are those of the capture."""
+    geom = _geom(B, window=100)
+    wl = synth.Workload("paged", "", "bf16", [50], [synth.LayerSpec(is_full, 0)], seed=80)
+    lw = B.LayerWeights(**synth.make_weights(wl, 0, "cuda"))
+    cls = B.SPARK_FULL if is_full else B.SPARK_SLIDING
+    case = Case([(300, 5), (200, 3)], page=16, seed=21)
+    for s, c in enumerate(case.ctx):        # every row: the replays end sequences elsewhere
+        p, r = case.where(s)
+        case.k[p, r], case.v[p, r] = case.rows_k[s], case.rows_v[s]
+    k0, v0 = case.k.clone(), case.v.clone()
+    ws, pws = B.make_workspace(geom, 8), B.make_paged_workspace(geom)
+    pool, batch = B.PagePool(case.k, case.v), case.batch(B, max_q=8)
+    h = torch.randn(8, 2560, generator=case.g, device="cuda")
+    out, ref = torch.zeros_like(h), torch.zeros_like(h)
+    positions = list(range(295, 300)) + list(range(197, 200))
+
+    def call(to, pos):
+        B.spark_attn_paged(geom, h, lw, pool, cls, batch, pos, to, ws, pws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(out, positions)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, positions)
+    for lens, new in (((300, 200), (5, 3)), ((130, 64), (1, 7)), ((299, 17), (8, 0))):
+        case.seq_len.copy_(_i32(lens))
+        case.q_start.copy_(_i32([0, new[0], sum(new)]))
+        h.normal_(generator=case.g)
+        got = []
+        for replay in (True, False):
+            case.k.copy_(k0), case.v.copy_(v0)
+            graph.replay() if replay else call(ref, positions)
+            torch.cuda.synchronize()
+            got.append((case.k.clone(), case.v.clone()))
+        iv = torch.int16
+        assert torch.equal(out, ref)
+        assert all(torch.equal(x.view(iv), y.view(iv)) for x, y in zip(*got))
+    # other positions are another result: what a replay cannot take up
+    call(ref, [p + 1 for p in positions])
+    assert not torch.equal(out, ref)
+    assert B.spark_attn_error_word(ws) == 0 and B.spark_attn_error_word(pws) == 0
