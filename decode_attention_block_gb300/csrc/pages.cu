@@ -4,8 +4,8 @@
 // Who holds a page is computed from the tables of the call, not kept: a page
 // is free when no slot keeps it.  One array `state` of a word per page says
 //   remap    INT_MAX free, -1 kept whole by some slot, s >= 0 kept in part,
-//            slot s the lowest of those that keep it so (an atomicMin, so the
-//            outcome does not depend on the order of arrivals);
+//            slot s the lowest of those that keep it so (atomicMin of either,
+//            so the outcome does not depend on the order of arrivals);
 //   compact  0 unused, 1 used, then the page's rank among those that move.
 // The plan is a few dependent passes over the tables and the pages' words.
 // Small pools and tables (kSmallPages, kSmallEntries) take one CTA with the
@@ -159,10 +159,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_remap(const __grid_const
         const int pg = __ldcg(old + i);
         if (pg < 0 || pg >= p.n_pages)
           bad = true;
-        else if (i < whole)
-          pl.state[pg] = -1;  // the lowest value there is: no order of arrival matters
         else
-          atomicMin(&pl.state[pg], s);
+          atomicMin(&pl.state[pg], i < whole ? -1 : s);
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) p.head->bad = 1;

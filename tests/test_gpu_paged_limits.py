@@ -61,6 +61,18 @@ def test_plans_around_the_default_shared_memory(B, sizes):
     assert res.returncode == 0, res.stderr[-2000:]
 
 
+def test_pages_kept_whole_and_in_part_at_once(B):
+    """Every page of a sequence kept whole by some of 300 slots and in part by
+    others: whole wins, whoever comes first."""
+    page, n_pages, width = 16, 700, 12
+    table = np.full((300, width), -1)
+    table[17, :10] = np.random.default_rng(3).permutation(n_pages)[:10]
+    keep = [(7 * s) % 160 + 1 for s in range(300)]
+    for parents in ([17] * 300, [17 if s % 3 else -1 for s in range(300)]):
+        kept = [k if p >= 0 else 0 for k, p in zip(keep, parents)]
+        assert _run_remap(B, table, parents, kept, [k + 1 for k in kept], page, n_pages, layers=1, n_kv=1) == 0
+
+
 # ---------------------------------------------------------------------------
 # appends
 # ---------------------------------------------------------------------------
