@@ -134,7 +134,7 @@ int spark_attn_workspace_init(void* workspace, size_t workspace_bytes, void* str
 
 /* Read and clear the workspace's device error word.  SYNCHRONISES `stream`.
  * Bits: 1 = a pipeline wait ran out of time, 2 = an index outside its buffer
- * was skipped. */
+ * was skipped, 4 = too few free pages (spark_pages_remap). */
 int spark_attn_error_word(void* workspace, size_t workspace_bytes, uint32_t* word, void* stream);
 
 /* One decode step of the attention block for `batch` independent sequences

@@ -102,16 +102,18 @@ int spark_paged_append(const spark_geom* g, const void* k, const void* v, int64_
  *         BF16), row t at element t * q_ld (q_ld >= n_q * head_dim, rows
  *         16-byte aligned): rotated queries.
  *   a     device [n_tokens][n_q * head_dim] of the same type: un-gated
- *         attention output, row t written for every token t.  Does not
- *         overlap q.
+ *         attention output, a row written for every new token of a sequence,
+ *         the others left as they were.  Does not overlap q.
  * fp32 queries meet a bf16 pool as q = hi + lo in bf16 (16 significant
- * bits), the probabilities too; bf16 queries with probabilities rounded to
- * bf16.  An fp32 pool is read by fp32 arithmetic.
+ * bits), the probabilities too.  bf16 queries meet it as they are, with
+ * probabilities of 16 significant bits where max_q_len is 1 and rounded to
+ * bf16 (8 bits) where it is more.  An fp32 pool is read by fp32 arithmetic.
  * Rows that no token of the sequence attends to may hold anything, NaN
  * included; a row that one of its new tokens attends to is expected finite
  * (a non-finite V row may reach every new token of its sequence).
- * max_q_len, with n_tokens and n_seqs, chooses the kernel, not the results
- * beyond rounding: give the true bound.
+ * max_q_len, with n_tokens and n_seqs, chooses the kernel, and with it the
+ * order of the sums and the rounding of the probabilities, not the results
+ * beyond these: give the true bound.
  * workspace and errors as spark_paged_append. */
 int spark_paged_attention(const spark_geom* g, const void* q, int64_t q_ld, int32_t dtype,
                           const spark_page_pool* pool, int32_t layer_class, const spark_paged_batch* batch,
