@@ -333,9 +333,9 @@ int spark_attn_paged(const spark_geom* g, const float* h, const spark_layer_weig
   int s;
   if ((s = check_geom(g)) != SPARK_OK) return s;
   if ((s = check_weights(w, true, true)) != SPARK_OK) return s;
-  if ((s = check_pool(g, pool)) != SPARK_OK) return s;
+  if ((s = check_pool(pool)) != SPARK_OK) return s;
   if (layer_class != SPARK_FULL && layer_class != SPARK_SLIDING) return SPARK_ERR_INVALID_ARG;
-  if ((s = check_paged_batch(batch, pool)) != SPARK_OK) return s;
+  if ((s = check_paged_batch(batch)) != SPARK_OK) return s;
   const int32_t m = batch->n_tokens;
   if ((s = check_batch(m)) != SPARK_OK) return s;
   if (!positions) return SPARK_ERR_INVALID_ARG;

@@ -20,8 +20,8 @@ int spark_paged_append(const spark_geom* g, const void* k, const void* v, int64_
                        size_t workspace_bytes, void* stream) {
   int s;
   if ((s = check_geom(g)) != SPARK_OK) return s;
-  if ((s = check_pool(g, pool)) != SPARK_OK) return s;
-  if ((s = check_paged_batch(batch, pool)) != SPARK_OK) return s;
+  if ((s = check_pool(pool)) != SPARK_OK) return s;
+  if ((s = check_paged_batch(batch)) != SPARK_OK) return s;
   if ((s = check_rows(k, dtype, ld, (int64_t)g->n_kv * kHeadDim)) != SPARK_OK) return s;
   if ((s = check_rows(v, dtype, ld, (int64_t)g->n_kv * kHeadDim)) != SPARK_OK) return s;
   if ((s = check_paged_ws(workspace, workspace_bytes)) != SPARK_OK) return s;
@@ -34,9 +34,9 @@ int spark_paged_attention(const spark_geom* g, const void* q, int64_t q_ld, int3
                           void* a, void* workspace, size_t workspace_bytes, void* stream) {
   int s;
   if ((s = check_geom(g)) != SPARK_OK) return s;
-  if ((s = check_pool(g, pool)) != SPARK_OK) return s;
+  if ((s = check_pool(pool)) != SPARK_OK) return s;
   if (layer_class != SPARK_FULL && layer_class != SPARK_SLIDING) return SPARK_ERR_INVALID_ARG;
-  if ((s = check_paged_batch(batch, pool)) != SPARK_OK) return s;
+  if ((s = check_paged_batch(batch)) != SPARK_OK) return s;
   if ((s = check_rows(q, dtype, q_ld, (int64_t)g->n_q * kHeadDim)) != SPARK_OK) return s;
   if (!a || !aligned16(a)) return SPARK_ERR_INVALID_ARG;
   // rows of q are read while rows of a are written
@@ -67,7 +67,7 @@ int pages_call(pages::Call* c, const spark_geom* g, const spark_page_pool* pools
   if (!pools || n_pools < 1) return SPARK_ERR_INVALID_ARG;
   if (n_pools > SPARK_MAX_PAGE_POOLS) return SPARK_ERR_UNSUPPORTED;
   for (int i = 0; i < n_pools; ++i) {
-    if ((s = check_pool(g, &pools[i])) != SPARK_OK) return s;
+    if ((s = check_pool(&pools[i])) != SPARK_OK) return s;
     if (pools[i].n_pages != pools[0].n_pages || pools[i].page_size != pools[0].page_size ||
         pools[i].dtype != pools[0].dtype)
       return SPARK_ERR_INVALID_ARG;

@@ -702,10 +702,9 @@ cudaError_t launch_append_t(const Args& p, const void* k, const void* v, int64_t
                     static_cast<CT*>(pv), per, p);
 }
 
-}  // namespace
-
-cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
-                               cudaStream_t st) {
+// single tokens (max_q 1)
+cudaError_t launch_tokens(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
+                          cudaStream_t st) {
   if (cdtype == SPARK_BF16)
     return qdtype == SPARK_BF16 ? launch_token<__nv_bfloat16, __nv_bfloat16>(p, k, v, st)
                                 : launch_token<__nv_bfloat16, float>(p, k, v, st);
@@ -713,9 +712,11 @@ cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, con
                               : launch_token<float, float>(p, k, v, st);
 }
 
+}  // namespace
+
 cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                    cudaStream_t st) {
-  if (p.max_q == 1) return launch_paged_token(p, qdtype, cdtype, k, v, st);
+  if (p.max_q == 1) return launch_tokens(p, qdtype, cdtype, k, v, st);
   if (cdtype != SPARK_BF16)
     return qdtype == SPARK_BF16 ? launch_rows<__nv_bfloat16>(p, k, v, st) : launch_rows<float>(p, k, v, st);
   if (p.max_q <= paged::kChunkTokens) return launch_paged_chunk(p, qdtype, k, v, st);

@@ -31,7 +31,7 @@ constexpr int32_t kMaxScoreRows = 1 << 20;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-inline int check_pool(const spark_geom*, const spark_page_pool* pool) {
+inline int check_pool(const spark_page_pool* pool) {
   if (!pool || !pool->k || !pool->v || !aligned16(pool->k) || !aligned16(pool->v)) return SPARK_ERR_INVALID_ARG;
   if (check_dtype(pool->dtype) != SPARK_OK) return SPARK_ERR_INVALID_ARG;
   if (pool->n_pages < 1 || pool->page_size < 1) return SPARK_ERR_INVALID_ARG;
@@ -41,7 +41,7 @@ inline int check_pool(const spark_geom*, const spark_page_pool* pool) {
   return SPARK_OK;
 }
 
-inline int check_paged_batch(const spark_paged_batch* b, const spark_page_pool* pool) {
+inline int check_paged_batch(const spark_paged_batch* b) {
   if (!b || !b->table || !b->q_start || !b->seq_len || !aligned4(b->table) || !aligned4(b->q_start) ||
       !aligned4(b->seq_len))
     return SPARK_ERR_INVALID_ARG;
@@ -49,7 +49,6 @@ inline int check_paged_batch(const spark_paged_batch* b, const spark_page_pool* 
       b->max_q_len > b->n_tokens)
     return SPARK_ERR_INVALID_ARG;
   if (b->max_pages > SPARK_MAX_TABLE_PAGES || b->n_tokens > SPARK_MAX_PAGED_TOKENS) return SPARK_ERR_UNSUPPORTED;
-  (void)pool;
   return SPARK_OK;
 }
 

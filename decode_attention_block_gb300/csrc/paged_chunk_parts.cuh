@@ -84,11 +84,6 @@ __device__ __forceinline__ void clear_rows(unsigned char* v, int r0, int r1, int
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return ffma2(a, make_float2(1.f, 1.f), b); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -230,7 +225,6 @@ __device__ __forceinline__ void max32(const uint32_t (&s)[32], float (&mx)[4]) {
       mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[i + k + 4])));
 }
 
-// 32 output dims of a row
 // scores of a negative or zero scale
 __device__ __forceinline__ void sign32(uint32_t (&s)[32], float sign) {
 #pragma unroll
@@ -248,15 +242,15 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&o)[
   }
 }
 
+constexpr int kStageRow = 64 + 16;             // bytes of a row of an output stage: 32 bf16 dims, padding
+constexpr int kStageBytes = 32 * kStageRow;    // of a warp
+
 // The four softmax warps (st: their thread, 0 .. 127) of a CTA of RANKS that
 // share a group, one row per thread: scores to probabilities, the running
 // maximum and sum, the output at the group's end.  arrive_q, arrive_p: one
 // lane per warp tells the MMA warp that fp32 queries are in halves, or the
-// probabilities in a buffer.
-// STAGE: whole groups' outputs leave through `stage`.
-constexpr int kStageRow = 64 + 16;             // bytes of a row of an output stage: 32 bf16 dims, padding
-constexpr int kStageBytes = 32 * kStageRow;    // of a warp
-
+// probabilities in a buffer.  STAGE: whole groups' outputs leave through
+// `stage`.
 template <typename QT, int RANKS, bool STAGE, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,

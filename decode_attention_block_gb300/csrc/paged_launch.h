@@ -10,11 +10,7 @@ namespace spark {
 cudaError_t launch_paged_attention(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
                                    cudaStream_t st);
 
-// The same for single tokens (any pool type).
-cudaError_t launch_paged_token(const paged::Args& p, int qdtype, int cdtype, const void* k, const void* v,
-                               cudaStream_t st);
-
-// The same for a bf16 pool on the tensor cores, 32 tokens at a time.
+// The same for chunks on a bf16 pool, on the tensor cores, 32 tokens at a time.
 cudaError_t launch_paged_chunk(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st);
 
 // The same on pairs of CTAs, 64 tokens at a time.
