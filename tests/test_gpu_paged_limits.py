@@ -105,6 +105,71 @@ def test_append_reports_one_sequence_of_many(B):
 
 
 # ---------------------------------------------------------------------------
+# more sequences than a warp has lanes
+# ---------------------------------------------------------------------------
+
+def _many(n, lo, hi, ctx, seed, long=0):
+    """n sequences of lo .. hi new tokens at up to ctx positions, every seventh
+    and the last two without new tokens, `long` of them ten times as long."""
+    r = np.random.default_rng(seed)
+    c, m = r.integers(1, ctx, n), r.integers(lo, hi + 1, n)
+    c[r.permutation(n)[:long]] *= 10
+    c = np.maximum(c, m)
+    m[::7], m[-2:] = 0, 0
+    return [(int(a), int(b)) for a, b in zip(c, m)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,n_kv,ctx,long", [(33, 4, 700, 3), (64, 1, 900, 5), (64, 4, 700, 3), (1024, 1, 90, 9),
+                                             (1024, 4, 60, 0)])
+def test_many_sequences_of_single_tokens(B, n, n_kv, ctx, long, dtype):
+    seqs = _many(n, 1, 1, ctx, n + n_kv, long)
+    _check_attention(B, Case(seqs, n_kv=n_kv, page=16, dtype=dtype, seed=n), F32)
+    _check_attention(B, Case(seqs, n_kv=n_kv, page=48, dtype=dtype, seed=n), BF16, full=False, window=100)
+
+
+@pytest.mark.parametrize("n,hi,n_kv,ctx", [(33, 20, 4, 500), (64, 9, 1, 900), (1024, 3, 1, 60)])
+def test_many_sequences_on_an_f32_pool(B, n, hi, n_kv, ctx):
+    seqs = _many(n, 2, hi, ctx, n, 2)
+    _check_attention(B, Case(seqs, n_kv=n_kv, page=32, dtype=F32, seed=n, pad=3), F32)
+    _check_attention(B, Case(seqs, n_kv=n_kv, page=16, dtype=F32, seed=n, pad=3), BF16, full=False, window=70)
+
+
+@pytest.mark.parametrize("q_type", [F32, BF16])
+@pytest.mark.parametrize("n,lo,hi,n_kv", [(33, 60, 90, 4), (40, 200, 300, 1), (130, 34, 40, 1)])
+def test_many_long_chunks(B, n, lo, hi, n_kv, q_type):
+    """Mostly long ones: pairs of CTAs."""
+    seqs = _many(n, lo, hi, 600, n + lo, 1)
+    case = Case(seqs, n_kv=n_kv, page=64, seed=n)
+    assert 2 * case.n_tokens > n * case.max_q and case.max_q > 32
+    _check_attention(B, case, q_type)
+    _check_attention(B, Case(seqs, n_kv=n_kv, page=16, seed=n), q_type, full=False, window=130)
+
+
+@pytest.mark.parametrize("q_type", [F32, BF16])
+def test_results_repeat_bit_for_bit(B, q_type):
+    """Whatever ran before, and beside them: every kernel, twenty times."""
+    g, ws = _geom(B), B.make_paged_workspace(_geom(B))
+    runs = []
+    for name, dtype in (("decode", BF16), ("long", BF16), ("mixed", BF16), ("big_chunk", BF16), ("far", BF16),
+                        ("edges", F32), ("decode", F32)):
+        case = Case(SETS[name], page=64, seed=len(name), dtype=dtype)
+        case.fill()
+        q = torch.randn(case.n_tokens, 4096, generator=case.g, device="cuda").to(q_type)
+        runs.append((q, B.PagePool(case.k, case.v), case.batch(B), torch.zeros_like(q), case))
+    first = None
+    r = np.random.default_rng(1)
+    for _ in range(20):
+        for i in r.permutation(len(runs)):
+            q, pool, batch, a, _ = runs[i]
+            B.spark_paged_attention(g, q, pool, B.SPARK_FULL, batch, a.fill_(7.0), ws)
+        now = [a.clone() for _, _, _, a, _ in runs]
+        first = first or now
+        assert all(torch.equal(x, y) for x, y in zip(first, now))
+    assert B.spark_attn_error_word(ws) == 0
+
+
+# ---------------------------------------------------------------------------
 # the block in a graph
 # ---------------------------------------------------------------------------
 

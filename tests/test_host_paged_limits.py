@@ -1,11 +1,32 @@
-"""Host checks of the paged cache beside ``test_host_paged.py`` (no GPU):
-tensors of another device than the current one, which the binding refuses
-before a call."""
+"""Host checks of the paged cache beside ``test_host_paged.py`` (no GPU): the
+work list's arithmetic for groups of eight tokens, and tensors of another
+device than the current one, which the binding refuses before a call."""
+
+import shutil
+import subprocess
 
 import pytest
 import torch
 
-from test_host_paged import B  # noqa: F401
+from test_host_paged import CSRC, PROGRAM, B  # noqa: F401
+
+
+def test_index_arithmetic_of_eight_token_groups(tmp_path):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    old = ("for (int step : {1, 4, 32})", "const Shape shapes[] = {{1, 16, 0},")
+    new = ("for (int step : {8, 64})", "const Shape shapes[] = {{8, 16, 0}, {8, 16, 7}, {8, 16, 512}, {8, 16, INT32_MAX}, {1, 16, 0},")
+    text = PROGRAM
+    for a, b in zip(old, new):
+        assert text.count(a) == 1
+        text = text.replace(a, b)
+    src, exe = tmp_path / "paged.cpp", tmp_path / "paged"
+    src.write_text(text)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-I", CSRC,
+                    str(src), "-o", str(exe)], check=True)
+    res = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout[-3000:] + res.stderr[-2000:]
 
 
 # -- devices -------------------------------------------------------------------
