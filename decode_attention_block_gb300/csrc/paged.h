@@ -125,10 +125,13 @@ SPARK_HD int64_t quotient(int64_t a, int64_t b) {
 }
 
 // CTAs that share `total` units of `groups` groups (0 < groups <= total) out of
-// at most `most`: a whole number of parts a group, so that where groups are
-// alike no CTA meets two of them.  A part has at least `least` units, and a
-// group of U units at most sqrt(spread U) parts: more would cost more to merge
-// than they save.
+// at most `most`.  A part has at least `least` units, and a group of U units at
+// most sqrt(spread U) parts: more would cost more to merge than they save.
+// Where these parts of all groups fit `most`, the CTAs are a whole number a
+// group, so that where groups are alike no CTA meets two of them.  Where they
+// do not, all of `most` share the units and borders fall inside groups: 256
+// groups of 33 units (64 sequences, 4 KV heads, a window of 512) on 304 CTAs
+// are all cut and merged.
 SPARK_HD int32_t ctas_for(int64_t total, int64_t groups, int32_t least, float spread, int32_t most) {
   if (groups >= most) return most;
   const int64_t units = quotient(total, groups);

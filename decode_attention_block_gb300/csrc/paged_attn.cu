@@ -12,10 +12,12 @@
 // holding the softmax states: the schedule and the tile of the contiguous
 // cache's decode attention (attn.cu, attn_parts.cuh).
 //
-// Measured: 64 sequences at 512-32768 (4.92 GB of rows) 0.71 ms, 6.95 TB/s,
-// 1.04 of the measured copy bandwidth; 16 at 400-3000 34 us, where the first
-// tile lands after 4 us and the merge takes 4 more; one at 700 8.2 us, all of
-// it latency (share 1.6 us, first tile 1.2, one tile a warp 1.1, merge 2.2).
+// Measured on the GPU (calls in a graph): 64 sequences at 512-32768 (4.92 GB of
+// rows) 0.71 ms, 6.95 TB/s, 1.04 of the measured copy bandwidth; the same with
+// a window of 512 (136 MB) 35 us, 3.9 TB/s, every group cut by a share's border
+// and merged; 16 at 400-3000 28 us; one at 700 9.0 us with bf16 queries, 9.6
+// with fp32 ones, all of it latency (share 1.6 us, first tile 1.2, one tile a
+// warp 1.1, merge 2.2).
 // fp32 pools run the same schedule on the CUDA cores, and chunks over them with
 // a warp for each of eight tokens (k_paged_rows).
 #include <math.h>
@@ -623,9 +625,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 // A CTA takes up to kAppendTokens consecutive tokens: their page rows first,
 // one thread each (a binary search in q_start, then the table), then the
 // rows' words four at a time per thread, whatever rows they are of.  Bound by
-// the rows' bytes where there are many (8370 tokens, 103 MB: 16.5 us, 6.2
-// TB/s; one CTA per token took 80 us, its dependent loads exposed), by the
-// chain of dependent loads where there are few (64 tokens: 3 us).
+// the rows' bytes where there are many (8370 tokens, 103 MB: 16.5 to 19 us, 5.4
+// to 6.2 TB/s; one CTA per token took 80 us, its dependent loads exposed), by
+// the chain of dependent loads where there are few (64 tokens: 3.2 us).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 16;
 constexpr int kAppendUnroll = 4;

@@ -33,7 +33,7 @@
 // read from HBM (32 sequences at 4096-8192, 0.82 GB, bf16 queries: 4 tokens
 // each 132 us, 6.2 TB/s; 32 tokens 147 us, 5.6 TB/s, 707 TFLOP/s), and batches
 // with few longer ones (32 sequences, 4 of them with chunks of ~400 tokens:
-// 107 us; 133 us for fp32 queries, whose MMAs alone take 80); many longer ones
+// 107 us; 131 to 141 us for fp32 queries, whose MMAs alone take 80); many longer ones
 // are bound by what a CTA alone takes in from L2, and go to paged_pair.cu.
 // What it cost on the way (a chunk of 4096 tokens at 4096): 128 columns
 // unrolled in the softmax missed the instruction cache, 566 us; operands of an

@@ -18,9 +18,12 @@
 // probabilities are reported by a lane of each softmax warp of both.  What the
 // MMAs release (slots, scores, output) they release in both CTAs.
 //
-// Measured, a chunk of 4096 tokens at 4096 (4.1e11 multiply-adds x 2): bf16
-// queries 224 us, 1840 TFLOP/s, 0.95 of the measured bf16 rate (240 us on
-// pages of 16 rows); fp32 queries (two MMAs for each) 410 us.  A tile takes
+// Measured, a chunk of 4096 tokens at 4096 (2.1e11 multiply-adds): bf16 queries
+// 223 us in a graph of ten calls, 1850 TFLOP/s, 0.96 of the measured bf16 rate
+// (240 us on pages of 16 rows), and 245 us, 1680 TFLOP/s, where calls follow
+// one another for a second and the power limit holds the SMs at 1.72 GHz (0.96
+// of the rate measured so); fp32 queries (two MMAs for each) 409 and 448 us;
+// with a window of 512 54 and 90 us.  A tile takes
 // 2050 cycles against 2048 of MMA, the softmax 1850 beside it; the rest is the
 // start, the first and last tile of a group (its queries come by TMA, its
 // output leaves through a stage: with both done by the softmax threads row by

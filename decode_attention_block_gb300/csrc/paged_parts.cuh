@@ -151,8 +151,9 @@ struct Cursor {
 // What a group of U units is split into at most is sqrt(kSpread U) parts.  One
 // token at 12000 with one KV head: 33 us with as many parts as there are CTAs,
 // 19.1 at 2.5, 19.8 at 5, 21.6 at 10; at 700 9.2 at 5, 10.0 at 2.5.  And a
-// whole number of parts a group: one token at 100 with 4 KV heads took 12.9 us
-// on 7 CTAs that met two groups each, 7.6 on one a group.
+// whole number of parts a group, where they fit the grid (ctas_for): one token
+// at 100 with 4 KV heads took 12.9 us on 7 CTAs that met two groups each, 7.6
+// on one a group.
 constexpr float kSpread = 4.f;
 
 // A CTA's share of the list: the units [u0, u1) of `total`, shared by G CTAs,

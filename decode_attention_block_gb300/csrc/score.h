@@ -25,11 +25,19 @@ constexpr size_t kTickets = 256;    // uint32 [kMaxSplit], zero between launches
 constexpr size_t kParts = kTickets + 4 * kMaxSplit;
 constexpr size_t kTotal = kParts + sizeof(Part) * kMaxSplit;
 
-// Parts per row.  A part's list of alternatives and the join cost more than the
-// CTAs gain where there are many: one row of 131072 with 20 alternatives takes
-// 22 us whole, 14 in 8 parts and 10.8 in 32; 32 rows 25, 18 and 22; 100 rows 26
-// whole and 28 in two; 511 rows 57 and 72.  Rows of 32001 take 12 us whole and
-// 10.4 in 8 parts at best, and longer as soon as there are 48 of them.
+// Parts per row: more CTAs for few rows, against a list of alternatives for each
+// part and the join.  fp32 rows of 131072, us on the GPU whole and in the parts
+// the rule takes, without alternatives, with 20 and with 32:
+//     32 rows, 8 parts   22.7 and  8.3   28.5 and 16.8   30.0 and 17.9
+//     64 rows, 4 parts   23.2 and 11.4   29.0 and 21.9   30.3 and 24.6
+//    100 rows, 2 parts   23.9 and 16.6   29.3 and 28.1   30.8 and 30.6
+//    128 rows, 2 parts   24.4 and 17.5   29.8 and 28.8   30.9 and 31.0
+// so kMaxSplit ends where a split stops paying (511 rows in two parts: 72
+// against 57).  At 65536 two parts of 86 to 128 rows win without alternatives
+// (13.3 and 10.9) and lose with them (18.8 and 21.3 with 20 for 100 rows), up to
+// 64 rows parts win or lose less than 1 us; rows of 262144 gain throughout (50.3 and 40.0).  Rows of
+// 32001 take 12 us whole and 10.4 in 8 parts at best, and longer as soon as
+// there are 48 of them: below kSplitElems a row stays whole.
 inline int parts_for(int n_rows, int vocab) {
   if (vocab < kSplitElems) return 1;
   int c = kMaxSplit / n_rows;
