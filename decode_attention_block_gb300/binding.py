@@ -1,6 +1,6 @@
 """ctypes binding of ``libspark_attn.so`` (the C ABI in ``include/spark_attn.h``,
-``include/spark_layer.h``, ``include/spark_paged.h`` and
-``include/spark_score.h``).
+``include/spark_layer.h``, ``include/spark_paged.h``, ``include/spark_score.h``
+and ``include/spark_beam.h``).
 
 Argument marshalling only: every step of the block runs in the library's CUDA
 kernels.  Tensors are PyTorch CUDA tensors (PyTorch provides device memory and
@@ -24,10 +24,13 @@ SPARK_OK = 0
 SPARK_PATH_AUTO, SPARK_PATH_GEMV, SPARK_PATH_MMA = 0, 1, 2
 SPARK_F32 = 0
 SPARK_BF16 = 1
+SPARK_FP4 = 2             # pages only
+SPARK_FP4_BLOCK_BYTES = 2304
 SPARK_SLIDING = 0
 SPARK_FULL = 1
 SPARK_MAX_BATCH = 1024
 SPARK_MAX_TOP = 32
+SPARK_MAX_BEAMS = 32
 # bits of a workspace's error word (spark_attn_error_word)
 SPARK_ERRBIT_TIMEOUT, SPARK_ERRBIT_INDEX, SPARK_ERRBIT_PAGES = 1, 2, 4
 
@@ -108,6 +111,16 @@ class SparkPagedBatch(ctypes.Structure):
     ]
 
 
+class SparkBeamState(ctypes.Structure):
+    _fields_ = [
+        ("src", ctypes.c_void_p),
+        ("dst", ctypes.c_void_p),
+        ("pitch", ctypes.c_int64),
+        ("elem", ctypes.c_int32),
+        ("push", ctypes.c_void_p),
+    ]
+
+
 # every symbol include/*.h declares, with its ctypes signature
 _P = ctypes.c_void_p
 _SIGNATURES = {
@@ -153,6 +166,14 @@ _SIGNATURES = {
     "spark_paged_attention": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, ctypes.c_int64, ctypes.c_int32,
                                              ctypes.POINTER(SparkPagePool), ctypes.c_int32,
                                              ctypes.POINTER(SparkPagedBatch), _P, _P, ctypes.c_size_t, _P]),
+    "spark_rope_table": (ctypes.c_int, [ctypes.POINTER(SparkGeom), ctypes.c_int32, ctypes.c_int32, _P, _P]),
+    "spark_paged_rope_append": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                               ctypes.c_int32, _P, ctypes.c_int32, ctypes.POINTER(SparkPagePool),
+                                               ctypes.POINTER(SparkPagedBatch), _P, ctypes.c_int64, _P,
+                                               ctypes.c_size_t, _P]),
+    "spark_paged_read": (ctypes.c_int, [ctypes.POINTER(SparkGeom), ctypes.POINTER(SparkPagePool),
+                                        ctypes.POINTER(SparkPagedBatch), _P, _P, ctypes.c_int64, ctypes.c_int32, _P,
+                                        ctypes.c_size_t, _P]),
     "spark_attn_paged": (ctypes.c_int, [ctypes.POINTER(SparkGeom), _P, ctypes.POINTER(SparkLayerWeights),
                                         ctypes.POINTER(SparkPagePool), ctypes.c_int32,
                                         ctypes.POINTER(SparkPagedBatch), ctypes.POINTER(ctypes.c_int32), _P, _P,
@@ -166,6 +187,12 @@ _SIGNATURES = {
     "spark_logprobs_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "spark_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P,
                                             ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "spark_beam_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "spark_beam_select": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_int32, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P,
+                                         ctypes.c_size_t, _P]),
+    "spark_beam_reorder": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.POINTER(SparkBeamState), ctypes.c_int32,
+                                          _P, ctypes.c_size_t, _P]),
     "spark_attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "spark_attn_abi_version": (ctypes.c_int32, []),
 }
@@ -355,7 +382,9 @@ def _rows(t: torch.Tensor, name: str) -> tuple:
 @dataclass
 class PagePool(_CachedC):
     """One layer's pages as CUDA tensors ``k``, ``v`` of shape
-    ``[n_pages, page_size, n_kv, head_dim]`` (float32 or bfloat16)."""
+    ``[n_pages, page_size, n_kv, head_dim]`` (float32 or bfloat16), or, held in
+    4 bits, uint8 ``[n_pages, page_size / 16, n_kv, 2304]`` (the header's
+    blocks)."""
 
     k: torch.Tensor
     v: torch.Tensor
@@ -364,15 +393,20 @@ class PagePool(_CachedC):
     def _build_c(self) -> tuple:
         """The C struct, its bytes (for arrays of them) and (n_kv, head_dim, device)."""
         dt = self.k.dtype
-        if dt not in _DTYPE_CODE:
-            raise TypeError(f"pages must be float32 or bfloat16, got {dt}")
+        if dt not in _DTYPE_CODE and dt != torch.uint8:
+            raise TypeError(f"pages must be float32, bfloat16 or uint8 (4 bits), got {dt}")
         if self.k.dim() != 4 or self.k.shape != self.v.shape:
             raise ValueError("k and v must both be [n_pages, page_size, n_kv, head_dim]")
-        c = SparkPagePool(_dev_ptr(self.k, "k", dt), _dev_ptr(self.v, "v", dt), int(self.k.shape[0]),
-                          int(self.k.shape[1]), _DTYPE_CODE[dt])
+        n_pages, page_size, n_kv, head_dim = (int(x) for x in self.k.shape)
+        code = _DTYPE_CODE.get(dt)
+        if code is None:
+            if head_dim != SPARK_FP4_BLOCK_BYTES:
+                raise ValueError(f"4-bit pages must be [n_pages, page_size / 16, n_kv, {SPARK_FP4_BLOCK_BYTES}]")
+            code, page_size, head_dim = SPARK_FP4, 16 * page_size, 256
+        c = SparkPagePool(_dev_ptr(self.k, "k", dt), _dev_ptr(self.v, "v", dt), n_pages, page_size, code)
         if self.v.get_device() != self.k.get_device():
             raise ValueError("k and v must be on the same device")
-        return c, bytes(c), (int(self.k.shape[2]), int(self.k.shape[3]), self.k.get_device())
+        return c, bytes(c), (n_kv, head_dim, self.k.get_device())
 
 
 @dataclass
@@ -648,6 +682,67 @@ def spark_paged_append(geom: SparkGeom, k: torch.Tensor, v: torch.Tensor, pool: 
            "spark_paged_append")
 
 
+def spark_rope_table(geom: SparkGeom, layer_class: int, rope: torch.Tensor, stream=None) -> None:
+    """rope [n_positions, r / 2, 2] (float32, r the class's rotary dim) = (cos,
+    sin) of the class's angles."""
+    _check(load().spark_rope_table(ctypes.byref(geom), int(layer_class), _rope_rows(geom, layer_class, rope),
+                                   _here(rope, "rope", torch.float32), _stream(stream)), "spark_rope_table")
+
+
+def _rope_rows(geom: SparkGeom, layer_class: int, rope: torch.Tensor) -> int:
+    half = (geom.full_rotary_dim if layer_class == SPARK_FULL else geom.head_dim) // 2
+    if rope.dim() != 3 or rope.shape[1] != half or rope.shape[2] != 2:
+        raise ValueError(f"rope must be [n_positions, {half}, 2]")
+    return int(rope.shape[0])
+
+
+def spark_paged_rope_append(geom: SparkGeom, q, k: torch.Tensor, v: torch.Tensor, layer_class: int, rope: torch.Tensor,
+                            pool: PagePool, batch: PagedBatch, q_out, ws: torch.Tensor, stream=None) -> None:
+    """Rotate the new tokens' queries q [n_tokens, n_q * 256] into q_out (which
+    may be q; both None: no queries) and their keys, and write the rows k, v
+    [n_tokens, n_kv * 256] into their pages.  q, k and v have one row stride
+    (slices of a fused projection's rows); rope: spark_rope_table's."""
+    kp, ld, dt = _rows(k, "k")
+    vp, vld, vdt = _rows(v, "v")
+    n, kv_dim, q_dim = batch.n_tokens, geom.n_kv * geom.head_dim, geom.n_q * geom.head_dim
+    if k.shape != (n, kv_dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [n_tokens, {kv_dim}]")
+    qp, op, old = None, None, 0
+    if q is not None:
+        qp, qld, qdt = _rows(q, "q")
+        op, old, odt = _rows(q_out, "q_out")
+        if q.shape != (n, q_dim) or q_out.shape != q.shape:
+            raise ValueError(f"q and q_out must be [n_tokens, {q_dim}]")
+        if n == 1:  # a single row has no stride
+            ld = vld = qld
+        if qdt != dt or odt != dt or qld != ld:
+            raise ValueError("q, q_out, k and v must have the same dtype, q, k and v the same row stride")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if vdt != dt or vld != ld:
+        raise ValueError("k and v must have the same dtype and row stride")
+    pc, bc = _pool_c(geom, pool), _batch_c(batch)
+    _check(load().spark_paged_rope_append(ctypes.byref(geom), qp, kp, vp, ld, dt, int(layer_class),
+                                          _here(rope, "rope", torch.float32), _rope_rows(geom, layer_class, rope),
+                                          ctypes.byref(pc), ctypes.byref(bc), op, old, _here(ws, "workspace"), ws.nbytes,
+                                          _stream(stream)), "spark_paged_rope_append")
+
+
+def spark_paged_read(geom: SparkGeom, pool: PagePool, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor,
+                     ws: torch.Tensor, stream=None) -> None:
+    """k, v [n_tokens, n_kv * 256] = the batch's rows out of their pages."""
+    kp, ld, dt = _rows(k, "k")
+    vp, vld, vdt = _rows(v, "v")
+    kv_dim = geom.n_kv * geom.head_dim
+    if k.shape != (batch.n_tokens, kv_dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [n_tokens, {kv_dim}]")
+    if vdt != dt or vld != ld:
+        raise ValueError("k and v must have the same dtype and row stride")
+    pc, bc = _pool_c(geom, pool), _batch_c(batch)
+    _check(load().spark_paged_read(ctypes.byref(geom), ctypes.byref(pc), ctypes.byref(bc), kp, vp, ld, dt,
+                                   _here(ws, "workspace"), ws.nbytes, _stream(stream)), "spark_paged_read")
+
+
 def spark_paged_attention(geom: SparkGeom, q: torch.Tensor, pool: PagePool, layer_class: int, batch: PagedBatch,
                           a: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """a [n_tokens, n_q * 256] = attention of the rotated queries q (float32
@@ -749,6 +844,94 @@ def spark_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, logprob: t
                                        _here(top_logprobs, "top_logprobs", torch.float32) if k else None,
                                        _here(ws, "workspace"), ws.nbytes, _stream(stream)),
            "spark_token_logprobs")
+
+
+def spark_beam_workspace_bytes(n_groups: int, n_beams: int) -> int:
+    return int(load().spark_beam_workspace_bytes(int(n_groups), int(n_beams)))
+
+
+def make_beam_workspace(n_groups: int, n_beams: int, device=None, stream=None) -> torch.Tensor:
+    """Allocate (through PyTorch) and initialise a workspace for
+    spark_beam_select and spark_beam_reorder."""
+    return _workspace(spark_beam_workspace_bytes(n_groups, n_beams), "number of groups or beams", device, stream)
+
+
+def _slots(t, name: str, n: int, dtype=torch.int32):
+    """Address of a list of n slots' values; None: none."""
+    if t is None:
+        return None
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}]")
+    return _here(t, name, dtype)
+
+
+def spark_beam_select(logits: torch.Tensor, score: torch.Tensor, done, length, n_beams: int, eos: int,
+                      new_score: torch.Tensor, token: torch.Tensor, parent: torch.Tensor, new_done, keep_len, new_len,
+                      ws: torch.Tensor, stream=None) -> None:
+    """The n_beams best continuations of every group of n_beams slots under
+    logits [slots, vocab] (float32 or bfloat16); lists [slots], float32 scores
+    and int32 otherwise.  done (and new_done, with eos -1) or the three lengths
+    may be None."""
+    lp, ld, dt = _rows(logits, "logits")
+    n, vocab = logits.shape
+    if n_beams < 1 or n % n_beams:
+        raise ValueError("logits must have a row for each beam of every group")
+    f32 = torch.float32
+    _check(load().spark_beam_select(lp, ld, dt, n // n_beams, int(n_beams), vocab, _slots(score, "score", n, f32),
+                                    _slots(done, "done", n), _slots(length, "length", n), int(eos),
+                                    _slots(new_score, "new_score", n, f32), _slots(token, "token", n),
+                                    _slots(parent, "parent", n), _slots(new_done, "new_done", n),
+                                    _slots(keep_len, "keep_len", n), _slots(new_len, "new_len", n),
+                                    _here(ws, "workspace"), ws.nbytes, _stream(stream)), "spark_beam_select")
+
+
+@dataclass
+class BeamState(_CachedC):
+    """A state of the beams as two CUDA tensors of the same shape, [slots, ...]
+    with rows of a multiple of 4 bytes: ``dst`` receives ``src``'s rows in their
+    new order.  ``positions``: the second dimension is a beam's positions, of
+    which the kept ones go along; ``push`` (int32 [slots], for int32 [slots,
+    positions]) is what to write behind them."""
+
+    src: torch.Tensor
+    dst: torch.Tensor
+    positions: bool = False
+    push: torch.Tensor | None = None
+    _c: object = field(default=None, init=False, repr=False, compare=False)
+
+    def _build_c(self) -> tuple:
+        """The C struct and (slots, device)."""
+        n, device = int(self.src.shape[0]), self.src.get_device()
+        if self.src.shape != self.dst.shape or self.src.dim() < 1 + bool(self.positions):
+            raise ValueError("src and dst must both be [slots, ...], with positions [slots, positions, ...]")
+        pitch = self.src.nbytes // max(1, n)
+        elem = pitch // max(1, int(self.src.shape[1])) if self.positions else 0
+        push = None
+        if self.push is not None:
+            if self.src.dtype != torch.int32 or self.src.dim() != 2 or self.push.shape != (n,):
+                raise ValueError("push must be [slots], of a state of positions that are int32")
+            push = _dev_ptr(self.push, "push", torch.int32)
+        for t in (self.dst, self.push):
+            if t is not None and t.get_device() != device:
+                raise ValueError("src, dst and push must be on the same device")
+        c = SparkBeamState(_dev_ptr(self.src, "src"), _dev_ptr(self.dst, "dst", self.src.dtype), pitch, elem, push)
+        return c, n, device
+
+
+def spark_beam_reorder(parent: torch.Tensor, keep_len, new_len, states, ws: torch.Tensor, stream=None) -> None:
+    """Rows of every BeamState to their new slots (spark_beam_select's parent,
+    keep_len and new_len; the lengths may be None without ``positions``)."""
+    n = int(parent.shape[0])
+    built = [st.to_c() for st in states]
+    for st, (_, slots, device) in zip(states, built):
+        if slots != n:
+            raise ValueError("every state must have a row for each slot")
+        if device != _current_device():
+            raise _not_here(st.src, "a state")
+    _check(load().spark_beam_reorder(_slots(parent, "parent", n), _slots(keep_len, "keep_len", n),
+                                     _slots(new_len, "new_len", n), n,
+                                     (SparkBeamState * max(1, len(built)))(*[b[0] for b in built]), len(built),
+                                     _here(ws, "workspace"), ws.nbytes, _stream(stream)), "spark_beam_reorder")
 
 
 def spark_attn_status_string(status: int) -> str:

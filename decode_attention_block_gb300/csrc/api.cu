@@ -350,12 +350,13 @@ int spark_attn_paged(const spark_geom* g, const float* h, const spark_layer_weig
   float* q_rot = ws_at<float>(workspace, L.q_rot);
   float* a = ws_at<float>(workspace, L.a);
   uint32_t* err = ws_at<uint32_t>(workspace, L.err);
-  // k and v in the pool's type, staged as "sequences" of one row each (as a
-  // chunk's), then written through the tables
+  // k and v in the pool's type (fp32 for 4-bit pages), staged as "sequences"
+  // of one row each (as a chunk's), then written through the tables
+  const int32_t sdtype = pool->dtype == SPARK_FP4 ? SPARK_F32 : pool->dtype;
   const size_t row = (size_t)g->n_kv * kHeadDim;
   unsigned char* ks = ws_at<unsigned char>(workspace, L.stage);
-  unsigned char* vs = ks + (size_t)m * row * (pool->dtype == SPARK_BF16 ? 2 : 4);
-  spark_kv_layer staged = {ks, vs, 1, 1, pool->dtype};
+  unsigned char* vs = ks + (size_t)m * row * (sdtype == SPARK_BF16 ? 2 : 4);
+  spark_kv_layer staged = {ks, vs, 1, 1, sdtype};
   int rotary_dim;
   double theta;
   rope_for(g, layer_class, &rotary_dim, &theta);
@@ -366,7 +367,7 @@ int spark_attn_paged(const spark_geom* g, const float* h, const spark_layer_weig
   cudaError_t e = run_qkv(pick_path(SPARK_PATH_AUTO, w->dtype, g, rotary_dim, m), g, h, w, &staged, rotary_dim, theta,
                           positions, m, q_rot, g_logits, err, workspace, L, st);
   if (e == cudaSuccess)
-    e = launch_paged_append(p, pool->dtype, pool->dtype, ks, vs, (int64_t)row, pool->k, pool->v, st);
+    e = launch_paged_append(p, sdtype, pool->dtype, ks, vs, (int64_t)row, pool->k, pool->v, st);
   if (e == cudaSuccess) e = launch_paged_attention(p, SPARK_F32, pool->dtype, pool->k, pool->v, st);
   if (e == cudaSuccess)
     e = run_oproj(pick_path(SPARK_PATH_AUTO, w->dtype, g, 0, m), g, a, g_logits, h, w, m, out, err, workspace, L, st);

@@ -53,6 +53,65 @@ int spark_paged_attention(const spark_geom* g, const void* q, int64_t q_ld, int3
   return cuda_status(launch_paged_attention(p, dtype, pool->dtype, pool->k, pool->v, (cudaStream_t)stream));
 }
 
+int spark_rope_table(const spark_geom* g, int32_t layer_class, int32_t n_positions, float* rope, void* stream) {
+  int s;
+  if ((s = check_geom(g)) != SPARK_OK) return s;
+  if (layer_class != SPARK_FULL && layer_class != SPARK_SLIDING) return SPARK_ERR_INVALID_ARG;
+  if (n_positions < 1 || n_positions > kMaxRopePositions || !rope || !aligned16(rope)) return SPARK_ERR_INVALID_ARG;
+  int rotary_dim;
+  double theta;
+  rope_for(g, layer_class, &rotary_dim, &theta);
+  return cuda_status(launch_rope_table(rope, n_positions, rotary_dim, theta, (cudaStream_t)stream));
+}
+
+int spark_paged_rope_append(const spark_geom* g, const void* q, const void* k, const void* v, int64_t ld, int32_t dtype,
+                            int32_t layer_class, const float* rope, int32_t n_positions, const spark_page_pool* pool,
+                            const spark_paged_batch* batch, void* q_out, int64_t q_out_ld, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  int s;
+  if ((s = check_geom(g)) != SPARK_OK) return s;
+  if ((s = check_pool(pool)) != SPARK_OK) return s;
+  if (layer_class != SPARK_FULL && layer_class != SPARK_SLIDING) return SPARK_ERR_INVALID_ARG;
+  if ((s = check_paged_batch(batch)) != SPARK_OK) return s;
+  const int64_t kv_width = (int64_t)g->n_kv * kHeadDim, q_width = (int64_t)g->n_q * kHeadDim;
+  if ((s = check_rows(k, dtype, ld, kv_width)) != SPARK_OK) return s;
+  if ((s = check_rows(v, dtype, ld, kv_width)) != SPARK_OK) return s;
+  if (n_positions < 1 || n_positions > kMaxRopePositions || !rope || !aligned16(rope)) return SPARK_ERR_INVALID_ARG;
+  if (q) {
+    if ((s = check_rows(q, dtype, ld, q_width)) != SPARK_OK) return s;
+    if ((s = check_rows(q_out, dtype, q_out_ld, q_width)) != SPARK_OK) return s;
+    // rows are read while others are written, but a row rotated in place
+    const RowSpan out(q_out, dtype, q_out_ld, q_width, batch->n_tokens);
+    const bool in_place = q_out == q && q_out_ld == ld;
+    if (!in_place && out.meets(RowSpan(q, dtype, ld, q_width, batch->n_tokens))) return SPARK_ERR_INVALID_ARG;
+    const RowSpan ks(k, dtype, ld, kv_width, batch->n_tokens), vs(v, dtype, ld, kv_width, batch->n_tokens);
+    if (in_place ? out.meets_rows(ks) || out.meets_rows(vs) : out.meets(ks) || out.meets(vs)) return SPARK_ERR_INVALID_ARG;
+  }
+  if ((s = check_paged_ws(workspace, workspace_bytes)) != SPARK_OK) return s;
+  const paged::Args p = paged_args(g, pool, SPARK_FULL, batch, workspace);
+  int rotary_dim;
+  double theta;
+  rope_for(g, layer_class, &rotary_dim, &theta);
+  const paged::RopeRows rows = {q, k, v, ld, rope, rotary_dim / 2, n_positions, q_out, q_out_ld, pool->k, pool->v};
+  return cuda_status(launch_paged_rope(p, dtype, pool->dtype, rows, (cudaStream_t)stream));
+}
+
+int spark_paged_read(const spark_geom* g, const spark_page_pool* pool, const spark_paged_batch* batch, void* k, void* v,
+                     int64_t ld, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int s;
+  if ((s = check_geom(g)) != SPARK_OK) return s;
+  if ((s = check_pool(pool)) != SPARK_OK) return s;
+  if ((s = check_paged_batch(batch)) != SPARK_OK) return s;
+  const int64_t width = (int64_t)g->n_kv * kHeadDim;
+  if ((s = check_rows(k, dtype, ld, width)) != SPARK_OK) return s;
+  if ((s = check_rows(v, dtype, ld, width)) != SPARK_OK) return s;
+  if (RowSpan(k, dtype, ld, width, batch->n_tokens).meets_rows(RowSpan(v, dtype, ld, width, batch->n_tokens)))
+    return SPARK_ERR_INVALID_ARG;
+  if ((s = check_paged_ws(workspace, workspace_bytes)) != SPARK_OK) return s;
+  const paged::Args p = paged_args(g, pool, SPARK_FULL, batch, workspace);
+  return cuda_status(launch_paged_read(p, dtype, pool->dtype, pool->k, pool->v, k, v, ld, (cudaStream_t)stream));
+}
+
 size_t spark_pages_workspace_bytes(int64_t n_pages, int32_t n_slots) {
   if (n_pages < 1 || n_pages > kMaxPoolPages || check_batch(n_slots) != SPARK_OK) return 0;
   return pages::ws_layout(n_pages, n_slots).total;
@@ -84,7 +143,10 @@ int pages_call(pages::Call* c, const spark_geom* g, const spark_page_pool* pools
   c->n_pools = n_pools;
   c->n_pages = pools[0].n_pages;
   c->page_size = pools[0].page_size;
-  c->row_bytes = (int64_t)g->n_kv * kHeadDim * (pools[0].dtype == SPARK_BF16 ? 2 : 4);
+  // 4-bit pages are copied in whole blocks of 16 positions
+  c->row_bytes = pools[0].dtype == SPARK_FP4 ? (int64_t)g->n_kv * (SPARK_FP4_BLOCK_BYTES / 16)
+                                             : (int64_t)g->n_kv * kHeadDim * (pools[0].dtype == SPARK_BF16 ? 2 : 4);
+  c->row_step = pools[0].dtype == SPARK_FP4 ? 16 : 1;
   c->table = table;
   c->new_table = new_table;
   c->n_slots = n_slots;

@@ -28,12 +28,13 @@ namespace checks {
 
 constexpr int64_t kMaxPoolPages = 1 << 24;
 constexpr int32_t kMaxScoreRows = 1 << 20;
+constexpr int32_t kMaxRopePositions = 1 << 24;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 inline int check_pool(const spark_page_pool* pool) {
   if (!pool || !pool->k || !pool->v || !aligned16(pool->k) || !aligned16(pool->v)) return SPARK_ERR_INVALID_ARG;
-  if (check_dtype(pool->dtype) != SPARK_OK) return SPARK_ERR_INVALID_ARG;
+  if (pool->dtype != SPARK_FP4 && check_dtype(pool->dtype) != SPARK_OK) return SPARK_ERR_INVALID_ARG;
   if (pool->n_pages < 1 || pool->page_size < 1) return SPARK_ERR_INVALID_ARG;
   if (pool->page_size % 16 != 0 || pool->page_size > 1024) return SPARK_ERR_UNSUPPORTED;
   // TMA coordinates of rows are 32-bit
@@ -58,6 +59,26 @@ inline int check_rows(const void* p, int32_t dtype, int64_t ld, int64_t width) {
   if (ld < width || ld > ((int64_t)1 << 32) || ld % (dtype == SPARK_BF16 ? 8 : 4) != 0) return SPARK_ERR_INVALID_ARG;
   return SPARK_OK;
 }
+
+// The bytes of `n` rows of `width` elements, `ld` elements apart.
+struct RowSpan {
+  uintptr_t begin;
+  int64_t step, width, n;
+  RowSpan(const void* p, int32_t dtype, int64_t ld, int64_t width_, int64_t n_)
+      : begin(reinterpret_cast<uintptr_t>(p)),
+        step(ld * (dtype == SPARK_BF16 ? 2 : 4)),
+        width(width_ * (dtype == SPARK_BF16 ? 2 : 4)),
+        n(n_) {}
+  uintptr_t end() const { return begin + (uintptr_t)((n - 1) * step + width); }
+  // whether their ranges overlap ...
+  bool meets(const RowSpan& o) const { return begin < o.end() && o.begin < end(); }
+  // ... or, of rows equally far apart (slices of the same rows), the rows themselves
+  bool meets_rows(const RowSpan& o) const {
+    if (!meets(o)) return false;
+    const int64_t d = (int64_t)(o.begin - begin), at = ((d % step) + step) % step;  // where o's rows begin among these
+    return at < width || at + o.width > step;
+  }
+};
 
 inline int check_paged_ws(void* ws, size_t bytes) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return SPARK_ERR_WORKSPACE;

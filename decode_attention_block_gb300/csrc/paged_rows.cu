@@ -1,0 +1,318 @@
+// paged_rows.cu -- rows of tokens into and out of pages beside the plain copy
+// of paged_attn.cu: the append with the rotation of queries and keys on the
+// way, the write and the read of 4-bit pages, and the table of rope angles.
+//
+// A CTA takes one token.  Its warps take the token's rows (query heads, key
+// heads, value heads) in turn, a lane 8 dims of each: a row is one load and one
+// store of the warp, and the two halves of a rotated pair that lie in other
+// lanes come by a shuffle.  Where a token's row lies is found once a CTA, while
+// its rows are on their way.
+#include <math.h>
+
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "launch.h"
+#include "paged_launch.h"
+#include "paged_parts.cuh"
+
+namespace spark {
+namespace {
+
+using paged::Args;
+
+constexpr int kRowWarps = 8;
+constexpr int kRowThreads = 32 * kRowWarps;
+
+// Where a token's row lies: position -1 where it belongs to no sequence, or
+// to one whose entries make no sense.
+struct Place {
+  int pos, page, row;
+};
+
+// The sequence that token t belongs to, by a warp: 32 starts a step.
+__device__ __forceinline__ Place find_place(const Args& p, int t, int lane) {
+  int lo = 0, n = p.n_seqs;  // the last start at or before t is one of lo .. lo + n - 1, or none is
+  while (n > 1) {
+    const int step = (n + 31) / 32, s = lo + lane * step;
+    const bool before = lane * step < n && __ldcg(p.q_start + s) <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, before);
+    const int last = m == 0 ? 0 : 31 - __clz(m);
+    lo += last * step;
+    n = min(step, n - last * step);
+    if (step == 1) break;
+  }
+  const paged::Seq s = paged::load_seq(p, lo);
+  Place at = {-1, -1, 0};
+  if (t < s.q0 || t >= s.q0 + s.n) return at;
+  at.pos = s.p0 + (t - s.q0);
+  const int pg = paged::page_entry(p, lo, paged::page_col(p, at.pos));
+  if (pg < 0 || pg >= p.n_pages) {
+    if (lane == 0) atomicOr(p.err, kErrIndex);
+    at.pos = -1;
+    return at;
+  }
+  at.page = pg;
+  at.row = paged::page_row(p, at.pos);
+  return at;
+}
+
+// every sequence is looked at, also one that no token's search ends in
+__device__ __forceinline__ void report_bad(const Args& p) {
+  for (int s = blockIdx.x * kRowThreads + (int)threadIdx.x; s < p.n_seqs; s += gridDim.x * kRowThreads)
+    if (paged::load_seq(p, s).bad) atomicOr(p.err, kErrIndex);
+}
+
+__device__ __forceinline__ void load8(float (&x)[8], const float* p) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
+  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+  const float2 a = bf16x2_to_f32x2(v.x), b = bf16x2_to_f32x2(v.y), c = bf16x2_to_f32x2(v.z), d = bf16x2_to_f32x2(v.w);
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y; x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+}
+__device__ __forceinline__ void put8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// a c - b s rounded once: both products with their errors (fma), their
+// difference with its error (Knuth's two-sum), the errors added at the end.
+// A 4-bit code then is that of the exact rotation, but for a value within
+// 2^-45 or so of a border.
+__device__ __forceinline__ float turned(float a, float c, float b, float s) {
+  const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
+  const float q = -__fmul_rn(b, s), qe = -__fmaf_rn(b, s, q);
+  const float sum = __fadd_rn(p, q), z = __fsub_rn(sum, p);
+  const float err = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, z)), __fsub_rn(q, z));
+  const float r = __fadd_rn(sum, __fadd_rn(err, __fadd_rn(pe, qe)));
+  return fabsf(sum) < INFINITY ? r : sum;
+}
+
+// A row's rotation: lane l has dims 8 l .. 8 l + 7.  VEC: r is a multiple of 16,
+// so that eight dims' partners lie in one lane, and their (cos, sin) stay for
+// all rows of the token.
+template <bool VEC>
+struct Turn {
+  float c[8], s[8];  // s negative for the first half of a pair
+  int half, from;    // the partner's lane
+  const float* cs;
+  bool on;
+  __device__ __forceinline__ void init(const float* rope, int pos, int half_, int lane) {
+    half = half_;
+    cs = rope + (int64_t)pos * 2 * half;
+    if constexpr (VEC) {
+      const int d = 8 * lane, lanes = half / 8;
+      on = d < 2 * half;
+      const bool second = d >= half;
+      from = on ? (second ? lane - lanes : lane + lanes) : lane;
+      if (on) {
+        const float4* src = reinterpret_cast<const float4*>(cs + 2 * (second ? d - half : d));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = __ldg(src + i);
+          c[2 * i] = v.x; s[2 * i] = second ? -v.y : v.y;
+          c[2 * i + 1] = v.z; s[2 * i + 1] = second ? -v.w : v.w;
+        }
+      }
+    }
+  }
+  // src: the row in memory, where the partners are read from without VEC
+  template <typename XT>
+  __device__ __forceinline__ void apply(float (&x)[8], const XT* src, int lane) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = __shfl_sync(0xffffffffu, x[i], from);
+        if (on) x[i] = turned(x[i], c[i], y, s[i]);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const int d = 8 * lane + i;
+        if (d >= 2 * half) break;
+        const bool second = d >= half;
+        const int e = second ? d - half : d;
+        const float y = (float)src[second ? e : e + half];
+        const float co = __ldg(cs + 2 * e), si = __ldg(cs + 2 * e + 1);
+        float mine = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mine = k == i ? x[k] : mine;
+        mine = turned(mine, co, y, second ? -si : si);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = k == i ? mine : x[k];
+      }
+    }
+  }
+};
+
+// Eight dims of a row into its page, by the whole warp.
+template <typename CT>
+__device__ __forceinline__ void put_row(unsigned char* pool, const Args& p, const Place& at, int head, const float (&x)[8],
+                                        int lane) {
+  put8(reinterpret_cast<CT*>(pool) + (((int64_t)at.page * p.page_size + at.row) * p.n_kv + head) * kHeadDim + 8 * lane, x);
+}
+struct Fp4 {};
+template <>
+__device__ __forceinline__ void put_row<Fp4>(unsigned char* pool, const Args& p, const Place& at, int head,
+                                             const float (&x)[8], int lane) {
+  float m = 0.f;
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    fine = fine && fabsf(x[i]) < INFINITY;
+    m = fmaxf(m, fabsf(x[i]));
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  fine = __shfl_xor_sync(0xffffffffu, (int)fine, 1) && fine;
+  const uint32_t b = fine ? fp4::scale_of(m) : fp4::kScaleNan;
+  const float s = fine ? fp4::scale_value(b) : 1.0f;
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = b == 0 ? 0.f : __fdiv_rn(x[i], s);
+  unsigned char* block = pool + fp4::block_at(at.page, at.row, head, p.page_size, p.n_kv);
+  const int row = at.row % fp4::kRows;
+  *reinterpret_cast<uint32_t*>(block + fp4::code_at(row, 8 * lane)) = fp4::codes8(y);
+  if ((lane & 1) == 0) block[fp4::scale_at(row, 8 * lane)] = (unsigned char)b;
+}
+
+template <typename CT>
+__device__ __forceinline__ void get_row(const unsigned char* pool, const Args& p, const Place& at, int head, float (&x)[8],
+                                        int lane) {
+  load8(x, reinterpret_cast<const CT*>(pool) + (((int64_t)at.page * p.page_size + at.row) * p.n_kv + head) * kHeadDim + 8 * lane);
+}
+template <>
+__device__ __forceinline__ void get_row<Fp4>(const unsigned char* pool, const Args& p, const Place& at, int head,
+                                             float (&x)[8], int lane) {
+  const unsigned char* block = pool + fp4::block_at(at.page, at.row, head, p.page_size, p.n_kv);
+  const int row = at.row % fp4::kRows;
+  const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(block + fp4::code_at(row, 8 * lane)));
+  const float s = fp4::scale_value(__ldcg(block + fp4::scale_at(row, 8 * lane)));
+  uint32_t h[4];
+  fp4::halves8(w, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = fp4::unpack(h[i]);
+    x[2 * i] = f.x * s;
+    x[2 * i + 1] = f.y * s;
+  }
+}
+
+// One token a CTA.  half 0: no rotation; q null: keys and values alone.
+template <typename XT, typename CT, bool VEC>
+__global__ void __launch_bounds__(kRowThreads)
+    k_paged_rope(const XT* q, const XT* k, const XT* v, int64_t ld, const float* rope, int half, int n_positions, XT* q_out,
+                 int64_t q_out_ld, unsigned char* pk, unsigned char* pv, const __grid_constant__ Args p) {
+  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  // no early trigger: a kernel that reads pages before its own wait must not
+  // start before these rows are written
+  const int n_q = q == nullptr ? 0 : kGroup * p.n_kv, rows = n_q + 2 * p.n_kv;
+  report_bad(p);
+  Place at = find_place(p, t, lane);
+  if (at.pos < 0) return;
+  Turn<VEC> turn;
+  if (half > 0) {
+    if (at.pos >= n_positions) {
+      if (threadIdx.x == 0) atomicOr(p.err, kErrIndex);
+      return;
+    }
+    turn.init(rope, at.pos, half, lane);
+  }
+  for (int r = warp; r < rows; r += kRowWarps) {
+    const bool is_q = r < n_q, is_k = !is_q && r < n_q + p.n_kv;
+    const int head = is_q ? r : is_k ? r - n_q : r - n_q - p.n_kv;
+    const XT* src = (is_q ? q : is_k ? k : v) + t * ld + (int64_t)head * kHeadDim;
+    float x[8];
+    load8(x, src + 8 * lane);
+    if (half > 0 && (is_q || is_k)) {
+      turn.apply(x, src, lane);
+      __syncwarp();  // (in place, a row's partners are read before any is written)
+    }
+    if (is_q)
+      put8(q_out + t * q_out_ld + (int64_t)head * kHeadDim + 8 * lane, x);
+    else
+      put_row<CT>(is_k ? pk : pv, p, at, head, x, lane);
+  }
+}
+
+template <typename XT, typename CT>
+__global__ void __launch_bounds__(kRowThreads)
+    k_paged_read(const unsigned char* pk, const unsigned char* pv, XT* k, XT* v, int64_t ld, const __grid_constant__ Args p) {
+  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  report_bad(p);
+  const Place at = find_place(p, t, lane);
+  if (at.pos < 0) return;
+  for (int r = warp; r < 2 * p.n_kv; r += kRowWarps) {
+    const int head = r >> 1;
+    float x[8];
+    get_row<CT>((r & 1) ? pv : pk, p, at, head, x, lane);
+    put8(((r & 1) ? v : k) + t * ld + (int64_t)head * kHeadDim + 8 * lane, x);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_rope_table(float2* rope, int64_t n, int half, double theta, int r) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= n) return;
+  const int i = (int)(e % half);
+  double s, c;
+  sincos((double)(e / half) * pow(theta, -2.0 * i / (double)r), &s, &c);
+  rope[e] = make_float2((float)c, (float)s);
+}
+
+template <typename XT, typename CT>
+cudaError_t rope_t(const Args& p, const paged::RopeRows& a, cudaStream_t st) {
+  auto kern = a.half % 8 == 0 ? k_paged_rope<XT, CT, true> : k_paged_rope<XT, CT, false>;
+  return launch_pdl(kern, dim3(p.n_tokens), dim3(kRowThreads), 0, st, static_cast<const XT*>(a.q),
+                    static_cast<const XT*>(a.k), static_cast<const XT*>(a.v), a.ld, a.rope, a.half, a.n_positions,
+                    static_cast<XT*>(a.q_out), a.q_out_ld, static_cast<unsigned char*>(a.pk),
+                    static_cast<unsigned char*>(a.pv), p);
+}
+
+template <typename XT, typename CT>
+cudaError_t read_t(const Args& p, const void* pk, const void* pv, void* k, void* v, int64_t ld, cudaStream_t st) {
+  return launch_pdl(k_paged_read<XT, CT>, dim3(p.n_tokens), dim3(kRowThreads), 0, st,
+                    static_cast<const unsigned char*>(pk), static_cast<const unsigned char*>(pv), static_cast<XT*>(k),
+                    static_cast<XT*>(v), ld, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rope(const paged::Args& p, int xdtype, int cdtype, const paged::RopeRows& a, cudaStream_t st) {
+  const bool bf = xdtype == SPARK_BF16;
+  if (cdtype == SPARK_FP4) return bf ? rope_t<__nv_bfloat16, Fp4>(p, a, st) : rope_t<float, Fp4>(p, a, st);
+  if (cdtype == SPARK_BF16)
+    return bf ? rope_t<__nv_bfloat16, __nv_bfloat16>(p, a, st) : rope_t<float, __nv_bfloat16>(p, a, st);
+  return bf ? rope_t<__nv_bfloat16, float>(p, a, st) : rope_t<float, float>(p, a, st);
+}
+
+cudaError_t launch_paged_read(const paged::Args& p, int xdtype, int cdtype, const void* pk, const void* pv, void* k,
+                              void* v, int64_t ld, cudaStream_t st) {
+  const bool bf = xdtype == SPARK_BF16;
+  if (cdtype == SPARK_FP4)
+    return bf ? read_t<__nv_bfloat16, Fp4>(p, pk, pv, k, v, ld, st) : read_t<float, Fp4>(p, pk, pv, k, v, ld, st);
+  if (cdtype == SPARK_BF16)
+    return bf ? read_t<__nv_bfloat16, __nv_bfloat16>(p, pk, pv, k, v, ld, st)
+              : read_t<float, __nv_bfloat16>(p, pk, pv, k, v, ld, st);
+  return bf ? read_t<__nv_bfloat16, float>(p, pk, pv, k, v, ld, st) : read_t<float, float>(p, pk, pv, k, v, ld, st);
+}
+
+cudaError_t launch_rope_table(float* rope, int n_positions, int rotary_dim, double theta, cudaStream_t st) {
+  const int64_t n = (int64_t)n_positions * (rotary_dim / 2);
+  k_rope_table<<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(reinterpret_cast<float2*>(rope), n, rotary_dim / 2, theta,
+                                                                  rotary_dim);
+  return cudaGetLastError();
+}
+
+}  // namespace spark

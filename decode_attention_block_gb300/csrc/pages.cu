@@ -304,9 +304,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact(const __grid_con
 // all of a piece's loads in flight together, the next piece's move asked for
 // before them.  Sources are kept pages and targets free ones, so no page is
 // read and written.  Pieces are numbered move by move, then by pool and side,
-// and dealt to the CTAs in turn.
+// and dealt to the CTAs in turn.  Rows are copied in multiples of row_step (a
+// power of two that divides a page: the rows of a 4-bit block).
 __global__ void __launch_bounds__(kCopyThreads)
-    k_pages_copy(const pages::Head* head, const Move* moves, int row_bytes, int pieces, int n_pools,
+    k_pages_copy(const pages::Head* head, const Move* moves, int row_bytes, int row_step, int pieces, int n_pools,
                  const __grid_constant__ pages::Pools pools, int64_t page_bytes) {
   pdl_wait();
   const int n_moves = __ldcg(&head->n_moves);
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kCopyThreads)
       ++m;
     }
     if (m < n_moves) next = load(m);
-    const int64_t bytes = (int64_t)mv.z * row_bytes;
+    const int64_t bytes = (int64_t)((mv.z + row_step - 1) & -row_step) * row_bytes;
     if (off >= bytes) continue;
     unsigned char* base = static_cast<unsigned char*>(pools.p[side]);
     const unsigned char* from = base + mv.x * page_bytes + off;
@@ -402,7 +403,8 @@ cudaError_t launch_pages(const pages::Call& c, cudaStream_t st) {
   const int64_t page_bytes = (int64_t)c.page_size * c.row_bytes;
   const int pieces = (int)((page_bytes + kPiece - 1) / kPiece);
   return launch_pdl(k_pages_copy, dim3(8 * device_sm_count()), dim3(kCopyThreads), 0, st,
-                    static_cast<const pages::Head*>(p.head), static_cast<const Move*>(p.moves), (int)c.row_bytes, pieces,
+                    static_cast<const pages::Head*>(p.head), static_cast<const Move*>(p.moves), (int)c.row_bytes, c.row_step,
+                    pieces,
                     c.n_pools, c.pools, page_bytes);
 }
 

@@ -36,6 +36,7 @@ struct Call {
   int64_t n_pages;
   int32_t page_size;
   int64_t row_bytes;
+  int32_t row_step;  // rows that lie together: a page's first rows are copied in multiples of it
   const int32_t* table;
   int32_t* new_table;
   int32_t n_slots, max_pages;

@@ -61,7 +61,8 @@ typedef enum spark_status {
   SPARK_ERR_DEVICE = -7        /* a kernel set the workspace error word */
 } spark_status;
 
-typedef enum spark_dtype { SPARK_F32 = 0, SPARK_BF16 = 1 } spark_dtype;
+/* SPARK_FP4: pages only (spark_paged.h) */
+typedef enum spark_dtype { SPARK_F32 = 0, SPARK_BF16 = 1, SPARK_FP4 = 2 } spark_dtype;
 
 /* Layer class: an entry of 1 in the model's full_attention_layer_mask marks a
  * full layer (src/families/spark/attn.rs, encode_attention_block, the rope

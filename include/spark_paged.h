@@ -45,7 +45,21 @@ extern "C" {
 /* One layer's pages (device, caller-owned): K and V are two buffers of
  * [n_pages][page_size][n_kv][head_dim] elements of `dtype`.
  * page_size: a multiple of 16 in [16, 1024]; n_pages: 1 .. 2^24, with
- * n_pages * page_size < 2^31. */
+ * n_pages * page_size < 2^31.
+ *
+ * SPARK_FP4 pages hold a row of one KV head in 144 bytes: 4-bit codes (a sign
+ * and 0, 0.5, 1, 1.5, 2, 3, 4 or 6) and a scale for each 16 dims, which is a
+ * number of 5 exponent and 3 mantissa bits (bits 14 .. 7 of an fp16, up to
+ * 10240); an element is code * scale, a number of at most 6 significant
+ * bits.  With m the largest magnitude of the 16, in fp32: scale = m / 6 and
+ * code = x / scale, each division rounded to fp32, then to the nearest of the
+ * format, ties to even; magnitudes above 61440 become that; 16 elements with
+ * an infinity or a NaN among them become NaN.
+ * K and V are [n_pages][page_size / 16][n_kv] blocks of 2304 bytes, one for 16
+ * positions: 16 rows of 128 bytes of codes, then 16 rows of 16 scales.  A byte
+ * of codes holds dim 2 i in its low half and 2 i + 1 in its high half; the
+ * 16-byte chunk c of row r lies at chunk c ^ (r % 2 + 2 (r / 4 % 4)). */
+#define SPARK_FP4_BLOCK_BYTES 2304
 typedef struct spark_page_pool {
   void* k;
   void* v;
@@ -83,7 +97,7 @@ typedef struct spark_paged_batch {
 size_t spark_paged_workspace_bytes(const spark_geom* g);
 
 /* Write the k and v rows of the batch's new tokens into their pages, rounded
- * once to the pool's type.
+ * once to the pool's type (SPARK_FP4: see there).
  *   k, v     device [n_tokens][n_kv * head_dim] of element type `dtype`;
  *            row t starts at element t * ld (slices of a fused projection's
  *            rows do; ld >= n_kv * head_dim, rows 16-byte aligned).
@@ -95,6 +109,47 @@ size_t spark_paged_workspace_bytes(const spark_geom* g);
 int spark_paged_append(const spark_geom* g, const void* k, const void* v, int64_t ld, int32_t dtype,
                        const spark_page_pool* pool, const spark_paged_batch* batch, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* The (cos, sin) of a layer class's rope angles position * theta^(-2 i / r) in
+ * fp32, computed in 64 bits, for positions 0 .. n_positions - 1: rope, device
+ * [n_positions][r / 2][2], with r the class's rotary dim (full_rotary_dim, or
+ * head_dim in sliding layers).  All layers of a class share one.
+ * n_positions: 1 .. 2^24.
+ * Errors: INVALID_ARG, UNSUPPORTED; CUDA if a launch fails. */
+int spark_rope_table(const spark_geom* g, int32_t layer_class, int32_t n_positions, float* rope, void* stream);
+
+/* spark_paged_append of new tokens whose queries and keys are not rotated
+ * yet: NeoX rope on the way (the class's rotary dim r, pairs i and i + r / 2,
+ * the dims behind r as they are), each result of the rotation rounded once to
+ * fp32 and once to its type.
+ *   q       rows [n_q * head_dim] of element type `dtype`, row t at element
+ *           t * ld; null: no queries.
+ *   k, v    rows [n_kv * head_dim], likewise at t * ld (three slices of a
+ *           fused projection's rows).
+ *   q_out   rows [n_q * head_dim] of the same type, row t at element
+ *           t * q_out_ld: the rotated queries of the tokens that belong to a
+ *           sequence, other rows are left as they were.  It is q itself with
+ *           q_out_ld == ld (in place), or overlaps neither q, k nor v.
+ *   rope    the class's table (spark_rope_table), n_positions long.
+ * A token's position is that of its cache row (seq_len, a device value: a
+ * captured call replays for the next token).  One at or behind n_positions
+ * raises bit 2 and is left out.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE before any work is enqueued;
+ * CUDA if a launch fails. */
+int spark_paged_rope_append(const spark_geom* g, const void* q, const void* k, const void* v, int64_t ld, int32_t dtype,
+                            int32_t layer_class, const float* rope, int32_t n_positions, const spark_page_pool* pool,
+                            const spark_paged_batch* batch, void* q_out, int64_t q_out_ld, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* The batch's rows out of their pages: k and v (device, element type `dtype`,
+ * row t at element t * ld) receive the row of every token that a sequence of
+ * the batch counts as new, whoever wrote it (q_start and seq_len choose the
+ * positions: a whole prefix with as many "new" tokens as it is long).  Rows
+ * behind q_start[n_seqs] are left as they were.  An element that `dtype` does
+ * not hold is rounded once (fp32 pages read as bf16).
+ * workspace and errors as spark_paged_append. */
+int spark_paged_read(const spark_geom* g, const spark_page_pool* pool, const spark_paged_batch* batch, void* k, void* v,
+                     int64_t ld, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Attention of every new token of the batch over its sequence's pages (its
  * own row included: spark_paged_append comes first).
@@ -108,6 +163,11 @@ int spark_paged_append(const spark_geom* g, const void* k, const void* v, int64_
  * bits), the probabilities too.  bf16 queries meet it as they are, with
  * probabilities of 16 significant bits where max_q_len is 1 and rounded to
  * bf16 (8 bits) where it is more.  An fp32 pool is read by fp32 arithmetic.
+ * 4-bit pages are met in fp16, queries scaled by a power of two for each token
+ * and head: fp32 ones as q = hi + lo (22 bits of the token's and head's
+ * largest element), bf16 ones as they are (elements below 2^-23 of the
+ * largest lose bits); probabilities as hi + lo, but rounded to fp16 (11 bits)
+ * for bf16 queries where max_q_len is more than 1.
  * Rows that no token of the sequence attends to may hold anything, NaN
  * included; a row that one of its new tokens attends to is expected finite
  * (a non-finite V row may reach every new token of its sequence).
