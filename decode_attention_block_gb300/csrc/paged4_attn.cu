@@ -408,6 +408,9 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
 }  // namespace
 
 cudaError_t launch_paged4_attention(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st) {
+  if (p.max_q > paged::kChunkTokens && (2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q || p.n_tokens > 128 * p.n_seqs))
+    return launch_paged4_pair(p, qdtype, k, v, st);
+  if (p.max_q > 1) return launch_paged4_chunk(p, qdtype, k, v, st);
   return qdtype == SPARK_BF16 ? launch_token4<__nv_bfloat16>(p, k, v, st) : launch_token4<float>(p, k, v, st);
 }
 

@@ -1,0 +1,142 @@
+// paged4_chunk_parts.cuh -- what the chunk attention kernels over 4-bit pages
+// share (paged4_chunk.cu: one CTA and 32 tokens a group; paged4_pair.cu: two
+// CTAs and 64): blocks of pages into fp16 operands in shared memory.
+//
+// A warp takes 16 positions, one block: plain loads of codes and scales into registers, a
+// tile ahead of their use (a block's parts are contiguous, so nothing is gained
+// by a copy engine, and no shared memory is spent on bytes that are read once),
+// then conversion and 16-byte stores in the layout of paged_chunk_parts.cuh.
+#pragma once
+
+#include "paged_chunk_parts.cuh"
+
+namespace spark {
+namespace chunk4 {
+
+using namespace chunk;
+
+constexpr int kDequant = 8;          // warps
+constexpr int kThreads4 = 128 * 2 + 32 * kDequant;
+constexpr int kFirstSoft = 4, kFirstDequant = 8;  // warps, in warpgroups: 0 and 1 load queries and issue MMAs
+// Registers a thread, by warpgroup (setmaxnreg): the softmax warps hold a row's
+// 128 scores.
+constexpr int kRegsLaunch = 128;     // of 65536 for 512 threads
+constexpr int kRegsIssue = 72, kRegsSoft = 240, kRegsDequant = 96;
+static_assert(kRegsIssue < kRegsLaunch && kRegsSoft > kRegsLaunch && kRegsDequant < kRegsLaunch &&
+                  kRegsIssue + kRegsSoft + 2 * kRegsDequant <= 4 * kRegsLaunch,
+              "some give up what the others take (a dec to more than a thread has is an illegal instruction)");
+
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// A lane's part of a block: chunk 4 h + lane / 8 of rows lane % 8 and lane % 8 +
+// 8, their codes and the two scales of each.  (Eight lanes with rows of their own
+// store 16 bytes of each in different banks.)
+struct Part {
+  uint4 code[2];
+  uint32_t scale[2];
+};
+
+// Where they lie in a pool: with X the first row's chunk of h = 0, that of h = 1
+// is X ^ 64 bytes, and 8 rows further the two have changed places (fp4::turn).
+struct Lanes {
+  const unsigned char *x0, *x1, *y;
+  __device__ __forceinline__ Lanes(const unsigned char* pool, int lane) {
+    const int row = lane & 7, c = lane >> 3;
+    const uint32_t x = (uint32_t)(row * fp4::kCodes + ((c ^ fp4::turn(row)) << 4));
+    x0 = pool + x;
+    x1 = pool + (x ^ 64u);
+    y = pool + fp4::kScalesAt + row * fp4::kScales + 2 * c;
+  }
+  static constexpr uint32_t kNone = 0xFFFFFFFFu;
+  // half h's part of a block (kNone: zeros)
+  __device__ __forceinline__ void load(Part& x, uint32_t block, int h) const {
+    if (block == kNone) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x.code[i] = make_uint4(0u, 0u, 0u, 0u);
+        x.scale[i] = 0u;
+      }
+      return;
+    }
+    const uint64_t at = (uint64_t)block * (uint64_t)fp4::kBlock;
+    x.code[0] = __ldcg(reinterpret_cast<const uint4*>((h ? x1 : x0) + at));
+    x.code[1] = __ldcg(reinterpret_cast<const uint4*>((h ? x0 : x1) + at + 8 * fp4::kCodes));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      x.scale[i] = __ldcg(reinterpret_cast<const unsigned short*>(y + at + 8 * h + 8 * i * fp4::kScales));
+  }
+  // both halves' parts
+  __device__ __forceinline__ void load(Part (&x)[2], uint32_t block) const {
+    if (block == kNone) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[h].code[i] = make_uint4(0u, 0u, 0u, 0u);
+          x[h].scale[i] = 0u;
+        }
+      return;
+    }
+    const uint64_t at = (uint64_t)block * (uint64_t)fp4::kBlock;
+    const unsigned char *a = x0 + at, *b = x1 + at, *s = y + at;
+    x[0].code[0] = __ldcg(reinterpret_cast<const uint4*>(a));
+    x[0].code[1] = __ldcg(reinterpret_cast<const uint4*>(b + 8 * fp4::kCodes));
+    x[1].code[0] = __ldcg(reinterpret_cast<const uint4*>(b));
+    x[1].code[1] = __ldcg(reinterpret_cast<const uint4*>(a + 8 * fp4::kCodes));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[h].scale[i] = __ldcg(reinterpret_cast<const unsigned short*>(s + 8 * h + 8 * i * fp4::kScales));
+  }
+};
+
+// The blocks of a warp's positions x, x + 128 .. of a group's tiles, found for 32
+// tiles at a time, one per lane.
+struct Blocks {
+  uint32_t mine;
+  // those of the tiles at x + 128 lane, before `end`
+  __device__ __forceinline__ void find(const Args& p, const Cursor& cur, int x, int end, int lane) {
+    x += lane * kPos;
+    mine = Lanes::kNone;
+    if (x < end && x <= cur.g.hi && x + fp4::kRows > cur.g.lo) {
+      const int col = paged::page_col(p, x), in_page = (x - col * p.page_size) / fp4::kRows;
+      const int page = paged::page_of(p, paged::page_entry(p, cur.s, col));
+      // (pages * page_size < 2^31: the blocks of all heads are below 2^30)
+      mine = ((uint32_t)page * (uint32_t)(p.page_size / fp4::kRows) + (uint32_t)in_page) * (uint32_t)p.n_kv + (uint32_t)cur.j;
+    }
+  }
+  __device__ __forceinline__ uint32_t of(int tile) const { return __shfl_sync(0xffffffffu, mine, tile & 31); }
+};
+
+// The part's 32 dims of each row as fp16: with c = lane / 8, line c / 2 of 64
+// dims, four 16-byte chunks of a row of 128 bytes, chunk 4 (c % 2) + e of row r at
+// (4 (c % 2) + e) ^ (r % 8): the lane's places are at[e] in the line; the second
+// row lies `group` bytes behind.
+__device__ __forceinline__ void store_part(unsigned char* line, const uint32_t (&at)[4], uint32_t group, const Part& x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
+    const uint32_t f[2] = {__byte_perm(x.scale[i], 0u, 0x4040u) << 7, __byte_perm(x.scale[i], 0u, 0x4141u) << 7};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t h[4];
+      fp4::halves8(w[k], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = fp4::mul2(h[j], f[k >> 1]);
+      *reinterpret_cast<uint4*>(line + at[k] + i * group) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+// the lane's places
+__device__ __forceinline__ void part_places(uint32_t (&at)[4], int lane) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    at[k] = (uint32_t)((lane & 7) * 128 + ((((lane >> 3 & 1) << 2 | k) ^ (lane & 7)) << 4));
+}
+
+}  // namespace chunk4
+}  // namespace spark

@@ -1,6 +1,7 @@
 // paged_chunk_parts.cuh -- what the chunk attention kernels share
 // (paged_chunk.cu: one CTA and 32 tokens a group; paged_pair.cu: two CTAs and
-// 64): the queries' layout in shared memory, the softmax warps, the join of
+// 64; paged4_chunk.cu, paged4_pair.cu: the same over 4-bit pages, whose MMAs
+// take fp16): the queries' layout in shared memory, the softmax warps, the join of
 // partial states, the tensor map of a pool.
 #pragma once
 
@@ -8,6 +9,7 @@
 
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "launch.h"
 #include "paged_launch.h"
 #include "paged_parts.cuh"
@@ -159,6 +161,73 @@ __device__ __forceinline__ void split_query(unsigned char* q_s, int i, int r) {
   }
 }
 
+// Row r of the queries as fp16 numbers, in place, scaled by a power of two (fp32
+// ones as a line of halves and a line of remainders, as split_query leaves them);
+// returns what the row's scores are to be multiplied by.
+template <typename QT>
+__device__ __forceinline__ float fp16_query(unsigned char* q_s, int r) {
+  unsigned char* row = q_s + r * 128;
+  auto at = [&](int line, int c) { return row + line * kLineBytes + ((c ^ (r & 7)) << 4); };
+  float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int line = 0; line < kQueryLines<QT>; ++line)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 w = *reinterpret_cast<const uint4*>(at(line, c));
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<QT, float>::value) {
+          mx[i] = fmaxf(mx[i], fabsf(__uint_as_float(x[i])));
+        } else {
+          const float2 f = bf16x2_to_f32x2(x[i]);
+          mx[i] = fmaxf(mx[i], fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+    }
+  const float2 unit = fp4::unit_of(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+  if constexpr (std::is_same<QT, float>::value) {
+#pragma unroll 1
+    for (int line = 0; line < kQueryLines<QT>; line += 2) {
+      float4 x[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) x[c] = *reinterpret_cast<const float4*>(at(line + (c >> 3), c & 7));
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float v[8] = {x[2 * c].x,     x[2 * c].y,     x[2 * c].z,     x[2 * c].w,
+                            x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = v[2 * i] * unit.x, b = v[2 * i + 1] * unit.x;
+          h[i] = fp4::pack(a, b);
+          const float2 f = fp4::unpack(h[i]);
+          l[i] = fp4::pack(a - f.x, b - f.y);
+        }
+        *reinterpret_cast<uint4*>(at(line, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(at(line + 1, c)) = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int line = 0; line < kQueryLines<QT>; ++line)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint4* p = reinterpret_cast<uint4*>(at(line, c));
+        const uint4 w = *p;
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_f32x2(x[i]);
+          h[i] = fp4::pack(f.x * unit.x, f.y * unit.x);
+        }
+        *p = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+  }
+  return unit.y;
+}
+
 // rows [token][head][256] as [line][token][head][128 bytes]
 template <typename QT>
 bool make_query_map(CUtensorMap* map, const Args& p, int tokens, int lines) {
@@ -189,9 +258,9 @@ __device__ __forceinline__ uint32_t seen32(int x0, int x1, int first) {
   return below_b & ~below_a;
 }
 
-// 32 scores of a row become P = e^(scale s - ref) in bf16 (SPLIT: and the
-// remainders) over their own columns at `ts`.
-template <bool SPLIT>
+// 32 scores of a row become P = e^(scale s - ref) in bf16 or fp16 (SPLIT: and
+// the remainders) over their own columns at `ts`.
+template <bool SPLIT, bool FP16 = false>
 __device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], float scale, float ref, float2 (&sum)[2]) {
   uint32_t hi[16], lo[16];
 #pragma unroll
@@ -200,10 +269,10 @@ __device__ __forceinline__ void exp32(uint32_t ts, const uint32_t (&s)[32], floa
                            make_float2(scale, scale), make_float2(-ref, -ref));
     const float2 e = make_float2(ex2(t.x), ex2(t.y));
     sum[i & 1] = fadd2(sum[i & 1], e);
-    hi[i] = pack2(e.x, e.y);
+    hi[i] = FP16 ? fp4::pack(e.x, e.y) : pack2(e.x, e.y);
     if (SPLIT) {
-      const float2 f = bf16x2_to_f32x2(hi[i]);
-      lo[i] = pack2(e.x - f.x, e.y - f.y);
+      const float2 f = FP16 ? fp4::unpack(hi[i]) : bf16x2_to_f32x2(hi[i]);
+      lo[i] = FP16 ? fp4::pack(e.x - f.x, e.y - f.y) : pack2(e.x - f.x, e.y - f.y);
     }
   }
   tc::st16(ts, hi);
@@ -250,8 +319,9 @@ constexpr int kStageBytes = 32 * kStageRow;    // of a warp
 // maximum and sum, the output at the group's end.  arrive_q, arrive_p: one
 // lane per warp tells the MMA warp that fp32 queries are in halves, or the
 // probabilities in a buffer.  STAGE: whole groups' outputs leave through
-// `stage`.
-template <typename QT, int RANKS, bool STAGE, typename ArriveQ, typename ArriveP>
+// `stage`.  FP16: queries of either type become fp16, scaled row by row, and so
+// do the probabilities.
+template <typename QT, int RANKS, bool STAGE, bool FP16 = false, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
                                               uint64_t* q_raw, uint64_t* s_full, uint64_t* pv_done,
@@ -264,28 +334,34 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
   // a scale of zero or below is taken to the scores before they are masked: a
   // masked one of -inf stays that
   const float sign = p.scale_log2 < 0.f ? -1.f : p.scale_log2 > 0.f ? 1.f : 0.f;
-  const float scale = sign == 0.f ? 1.f : fabsf(p.scale_log2);
+  const float scale_all = sign == 0.f ? 1.f : fabsf(p.scale_log2);
+  float scale = scale_all, scale_next = scale_all;  // of the row's scores, in this group and the next
   QT* out = static_cast<QT*>(p.a);
   uint32_t tile = 0;
   bool ok = true;
-  constexpr bool kSplit = std::is_same<QT, float>::value;
+  constexpr bool kSplit = std::is_same<QT, float>::value, kConvert = kSplit || FP16;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, flags, kWaitLimitNs));
     tc::fence_after();
     return ok;
   };
-  // fp32 queries have landed: into halves
+  // fp32 queries (FP16: any) have landed: into halves
   uint32_t item = 0;
   auto split_queries = [&](const Cursor& at) {
     if (!wait(q_raw, item++ & 1)) return;
+    if constexpr (FP16) {
+      // (a warp's rows are those of one box)
+      if (quad < query_boxes(at.g.n_tok, tok0)) scale_next = scale_all * fp16_query<QT>(q_s, row);
+    } else
 #pragma unroll 1
     for (int b = 0; b < query_boxes(at.g.n_tok, tok0); ++b) split_query(q_s, quad, 32 * b + lane);  // a line per warp
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
     __syncwarp();
     if (lane == 0) arrive_q();
   };
-  if (kSplit) split_queries(cur);
+  if (kConvert) split_queries(cur);
   for (;;) {
+    scale = scale_next;
     const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
     const paged::Group g = cur.g;
     const int tok = tok0 + (row >> 2);
@@ -354,10 +430,10 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         }
         const float ref = m == -INFINITY ? 0.f : m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        exp32<kSplit>(ts, s0, scale, ref, sum);
-        exp32<kSplit>(ts + 32, s1, scale, ref, sum);
-        exp32<kSplit>(ts + 64, s2, scale, ref, sum);
-        exp32<kSplit>(ts + 96, s3, scale, ref, sum);
+        exp32<kSplit, FP16>(ts, s0, scale, ref, sum);
+        exp32<kSplit, FP16>(ts + 32, s1, scale, ref, sum);
+        exp32<kSplit, FP16>(ts + 64, s2, scale, ref, sum);
+        exp32<kSplit, FP16>(ts + 96, s3, scale, ref, sum);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::wait_st();
       }
@@ -366,10 +442,10 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       if (lane == 0) arrive_p(buf);
     }
     if (!ok) break;
-    // (the next group's fp32 queries are split while this one's last product runs)
+    // (the next group's queries are split while this one's last product runs)
     Cursor nxt = cur;
     const bool more = nxt.advance(p, sh, u1);
-    if (kSplit && more) split_queries(nxt);
+    if (kConvert && more) split_queries(nxt);
     if (!wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1)) break;
     const bool split = cur.begin < u0 || cur.end > u1;
     if (live) {

@@ -34,6 +34,12 @@ cudaError_t launch_paged_pair(const paged::Args& p, int qdtype, const void* k, c
 // Attention over 4-bit pages.
 cudaError_t launch_paged4_attention(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st);
 
+// The same for chunks, on the tensor cores, 32 tokens at a time.
+cudaError_t launch_paged4_chunk(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st);
+
+// The same on pairs of CTAs, 64 tokens at a time.
+cudaError_t launch_paged4_pair(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st);
+
 // The new tokens' rows into their pages, rotated on the way; any pool.
 cudaError_t launch_paged_rope(const paged::Args& p, int xdtype, int cdtype, const paged::RopeRows& a, cudaStream_t st);
 

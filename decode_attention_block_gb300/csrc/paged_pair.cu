@@ -29,13 +29,13 @@
 // output leaves through a stage: with both done by the softmax threads row by
 // row it was 250 us) and the join.
 #include "paged_chunk_parts.cuh"
+#include "paged_pair_parts.cuh"
 
 namespace spark {
 namespace {
 
 using namespace chunk;
 
-constexpr int kPairTokens = 2 * paged::kChunkTokens;
 // Units per pair at least (one sequence of 48 tokens at 1000, bf16 queries: 15.7
 // us at 2, 16.9 at 1, 18.2 at 3).
 constexpr int kMinUnits = 2;
@@ -62,54 +62,6 @@ struct PairSmem {
 };
 static_assert(PairSmem<true>::kAlloc <= 232448 && PairSmem<false>::kAlloc <= 232448, "227 KB per CTA");
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// every thread of both CTAs
-__device__ __forceinline__ void pair_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// this shared-memory address in rank 0, and an arrival there
-__device__ __forceinline__ uint32_t in_rank0(const void* p) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
-  return a;
-}
-// ... releasing what this thread wrote to memory,
-__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-// ... or without: what the barrier is about lies in tensor memory, which
-// tcgen05's own fences order (a release over the cluster took 1000 to 1400
-// cycles of a 3400-cycle tile here)
-__device__ __forceinline__ void arrive_tmem_at(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-// a wait, bounded like every other, for what the other CTA did
-__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  auto done = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  if (done()) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 0;; ++it) {
-    if (done()) return true;
-    if ((it & 63u) == 63u) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) return false;
-    }
-  }
-}
 // TMA into this CTA's shared memory, its bytes counted on a barrier of rank 0
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int c0, int c1,
                                                  int c2, int c3) {

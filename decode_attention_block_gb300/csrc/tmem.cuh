@@ -34,7 +34,7 @@ __device__ __forceinline__ bool elect() {
   return is != 0;
 }
 
-// D (+)= A B^T, bf16 in, fp32 accumulate; A from shared memory ...
+// D (+)= A B^T, bf16 or fp16 in, fp32 accumulate; A from shared memory ...
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -43,7 +43,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// ... or from tensor memory (lane = row, two bf16 of a row per column)
+// ... or from tensor memory (lane = row, two elements of a row per column)
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -113,10 +113,10 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, uint32_t line,
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(line >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// Instruction descriptor of kind::f16: fp32 accumulator [4,6), bf16 A and B
-// [7,10), [10,13), B MN-major [16], N >> 3 [17,23), M >> 4 [24,29).
-__host__ __device__ constexpr uint32_t idesc(int m, int n, bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+// Instruction descriptor of kind::f16: fp32 accumulator [4,6), A and B bf16 (1)
+// or fp16 (0) [7,10), [10,13), B MN-major [16], N >> 3 [17,23), M >> 4 [24,29).
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool b_mn_major, bool fp16 = false) {
+  return (1u << 4) | (fp16 ? 0u : (1u << 7) | (1u << 10)) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
 
