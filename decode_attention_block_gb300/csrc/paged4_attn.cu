@@ -1,12 +1,11 @@
 // paged4_attn.cu -- attention of single new tokens over pages held in 4 bits.
 //
-// The schedule is that of paged_attn.cu: a group is one token's four query
-// heads of one KV head, the work list of 16-position tiles is split evenly
-// over the CTAs, the last CTA of a split group merges its partial states.  A
-// tile of one head is one block of K and one of V (fp4.cuh), 2304 contiguous
-// bytes each: a plain bulk copy, no tensor map.
+// A group is one token's four query heads of one KV head, as in paged_attn.cu:
+// the work list of tiles (32 positions here: two blocks of K, two of V) is split
+// evenly over the CTAs, the last CTA of a split group merges its partial states.
+// A block (fp4.cuh) is 2304 contiguous bytes: a plain bulk copy, no tensor map.
 //
-// A warp folds a block by itself, codes to fp16 in registers, straight into
+// A warp folds a tile by itself, codes to fp16 in registers, straight into
 // the fragments of mma.m16n8k16 (fp16 in, fp32 sums):
 //   s = K q^T      A = K (16 positions x 16 dims), B = [q_hi | q_lo]^T, the four
 //                  heads' queries as two fp16 halves
@@ -22,6 +21,19 @@
 // Queries are scaled by a power of two into fp16's range; scores take it back
 // in fp32.  The running maximum is raised once a score passes it by 2^8 (as in
 // the chunk kernels): most tiles cost one vote for it.
+//
+// With a quarter of the bytes of bf16 pages the instructions count: a tile costs
+// a warp some 1200, 256 conversions and 256 products among them, each two cycles
+// of its pipe.  So everything is done for 12 folding warps an SM at 168
+// registers, three a scheduler: no producer warp (each warp asks for its own
+// tiles, K and V by turns, three halves ahead), the walk over the groups in shared
+// memory, the queries' fragments too, and loops short enough for the instruction
+// cache.  64 sequences at 512-32768 (1.2 GB of pages): 338 us with a producer
+// warp, 16-position tiles and 8 folding warps an SM, 288 with 12 (of 128
+// registers), 275 with 8 and 32-position tiles, 245 with loops over their blocks,
+// 223 as it is: 5.4 TB/s, 0.80 of the measured copy bandwidth.  A pair of warps a
+// tile, each half of the output's dims, took 268.  One sequence at 700: 11 us,
+// latency.
 #include <math.h>
 
 #include <type_traits>
@@ -40,44 +52,56 @@ using namespace token;
 using paged::Cursor;
 using paged::Shape;
 
-constexpr int kThreads4 = (kConsumers + 1) * 32;
-constexpr int kBlocks4 = 2;      // CTAs per SM
-constexpr int kStages4 = 16;     // tiles in flight per CTA
-constexpr int kMinUnits4 = 4;    // tiles per CTA at least: one per consumer warp
+constexpr int kThreads4 = kConsumerThreads;
+constexpr int kTileBlocks = 2;   // of K and of V in a tile
+constexpr int kTile4 = kTileBlocks * fp4::kRows;  // positions of a tile
+constexpr int kCtas4 = 3;        // CTAs per SM
+constexpr int kSlots4 = 3;       // halves of tiles (K or V) a warp has room for
+constexpr int kMinUnits4 = 4;    // tiles per CTA at least: one per warp
 constexpr int kPad = 4;          // floats behind each 32 of a state in shared memory
-constexpr int kPRow = 20;        // floats of a head's probabilities of a tile (16, and a shift of banks)
+constexpr int kPRow = kTile4 + 4;  // floats of a head's scores of a tile, and a shift of banks
 constexpr float kRaise4 = 8.0f;
-static_assert(kStages4 % kConsumers == 0, "a stage serves one warp: no wait aliases an older phase");
+constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
+
+// The walk over the groups waits in shared memory, a copy for each warp, while
+// tiles are folded.
+constexpr int kWalkBytes = 128;
+static_assert(sizeof(paged::Share) <= kWalkBytes, "room for it");
 
 struct Smem4 {
-  static constexpr int kStage = 2 * fp4::kBlock;
-  static constexpr int kP = kStages4 * kStage;
+  static constexpr int kSlot = kTileBlocks * fp4::kBlock;
+  static constexpr int kWarp = kSlots4 * kSlot;  // a warp's slots
+  static constexpr int kQ = kConsumers * kWarp;
+  static constexpr int kP = kQ + kHeadDim / 32 * 32 * 16;
   static constexpr int kM = kP + kConsumers * 4 * kPRow * 4;
   static constexpr int kL = kM + kConsumers * 16;
-  static constexpr int kO = kL + kConsumers * 16;
-  static constexpr int kBars = kO + kConsumers * 4 * kStateFloats<kPad> * 4;
-  static constexpr int kFlags = kBars + 2 * kStages4 * 8;
-  static constexpr int kPrefix = kFlags + 16;
-  static constexpr int kBytes = kPrefix + 8 * (SPARK_MAX_BATCH + 2 + kThreads4 / 16);
+  static constexpr int kBars = kL + kConsumers * 16;
+  static constexpr int kFlags = kBars + kConsumers * kSlots4 * 8;
+  static constexpr int kWalk = kFlags + 16;
+  static constexpr int kBytes = kWalk + kConsumers * kWalkBytes;
+  // the prefix sums, before the first copy
+  static_assert(8 * (SPARK_MAX_BATCH + 2 + kThreads4 / 16) <= kQ, "room in the slots");
+  static_assert(4 * kStateFloats<kPad> * 4 <= kSlot, "a warp's state in a slot");
 };
 
-// the queries of a KV head as the B fragments of all 16-dim steps: step s holds
-// dims 64 t + 4 s .. + 3, column g head g & 3, its high half for g < 4
+// The queries of a KV head as the B fragments of all 16-dim steps, in shared
+// memory for all warps: step s holds dims 64 t + 4 s .. + 3, column g head g & 3,
+// its high half for g < 4; steps 2 i and 2 i + 1 of a lane are 16 bytes.
 struct Queries {
-  uint32_t b[kHeadDim / 16][2];
+  uint32_t b;      // [8][32] of 16 bytes, the lane's
   float scale[2];  // of the scores of heads 2 (t & 1) + j
 };
 
-__device__ __forceinline__ void load64(float (&x)[64], const float* q) {
+__device__ __forceinline__ void load16(float (&x)[16], const float* q) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + i);
     x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
   }
 }
-__device__ __forceinline__ void load64(float (&x)[64], const __nv_bfloat16* q) {
+__device__ __forceinline__ void load16(float (&x)[16], const __nv_bfloat16* q) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint4 v = __ldcg(reinterpret_cast<const uint4*>(q) + i);
     const float2 a = bf16x2_to_f32x2(v.x), b = bf16x2_to_f32x2(v.y), c = bf16x2_to_f32x2(v.z), d = bf16x2_to_f32x2(v.w);
     x[8 * i] = a.x; x[8 * i + 1] = a.y; x[8 * i + 2] = b.x; x[8 * i + 3] = b.y;
@@ -85,84 +109,160 @@ __device__ __forceinline__ void load64(float (&x)[64], const __nv_bfloat16* q) {
   }
 }
 
+// Every warp finds the heads' units, and puts a quarter of the steps down.
 template <typename QT>
-__device__ __forceinline__ void load_queries(Queries& Q, const QT* qg, float scale_log2, int lane) {
+__device__ __forceinline__ void load_queries(Queries& Q, uint4* q_s, const QT* qg, float scale_log2, int warp, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  float x[64];
-  load64(x, qg + (g & 3) * kHeadDim + 64 * t);
-  float m = 0.f;
+  const QT* mine = qg + (g & 3) * kHeadDim + 64 * t;
+  float m = 0.f, y[16];
 #pragma unroll
-  for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(x[i]));
+  for (int i = 0; i < 4; ++i) {
+    float x[16];
+    load16(x, mine + 16 * i);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      m = fmaxf(m, fabsf(x[e]));
+      y[e] = i == warp ? x[e] : y[e];
+    }
+  }
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const float2 unit = fp4::unit_of(m);
 #pragma unroll
-  for (int s = 0; s < kHeadDim / 16; ++s)
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      Q.b[s][i] = fp4::pack(fp4::split_part(x[4 * s + 2 * i] * unit.x, g >= 4),
-                            fp4::split_part(x[4 * s + 2 * i + 1] * unit.x, g >= 4));
+    for (int j = 0; j < 4; ++j)
+      h[j] = fp4::pack(fp4::split_part(y[8 * i + 2 * j] * unit.x, g >= 4), fp4::split_part(y[8 * i + 2 * j + 1] * unit.x, g >= 4));
+    q_s[32 * (2 * warp + i) + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  Q.b = smem_u32(q_s + lane);
 #pragma unroll
   for (int j = 0; j < 2; ++j) Q.scale[j] = scale_log2 * __shfl_sync(0xffffffffu, unit.y, 4 * (2 * (t & 1) + j));
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Shared memory by its own addresses.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+
+// A lane's places in a block: its first chunk of rows g and g + 8 of K and their
+// scales, its chunk of row 4 t of V (of row 4 t + j at ^ 16 (j & 1), 128 j behind)
+// and its scales.
+struct Places {
+  uint32_t ka, kb, ks, v, vs;
+  __device__ __forceinline__ explicit Places(int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    ka = (uint32_t)fp4::code_at(g, 64 * t);
+    kb = (uint32_t)fp4::code_at(g + 8, 64 * t);
+    ks = (uint32_t)fp4::scale_at(g, 64 * t);
+    v = (uint32_t)fp4::code_at(4 * t, 32 * g);
+    vs = (uint32_t)fp4::scale_at(4 * t, 32 * g);
+  }
+};
+
 // Byte `i` of a word of scales as an fp16 pair of it.
 __device__ __forceinline__ uint32_t scale2(uint32_t w, int i) { return __byte_perm(w, 0u, 0x4040u | (uint32_t)(i | (i << 8))) << 7; }
 
-// One warp folds rows [r0, r1) of a block of K and V into its state (o[i]: dims
-// 32 g + 2 i in [0], [1], the next in [2], [3], columns 2 t and 2 t + 1; l: this
-// lane's rows only).  p_w: the warp's 4 x kPRow probability scratch.
-__device__ __forceinline__ void fold_block(const unsigned char* kst, const unsigned char* vst, int r0, int r1,
-                                           const Queries& Q, float* p_w, MmaState& st) {
+// One warp's running state: o[i] holds dims 32 g + 2 i in [0], [1], the next in
+// [2], [3], of columns 2 t and 2 t + 1; m the maxima (base 2) of the columns'
+// heads 2 (t & 1) + j, mg of head g & 3, l the sum of head g & 3 over positions 4
+// t .. 4 t + 3 of every block.
+struct State4 {
+  float o[kHeadDim / 16][4];
+  float m[2], mg, l;
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < kHeadDim / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m[0] = m[1] = mg = -INFINITY;
+    l = 0.f;
+  }
+};
+
+// One warp folds rows [r0, r1) of a tile into its state: first K's blocks, their
+// scores into the warp's 4 x kPRow scratch and the lane's maxima, then V's.  Rows
+// outside may hold anything.  (The loops over blocks are not unrolled, see above.)
+__device__ __forceinline__ void fold_keys(uint32_t kst, int r0, int r1, const Queries& Q, const Places& at, uint32_t p_w,
+                                          float (&mx)[2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool whole = r0 == 0 && r1 == fp4::kRows;
-  // s = K q^T, even and odd steps in two chains
-  float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
-  {
-    const uint32_t sa = *reinterpret_cast<const uint32_t*>(kst + fp4::scale_at(g, 64 * t));
-    const uint32_t sb = *reinterpret_cast<const uint32_t*>(kst + fp4::scale_at(g + 8, 64 * t));
+  const bool whole = r0 == 0 && r1 == kTile4;
+  mx[0] = mx[1] = -INFINITY;
+  __syncwarp();  // the scratch is free
+#pragma unroll 1
+  for (int blk = 0; blk < kTileBlocks; ++blk) {
+    const uint32_t kb = kst + blk * fp4::kBlock;
+    // s = K q^T, even and odd steps in two chains
+    float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t sa = lds32(kb + at.ks), sb = lds32(kb + at.ks + 8 * fp4::kScales);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 ka = *reinterpret_cast<const uint4*>(kst + fp4::code_at(g, 64 * t + 32 * i));
-      const uint4 kb = *reinterpret_cast<const uint4*>(kst + fp4::code_at(g + 8, 64 * t + 32 * i));
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+      const uint4 xa = lds128(kb + (at.ka ^ (uint32_t)(16 * i))), xb = lds128(kb + (at.kb ^ (uint32_t)(16 * i)));
+      const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t fa = scale2(sa, 2 * i + (w >> 1)), fb = scale2(sb, 2 * i + (w >> 1));
+        const uint32_t fa = scale2(sa, w >> 1), fb = scale2(sb, w >> 1);
         uint32_t ha[4], hb[4];
         fp4::halves8(wa[w], ha);
         fp4::halves8(wb[w], hb);
         const uint32_t a0[4] = {fp4::mul2(ha[0], fa), fp4::mul2(hb[0], fb), fp4::mul2(ha[1], fa), fp4::mul2(hb[1], fb)};
         const uint32_t a1[4] = {fp4::mul2(ha[2], fa), fp4::mul2(hb[2], fb), fp4::mul2(ha[3], fa), fp4::mul2(hb[3], fb)};
-        const int s = 8 * i + 2 * w;
-        mma_f16(c, a0, Q.b[s][0], Q.b[s][1]);
-        mma_f16(c2, a1, Q.b[s + 1][0], Q.b[s + 1][1]);
+        const uint4 qb = lds128(Q.b + 512 * (4 * i + w));
+        mma_f16(c, a0, qb.x, qb.y);
+        mma_f16(c2, a1, qb.z, qb.w);
       }
+      sa >>= 16;
+      sb >>= 16;
+    }
+    // hi and lo columns, scale, mask: c[2 r + j] is row g + 8 r, head 2 (t & 1) + j
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] += c2[e];
+      c[e] += __shfl_xor_sync(0xffffffffu, c[e], 2);
+      c[e] *= Q.scale[e & 1];
+    }
+    if (!whole) {
+      const int row = 16 * blk + g;
+      if (row < r0 || row >= r1) c[0] = c[1] = -INFINITY;
+      if (row + 8 < r0 || row + 8 >= r1) c[2] = c[3] = -INFINITY;
+    }
+    mx[0] = fmaxf(mx[0], fmaxf(c[0], c[2]));
+    mx[1] = fmaxf(mx[1], fmaxf(c[1], c[3]));
+    if (t < 2) {
+      const uint32_t to = p_w + 4 * (2 * t * kPRow + 16 * blk + g);
+      sts32(to, c[0]);
+      sts32(to + 4 * kPRow, c[1]);
+      sts32(to + 32, c[2]);
+      sts32(to + 4 * kPRow + 32, c[3]);
     }
   }
-  // hi and lo columns, scale, mask: sc[r][j] = row g + 8 r, head 2 (t & 1) + j
-  float sc[2][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] += c2[i];
-    c[i] += __shfl_xor_sync(0xffffffffu, c[i], 2);
-    sc[i >> 1][i & 1] = c[i] * Q.scale[i & 1];
-  }
-  if (!whole) {
-    if (g < r0 || g >= r1) sc[0][0] = sc[0][1] = -INFINITY;
-    if (g + 8 < r0 || g + 8 >= r1) sc[1][0] = sc[1][1] = -INFINITY;
-  }
-  const float m0 = fmaxf(sc[0][0], sc[1][0]), m1 = fmaxf(sc[0][1], sc[1][1]);
-  if (__any_sync(0xffffffffu, m0 > st.m[0] + kRaise4 || m1 > st.m[1] + kRaise4)) {
-    float mx[2] = {m0, m1}, corr[2];
+}
+
+__device__ __forceinline__ void fold_values(uint32_t vst, int r0, int r1, const Places& at, uint32_t p_w, float (&mx)[2], State4& st) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const bool whole = r0 == 0 && r1 == kTile4;
+  if (__any_sync(0xffffffffu, mx[0] > st.m[0] + kRaise4 || mx[1] > st.m[1] + kRaise4)) {
+    float corr[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
@@ -171,8 +271,12 @@ __device__ __forceinline__ void fold_block(const unsigned char* kst, const unsig
       const float mn = fmaxf(st.m[j], mx[j]);
       corr[j] = st.m[j] == -INFINITY ? 0.f : exp2f(st.m[j] - mn);
       st.m[j] = mn;
-      st.l[j] *= corr[j];
     }
+    // of head g & 3: the lane t = (g & 3) / 2 has it
+    const float m0 = __shfl_sync(0xffffffffu, st.m[0], (g & 3) >> 1), m1 = __shfl_sync(0xffffffffu, st.m[1], (g & 3) >> 1);
+    const float mn = (g & 1) ? m1 : m0;
+    st.l *= st.mg == -INFINITY ? 0.f : exp2f(st.mg - mn);
+    st.mg = mn;
 #pragma unroll
     for (int i = 0; i < kHeadDim / 16; ++i) {
       st.o[i][0] *= corr[0];
@@ -181,116 +285,162 @@ __device__ __forceinline__ void fold_block(const unsigned char* kst, const unsig
       st.o[i][3] *= corr[1];
     }
   }
-  // (a row that is masked, or a maximum of -inf under it, is a probability of 0)
-  float pr[2][2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float ref = st.m[j] == -INFINITY ? 0.f : st.m[j];
-    pr[0][j] = ex2(sc[0][j] - ref);
-    pr[1][j] = ex2(sc[1][j] - ref);
-    st.l[j] += pr[0][j] + pr[1][j];
-  }
+  const float ref = st.mg == -INFINITY ? 0.f : st.mg;
   __syncwarp();
-  if (t < 2) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      p_w[(2 * t + j) * kPRow + g] = pr[0][j];
-      p_w[(2 * t + j) * kPRow + g + 8] = pr[1][j];
-    }
-  }
-  __syncwarp();
-  // B fragments of [p_hi | p_lo]^T: the MMA's steps 2 t, 2 t + 1, 2 t + 8, 2 t +
-  // 9 are positions 4 t .. 4 t + 3
-  const float4 p4 = *reinterpret_cast<const float4*>(p_w + (g & 3) * kPRow + 4 * t);
-  const uint32_t pb0 = fp4::pack(fp4::split_part(p4.x, g >= 4), fp4::split_part(p4.y, g >= 4));
-  const uint32_t pb1 = fp4::pack(fp4::split_part(p4.z, g >= 4), fp4::split_part(p4.w, g >= 4));
-  // o^T += V^T p^T
-  uint32_t v[4][4], f01[2], f23[2];
-  {
-    uint32_t s[4];
+  // p, and o^T += V^T p^T
+#pragma unroll 1
+  for (int blk = 0; blk < kTileBlocks; ++blk) {
+    const uint32_t vb = vst + blk * fp4::kBlock;
+    uint32_t v[4][4], f01[2], f23[2], s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = 4 * t + j;
-      const uint4 x = *reinterpret_cast<const uint4*>(vst + fp4::code_at(row, 32 * g));
+      const uint4 x = lds128(vb + (at.v ^ (uint32_t)(16 * (j & 1))) + j * fp4::kCodes);
       v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-      s[j] = *reinterpret_cast<const uint16_t*>(vst + fp4::scale_at(row, 32 * g));
+      s[j] = lds16(vb + at.vs + j * fp4::kScales);
       // (0 times whatever a row outside holds, a NaN's scale included)
-      if (!whole && (row < r0 || row >= r1)) s[j] = 0;
+      if (!whole && (16 * blk + row < r0 || 16 * blk + row >= r1)) s[j] = 0;
     }
+    // B fragments of [p_hi | p_lo]^T: the MMA's steps 2 t, 2 t + 1, 2 t + 8, 2 t +
+    // 9 are positions 4 t .. 4 t + 3 (a masked one's probability is 0, also
+    // under a maximum of -inf)
+    const uint4 s4 = lds128(p_w + 4 * ((g & 3) * kPRow + 16 * blk + 4 * t));
+    const float4 p4 = make_float4(ex2(__uint_as_float(s4.x) - ref), ex2(__uint_as_float(s4.y) - ref),
+                                  ex2(__uint_as_float(s4.z) - ref), ex2(__uint_as_float(s4.w) - ref));
+    st.l += (p4.x + p4.y) + (p4.z + p4.w);
+    const uint32_t pb0 = fp4::pack(fp4::split_part(p4.x, g >= 4), fp4::split_part(p4.y, g >= 4));
+    const uint32_t pb1 = fp4::pack(fp4::split_part(p4.z, g >= 4), fp4::split_part(p4.w, g >= 4));
     const uint32_t s01 = s[0] | (s[1] << 16), s23 = s[2] | (s[3] << 16);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f01[u] = ((s01 >> (8 * u)) & 0x00FF00FFu) << 7;
       f23[u] = ((s23 >> (8 * u)) & 0x00FF00FFu) << 7;
     }
-  }
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    // bytes of one dim of two rows: even dims, odd dims
-    constexpr uint32_t kLow = 0x0F0F0F0Fu;
-    uint32_t e01[4], d01[4], e23[4], d23[4];
-    fp4::halves8((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), e01);
-    fp4::halves8(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), d01);
-    fp4::halves8((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), e23);
-    fp4::halves8(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), d23);
+    for (int w = 0; w < 4; ++w) {
+      // bytes of one dim of two rows: even dims, odd dims
+      constexpr uint32_t kLow = 0x0F0F0F0Fu;
+      uint32_t e01[4], d01[4], e23[4], d23[4];
+      fp4::halves8((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), e01);
+      fp4::halves8(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), d01);
+      fp4::halves8((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), e23);
+      fp4::halves8(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), d23);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint32_t a[4] = {fp4::mul2(e01[b], f01[w >> 1]), fp4::mul2(d01[b], f01[w >> 1]),
-                             fp4::mul2(e23[b], f23[w >> 1]), fp4::mul2(d23[b], f23[w >> 1])};
-      mma_f16(st.o[4 * w + b], a, pb0, pb1);
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t a[4] = {fp4::mul2(e01[b], f01[w >> 1]), fp4::mul2(d01[b], f01[w >> 1]),
+                               fp4::mul2(e23[b], f23[w >> 1]), fp4::mul2(d23[b], f23[w >> 1])};
+        mma_f16(st.o[4 * w + b], a, pb0, pb1);
+      }
     }
   }
 }
 
 // Put one warp's state into the merge scratch: the hi and lo columns and the
 // lanes' sums added.
-__device__ __forceinline__ void store_state4(MmaState& st, const MergeSmem& sm) {
+__device__ __forceinline__ void store_state4(State4& st, const MergeSmem& sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < kHeadDim / 16; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) st.o[i][k] += __shfl_xor_sync(0xffffffffu, st.o[i][k], 2);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    st.l[j] += __shfl_xor_sync(0xffffffffu, st.l[j], 4);
-    st.l[j] += __shfl_xor_sync(0xffffffffu, st.l[j], 8);
-    st.l[j] += __shfl_xor_sync(0xffffffffu, st.l[j], 16);
+  st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
+  st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
+  if (lane < 16 && t == 0) {
+    sm.ms[warp * 4 + g] = st.mg;
+    sm.ls[warp * 4 + g] = st.l;
   }
   if (t < 2) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int h = 2 * t + j;
-      float* os = sm.os + (warp * 4 + h) * kStateFloats<kPad> + state_at<kPad>(32 * g);
+      float* os = sm.os + warp * (Smem4::kWarp / 4) + h * kStateFloats<kPad> + state_at<kPad>(32 * g);
 #pragma unroll
       for (int i = 0; i < kHeadDim / 16; i += 2)
         *reinterpret_cast<float4*>(os + 2 * i) = make_float4(st.o[i][j], st.o[i][2 + j], st.o[i + 1][j], st.o[i + 1][2 + j]);
-      if (g == 0) {
-        sm.ms[warp * 4 + h] = st.m[j];
-        sm.ls[warp * 4 + h] = st.l[j];
-      }
     }
   }
 }
 
+// A warp's way through its tiles of a group (every kConsumers-th of the CTA's):
+// item 2 j is K of its tile j, 2 j + 1 V; the copies run kSlots4 items ahead.  A
+// warp fills its own slots, lanes 0 and 1 a block each, so nothing but the copies'
+// own barriers is waited for.
+struct Stream {
+  uint32_t slots, bars;  // shared addresses
+  uint32_t fill, use;    // slots filled and used next
+  uint32_t phase;        // of the slot used next
+  uint32_t block;        // of lane 2 i + b: block b of tile i of the 16 looked up
+  int issued, items;     // of this group
+  int x0;                // first position of the group's first tile of the warp
+
+  __device__ __forceinline__ void begin(int x, int tiles) {
+    x0 = x;
+    issued = 0;
+    items = 2 * tiles;
+  }
+  __device__ __forceinline__ uint32_t slot() const { return slots + use * Smem4::kSlot; }
+  __device__ __forceinline__ void issue(const Args& p, const Cursor& cur, const unsigned char* pk, const unsigned char* pv,
+                                        int lane) {
+    if (issued >= items) return;
+    if ((issued & 31) == 0) {
+      const int tile = (issued >> 1) + (lane >> 1), x = x0 + tile * (kConsumers * kTile4) + (lane & 1) * fp4::kRows;
+      block = kNoBlock;
+      if (2 * tile < items && x <= cur.g.hi && x + fp4::kRows > cur.g.lo) {
+        const int col = paged::page_col(p, x), in_page = (x - col * p.page_size) / fp4::kRows;
+        const int page = paged::page_of(p, paged::page_entry(p, cur.s, col));
+        // (pages * page_size < 2^31: the blocks of all heads are below 2^30)
+        block = ((uint32_t)page * (uint32_t)(p.page_size / fp4::kRows) + (uint32_t)in_page) * (uint32_t)p.n_kv + (uint32_t)cur.j;
+      }
+    }
+    const uint32_t mine = __shfl_sync(0xffffffffu, block, (issued & 30) | (lane & 1));
+    if (lane < 2) {
+      const uint32_t bar = bars + 8 * fill;
+      if (mine != kNoBlock) {
+        const unsigned char* from = ((issued & 1) ? pv : pk) + (uint64_t)mine * fp4::kBlock;
+        asm volatile(
+            "{\n\t.reg .b64 st;\n\t"
+            "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 st, [%0], %1;\n\t"
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%2], [%3], %1, [%0];\n\t}" ::"r"(bar),
+            "r"(fp4::kBlock), "r"(slots + fill * Smem4::kSlot + lane * fp4::kBlock), "l"(reinterpret_cast<uint64_t>(from))
+            : "memory");
+      } else {
+        asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.release.cta.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
+      }
+    }
+    ++issued;
+    fill = fill + 1 == kSlots4 ? 0 : fill + 1;
+  }
+  __device__ __forceinline__ bool wait(volatile int* abort) const {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 q, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(done)
+        : "r"(bars + 8 * use), "r"(phase)
+        : "memory");
+    if (__all_sync(0xffffffffu, done != 0)) return true;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bars + 8 * use));
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, abort, kWaitLimitNs));
+  }
+  __device__ __forceinline__ void advance() {
+    const bool last = use + 1 == kSlots4;
+    use = last ? 0 : use + 1;
+    phase ^= last ? 1u : 0u;
+  }
+};
+
 template <typename QT>
-__global__ void __launch_bounds__(kThreads4, kBlocks4)
+__global__ void __launch_bounds__(kThreads4, kCtas4)
     k_paged4_token(const unsigned char* pk, const unsigned char* pv, const __grid_constant__ Args p) {
   using S = Smem4;
   extern __shared__ __align__(128) unsigned char base[];
-  float* p_s = reinterpret_cast<float*>(base + S::kP);
-  const MergeSmem msm{reinterpret_cast<float*>(base + S::kM), reinterpret_cast<float*>(base + S::kL),
-                      reinterpret_cast<float*>(base + S::kO)};
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(base + S::kBars);
-  uint64_t* empty_bar = full_bar + kStages4;
   volatile int* flags = reinterpret_cast<volatile int*>(base + S::kFlags);  // [0] abort, [1] last
-  int64_t* prefix = reinterpret_cast<int64_t*>(base + S::kPrefix);
-
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t p_w = smem_u32(base + S::kP) + warp * 16 * kPRow;
+  const Places places(lane);
   if (tid == 0) {
-    for (int s = 0; s < kStages4; ++s) {
-      mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1);
-    }
+    for (int s = 0; s < kConsumers * kSlots4; ++s) mbar_init(reinterpret_cast<uint64_t*>(base + S::kBars) + s, 2);
     flags[0] = 0;
     flags[1] = 0;
     fence_mbar_init();
@@ -298,95 +448,90 @@ __global__ void __launch_bounds__(kThreads4, kBlocks4)
   // tables, lengths, rows and queries may come from the kernel before
   pdl_wait();
   pdl_trigger();
-  const Shape sh{1, kTile, p.window};
+  const Shape sh{1, kTile4, p.window};
   const int c = blockIdx.x;
   paged::Share share;
-  if (!paged::find_share<kThreads4>(p, sh, c, kMinUnits4, gridDim.x, prefix, share)) return;
-  const int64_t total = share.total, u0 = share.u0, u1 = share.u1;
-  const int G = share.G;
-  Cursor cur = share.cur;
-  if (warp == kConsumers) {
-    // ---- the producer: the tiles of the share, a stage of the ring each
-    uint32_t k = 0;
-    bool ok = true;
-    for (;;) {
-      const int64_t t1 = cur.end < u1 ? cur.end : u1;
-      for (int64_t u = cur.begin > u0 ? cur.begin : u0; ok && u < t1; u += 32) {
-        // the blocks of the next 32 tiles, one per lane
-        const int n = t1 - u < 32 ? (int)(t1 - u) : 32;
-        const int pos = (cur.g.tile0 + (int)(u - cur.begin) + lane) * kTile;
-        int64_t at = 0;
-        if (lane < n)
-          at = fp4::block_at(paged::page_of(p, paged::page_entry(p, cur.s, paged::page_col(p, pos))),
-                             paged::page_row(p, pos), cur.j, p.page_size, p.n_kv);
-        for (int i = 0; i < n; ++i, ++k) {
-          const int64_t from = __shfl_sync(0xffffffffu, at, i);
-          if (lane == 0) {
-            const int s = (int)(k % kStages4);
-            const uint32_t r = k / kStages4;
-            if (r > 0 && !mbar_wait_bounded(&empty_bar[s], (r - 1) & 1, flags, kWaitLimitNs)) {
-              ok = false;
-              flags[0] = 1;
-              atomicOr(p.err, kErrWaitTimeout);
-            }
-            if (ok) {
-              mbar_arrive_expect_tx(&full_bar[s], S::kStage);
-              bulk_load(base + s * S::kStage, pk + from, fp4::kBlock, &full_bar[s]);
-              bulk_load(base + s * S::kStage + fp4::kBlock, pv + from, fp4::kBlock, &full_bar[s]);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-          if (!ok) break;
-        }
-      }
-      if (!ok || cur.end >= u1) break;
-      cur.next(p, sh);
-    }
-    if (lane == 0 && flags[0]) {
-      // let the copies in flight land before the CTA can exit
-      int never = 0;
-      for (uint32_t i = k > kStages4 ? k - kStages4 : 0; i < k; ++i)
-        mbar_wait_bounded(&full_bar[i % kStages4], (i / kStages4) & 1, &never, kWaitLimitNs);
-    }
-    return;
-  }
-  // ---- consumers
-  uint32_t k = 0;
+  if (!paged::find_share<kThreads4>(p, sh, c, kMinUnits4, gridDim.x, reinterpret_cast<int64_t*>(base), share)) return;
+  paged::Share& walk = *reinterpret_cast<paged::Share*>(base + S::kWalk + warp * kWalkBytes);
+  if (lane == 0) walk = share;
+  __syncthreads();  // the prefix sums have been read
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // and make way for the copies
+  Stream in;
+  in.slots = smem_u32(base) + warp * S::kWarp;
+  in.bars = smem_u32(base + S::kBars) + warp * kSlots4 * 8;
+  in.fill = in.use = in.phase = 0;
+  int skip = warp;  // the CTA's tiles before the warp's next one
   Queries Q;
-  MmaState st;
-  const QT* q = static_cast<const QT*>(p.q);
-  QT* a = static_cast<QT*>(p.a);
+  State4 st;
+  bool ok = true;
   for (;;) {
-    const int64_t t1 = cur.end < u1 ? cur.end : u1;
-    const int64_t row = cur.seq.q0 + cur.g.tok;
-    named_bar_sync(kBarConsumers, kConsumerThreads);  // the previous group's merge is done
-    load_queries(Q, q + row * p.q_ld + (int64_t)cur.j * kGroup * kHeadDim, p.scale_log2, lane);
-    st.reset();
-    const Parts parts(cur.begin, cur.end, total, G, c);
-    for (int64_t u = cur.begin > u0 ? cur.begin : u0; u < t1; ++u, ++k) {
-      if ((int)(k % kConsumers) != warp) continue;
-      const int s = (int)(k % kStages4);
-      const bool ok =
-          __all_sync(0xffffffffu, !flags[0] && mbar_wait_bounded(&full_bar[s], (k / kStages4) & 1, flags, kWaitLimitNs));
-      if (!ok) {
-        if (lane == 0 && !flags[0]) {
-          flags[0] = 1;
-          atomicOr(p.err, kErrWaitTimeout);
-        }
-      } else {
-        const int pos = (cur.g.tile0 + (int)(u - cur.begin)) * kTile;
-        const int r0 = cur.g.lo > pos ? cur.g.lo - pos : 0;
-        const int r1 = cur.g.hi + 1 - pos < kTile ? cur.g.hi + 1 - pos : kTile;
-        const unsigned char* kst = base + s * S::kStage;
-        fold_block(kst, kst + fp4::kBlock, r0, r1, Q, p_s + warp * 4 * kPRow, st);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty_bar[s]);
+    int n, tiles, pos, lo, hi;
+    {
+      const paged::Share w = walk;
+      const int64_t t0 = w.cur.begin > w.u0 ? w.cur.begin : w.u0, t1 = w.cur.end < w.u1 ? w.cur.end : w.u1;
+      n = (int)(t1 - t0);
+      tiles = skip < n ? (n - skip + kConsumers - 1) / kConsumers : 0;
+      pos = (w.cur.g.tile0 + (int)(t0 - w.cur.begin) + skip) * kTile4;
+      lo = w.cur.g.lo;
+      hi = w.cur.g.hi;
     }
+    in.begin(pos, tiles);
+    skip += tiles * kConsumers - n;
+#pragma unroll 1
+    for (int i = 0; i < kSlots4; ++i) in.issue(p, walk.cur, pk, pv, lane);
+    load_queries(Q, reinterpret_cast<uint4*>(base + S::kQ),
+                 static_cast<const QT*>(p.q) + (int64_t)(walk.cur.seq.q0 + walk.cur.g.tok) * p.q_ld + walk.cur.j * (kGroup * kHeadDim),
+                 p.scale_log2, warp, lane);
+    st.reset();
+    named_bar_sync(kBarConsumers, kConsumerThreads);  // the queries are there
+    int done = 0;  // items
+    auto landed = [&] {
+      ok = ok && in.wait(flags);
+      return ok;
+    };
+    auto used = [&] {
+      ++done;
+      in.advance();
+      __syncwarp();  // the slot has been read
+      in.issue(p, walk.cur, pk, pv, lane);
+    };
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i, pos += kConsumers * kTile4) {
+      const int r0 = lo > pos ? lo - pos : 0, r1 = hi + 1 - pos < kTile4 ? hi + 1 - pos : kTile4;
+      float mx[2];
+      if (!landed()) break;
+      fold_keys(in.slot(), r0, r1, Q, places, p_w, mx);
+      used();
+      if (!landed()) break;
+      fold_values(in.slot(), r0, r1, places, p_w, mx, st);
+      used();
+    }
+    if (!ok) {
+      if (lane == 0) {
+        if (!flags[0]) atomicOr(p.err, kErrWaitTimeout);
+        flags[0] = 1;
+      }
+      // let the copies in flight land before the CTA can exit
+      for (; done < in.issued; ++done) {
+        int never = 0;
+        mbar_wait_bounded(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(in.bars + 8 * in.use)), in.phase, &never, kWaitLimitNs);
+        in.advance();
+      }
+    }
+    // the warps' states lie in a slot of each: the slots are all free now
+    const MergeSmem msm{reinterpret_cast<float*>(base + S::kM), reinterpret_cast<float*>(base + S::kL),
+                        reinterpret_cast<float*>(base)};
     store_state4(st, msm);
-    finish_group<QT, kPad>(msm, flags, p, a + (row * p.n_kv + cur.j) * kGroup * kHeadDim, parts);
-    if (cur.end >= u1) break;
+    Cursor cur = walk.cur;
+    finish_group<QT, kPad, S::kWarp / 4>(
+        msm, flags, p, static_cast<QT*>(p.a) + ((int64_t)(cur.seq.q0 + cur.g.tok) * p.n_kv + cur.j) * (kGroup * kHeadDim),
+        Parts(cur.begin, cur.end, walk.total, walk.G, c));
+    if (cur.end >= walk.u1) break;
     cur.next(p, sh);
+    __syncwarp();
+    if (lane == 0) walk.cur = cur;
+    named_bar_sync(kBarConsumers, kConsumerThreads);  // the states have been read
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // and make way for the copies
   }
 }
 
@@ -396,9 +541,9 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem4::kBytes);
   if (e != cudaSuccess) return e;
   // no more CTAs than the tables' rows could give work to
-  const int64_t parts = ((int64_t)p.max_pages * (p.page_size / kTile) + kMinUnits4 - 1) / kMinUnits4;
+  const int64_t rows = (int64_t)p.max_pages * p.page_size, parts = (rows + kTile4 * kMinUnits4 - 1) / (kTile4 * kMinUnits4);
   const int64_t most = (int64_t)p.n_seqs * p.n_kv * p.max_q * parts;
-  int grid = kBlocks4 * device_sm_count();
+  int grid = kCtas4 * device_sm_count();
   if (grid > paged::kMaxCtas) grid = paged::kMaxCtas;
   if (grid > most) grid = (int)most;
   return launch_pdl(kern, dim3(grid), dim3(kThreads4), Smem4::kBytes, st, static_cast<const unsigned char*>(k),

@@ -10,7 +10,7 @@ namespace spark {
 namespace paged {
 
 // CTAs of an attention launch at most (two partial slots each)
-constexpr int kMaxCtas = 320;
+constexpr int kMaxCtas = 480;
 // the chunk kernel: tokens of a group, CTAs at most, floats of a partial
 // state (128 rows of 256 dims, their maxima, their sums)
 constexpr int kChunkTokens = 32;

@@ -44,9 +44,9 @@ constexpr int kStateFloats = kHeadDim + kHeadDim / 32 * PAD;
 // The group's state from the consumer warps' states in `sm`: finished if
 // whole, else this CTA's partial; the last of the group's CTAs to arrive
 // merges them in CTA order.  Warp h takes query head h, lane l its dims
-// [8 l, 8 l + 8).  (The parts are worked out before the tiles arrive: their
+// [8 l, 8 l + 8); the warps' states are WARP floats apart.  (The parts are worked out before the tiles arrive: their
 // divisions took up to 2000 cycles here.)
-template <typename QT, int PAD = 0>
+template <typename QT, int PAD = 0, int WARP = 4 * kStateFloats<PAD>>
 __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* flags, const Args& p, QT* a_head0,
                                              const Parts& parts) {
   const int tid = threadIdx.x, h = tid >> 5, lane = tid & 31;
@@ -62,7 +62,7 @@ __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* 
     const float mw = sm.ms[w * 4 + h];
     const float scl = mw == -INFINITY ? 0.f : exp2f(mw - M);
     L = fmaf(sm.ls[w * 4 + h], scl, L);
-    const float4* src = reinterpret_cast<const float4*>(sm.os + (w * 4 + h) * kStateFloats<PAD> + state_at<PAD>(8 * lane));
+    const float4* src = reinterpret_cast<const float4*>(sm.os + w * WARP + h * kStateFloats<PAD> + state_at<PAD>(8 * lane));
     const float4 x0 = src[0], x1 = src[1];
     O[0] = fmaf(x0.x, scl, O[0]); O[1] = fmaf(x0.y, scl, O[1]);
     O[2] = fmaf(x0.z, scl, O[2]); O[3] = fmaf(x0.w, scl, O[3]);
