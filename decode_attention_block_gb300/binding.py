@@ -191,8 +191,8 @@ _SIGNATURES = {
     "spark_beam_select": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_int32, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P,
                                          ctypes.c_size_t, _P]),
-    "spark_beam_reorder": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.POINTER(SparkBeamState), ctypes.c_int32,
-                                          _P, ctypes.c_size_t, _P]),
+    # (states: an array of SparkBeamState, or its bytes)
+    "spark_beam_reorder": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "spark_attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "spark_attn_abi_version": (ctypes.c_int32, []),
 }
@@ -377,6 +377,21 @@ def _rows(t: torch.Tensor, name: str) -> tuple:
     if len(shape) != 2 or stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must be a matrix with contiguous rows")
     return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1], code
+
+
+def _matrix(t: torch.Tensor, name: str, shape: tuple, device: int) -> tuple:
+    """As _rows, of a matrix of this shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise _not_here(t, name)
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [n_tokens, {shape[1]}]")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1], code
 
 
 @dataclass
@@ -691,9 +706,10 @@ def spark_rope_table(geom: SparkGeom, layer_class: int, rope: torch.Tensor, stre
 
 def _rope_rows(geom: SparkGeom, layer_class: int, rope: torch.Tensor) -> int:
     half = (geom.full_rotary_dim if layer_class == SPARK_FULL else geom.head_dim) // 2
-    if rope.dim() != 3 or rope.shape[1] != half or rope.shape[2] != 2:
+    shape = rope.shape
+    if shape[1:] != (half, 2):
         raise ValueError(f"rope must be [n_positions, {half}, 2]")
-    return int(rope.shape[0])
+    return shape[0]
 
 
 def spark_paged_rope_append(geom: SparkGeom, q, k: torch.Tensor, v: torch.Tensor, layer_class: int, rope: torch.Tensor,
@@ -702,18 +718,16 @@ def spark_paged_rope_append(geom: SparkGeom, q, k: torch.Tensor, v: torch.Tensor
     may be q; both None: no queries) and their keys, and write the rows k, v
     [n_tokens, n_kv * 256] into their pages.  q, k and v have one row stride
     (slices of a fused projection's rows); rope: spark_rope_table's."""
-    kp, ld, dt = _rows(k, "k")
-    vp, vld, vdt = _rows(v, "v")
-    n, kv_dim, q_dim = batch.n_tokens, geom.n_kv * geom.head_dim, geom.n_q * geom.head_dim
-    if k.shape != (n, kv_dim) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [n_tokens, {kv_dim}]")
+    device, head_dim = _current_device(), geom.head_dim
+    kv_shape = (batch.n_tokens, geom.n_kv * head_dim)
+    kp, ld, dt = _matrix(k, "k", kv_shape, device)
+    vp, vld, vdt = _matrix(v, "v", kv_shape, device)
     qp, op, old = None, None, 0
     if q is not None:
-        qp, qld, qdt = _rows(q, "q")
-        op, old, odt = _rows(q_out, "q_out")
-        if q.shape != (n, q_dim) or q_out.shape != q.shape:
-            raise ValueError(f"q and q_out must be [n_tokens, {q_dim}]")
-        if n == 1:  # a single row has no stride
+        q_shape = (batch.n_tokens, geom.n_q * head_dim)
+        qp, qld, qdt = _matrix(q, "q", q_shape, device)
+        op, old, odt = _matrix(q_out, "q_out", q_shape, device)
+        if batch.n_tokens == 1:  # a single row has no stride
             ld = vld = qld
         if qdt != dt or odt != dt or qld != ld:
             raise ValueError("q, q_out, k and v must have the same dtype, q, k and v the same row stride")
@@ -722,7 +736,7 @@ def spark_paged_rope_append(geom: SparkGeom, q, k: torch.Tensor, v: torch.Tensor
     if vdt != dt or vld != ld:
         raise ValueError("k and v must have the same dtype and row stride")
     pc, bc = _pool_c(geom, pool), _batch_c(batch)
-    _check(load().spark_paged_rope_append(ctypes.byref(geom), qp, kp, vp, ld, dt, int(layer_class),
+    _check(load().spark_paged_rope_append(ctypes.byref(geom), qp, kp, vp, ld, dt, layer_class,
                                           _here(rope, "rope", torch.float32), _rope_rows(geom, layer_class, rope),
                                           ctypes.byref(pc), ctypes.byref(bc), op, old, _here(ws, "workspace"), ws.nbytes,
                                           _stream(stream)), "spark_paged_rope_append")
@@ -856,13 +870,17 @@ def make_beam_workspace(n_groups: int, n_beams: int, device=None, stream=None) -
     return _workspace(spark_beam_workspace_bytes(n_groups, n_beams), "number of groups or beams", device, stream)
 
 
-def _slots(t, name: str, n: int, dtype=torch.int32):
-    """Address of a list of n slots' values; None: none."""
+def _slots(t, name: str, shape: tuple, device: int, dtype=torch.int32):
+    """Address of a list of a value for each slot; None: none."""
     if t is None:
         return None
-    if t.shape != (n,):
-        raise ValueError(f"{name} must be [{n}]")
-    return _here(t, name, dtype)
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise _not_here(t, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be [{shape[0]}] and contiguous")
+    return t.data_ptr()
 
 
 def spark_beam_select(logits: torch.Tensor, score: torch.Tensor, done, length, n_beams: int, eos: int,
@@ -876,12 +894,12 @@ def spark_beam_select(logits: torch.Tensor, score: torch.Tensor, done, length, n
     n, vocab = logits.shape
     if n_beams < 1 or n % n_beams:
         raise ValueError("logits must have a row for each beam of every group")
-    f32 = torch.float32
-    _check(load().spark_beam_select(lp, ld, dt, n // n_beams, int(n_beams), vocab, _slots(score, "score", n, f32),
-                                    _slots(done, "done", n), _slots(length, "length", n), int(eos),
-                                    _slots(new_score, "new_score", n, f32), _slots(token, "token", n),
-                                    _slots(parent, "parent", n), _slots(new_done, "new_done", n),
-                                    _slots(keep_len, "keep_len", n), _slots(new_len, "new_len", n),
+    f32, device, of = torch.float32, _current_device(), (n,)
+    _check(load().spark_beam_select(lp, ld, dt, n // n_beams, n_beams, vocab, _slots(score, "score", of, device, f32),
+                                    _slots(done, "done", of, device), _slots(length, "length", of, device), eos,
+                                    _slots(new_score, "new_score", of, device, f32), _slots(token, "token", of, device),
+                                    _slots(parent, "parent", of, device), _slots(new_done, "new_done", of, device),
+                                    _slots(keep_len, "keep_len", of, device), _slots(new_len, "new_len", of, device),
                                     _here(ws, "workspace"), ws.nbytes, _stream(stream)), "spark_beam_select")
 
 
@@ -900,7 +918,7 @@ class BeamState(_CachedC):
     _c: object = field(default=None, init=False, repr=False, compare=False)
 
     def _build_c(self) -> tuple:
-        """The C struct and (slots, device)."""
+        """The C struct's bytes and (slots, device)."""
         n, device = int(self.src.shape[0]), self.src.get_device()
         if self.src.shape != self.dst.shape or self.src.dim() < 1 + bool(self.positions):
             raise ValueError("src and dst must both be [slots, ...], with positions [slots, positions, ...]")
@@ -915,23 +933,22 @@ class BeamState(_CachedC):
             if t is not None and t.get_device() != device:
                 raise ValueError("src, dst and push must be on the same device")
         c = SparkBeamState(_dev_ptr(self.src, "src"), _dev_ptr(self.dst, "dst", self.src.dtype), pitch, elem, push)
-        return c, n, device
+        return bytes(c), (n, device)
 
 
 def spark_beam_reorder(parent: torch.Tensor, keep_len, new_len, states, ws: torch.Tensor, stream=None) -> None:
     """Rows of every BeamState to their new slots (spark_beam_select's parent,
     keep_len and new_len; the lengths may be None without ``positions``)."""
-    n = int(parent.shape[0])
-    built = [st.to_c() for st in states]
-    for st, (_, slots, device) in zip(states, built):
-        if slots != n:
-            raise ValueError("every state must have a row for each slot")
-        if device != _current_device():
+    of, device = parent.shape, _current_device()
+    built = [st._c or st.to_c() for st in states]
+    for st, b in zip(states, built):
+        if b[1] != (of[0], device):
+            if b[1][0] != of[0]:
+                raise ValueError("every state must have a row for each slot")
             raise _not_here(st.src, "a state")
-    _check(load().spark_beam_reorder(_slots(parent, "parent", n), _slots(keep_len, "keep_len", n),
-                                     _slots(new_len, "new_len", n), n,
-                                     (SparkBeamState * max(1, len(built)))(*[b[0] for b in built]), len(built),
-                                     _here(ws, "workspace"), ws.nbytes, _stream(stream)), "spark_beam_reorder")
+    _check(load().spark_beam_reorder(_slots(parent, "parent", of, device), _slots(keep_len, "keep_len", of, device),
+                                     _slots(new_len, "new_len", of, device), of[0], b"".join([b[0] for b in built]),
+                                     len(built), _here(ws, "workspace"), ws.nbytes, _stream(stream)), "spark_beam_reorder")
 
 
 def spark_attn_status_string(status: int) -> str:

@@ -5,11 +5,18 @@
 // maximum, its sum of exponentials and its best n_beams logits (score_parts.cuh):
 // within a row the offers are ordered as the logits are, so no other can be
 // chosen.  The last CTA of a group to arrive joins them: an offer's score is
-// (score - ln z) + (x - m) in 64 bits, and the order (score, then the
-// lower beam, then the lower token) of which no two offers are equal.  Lists are
-// sorted, so the n_beams best offers are in the n_beams lists of highest heads:
-// a floor that n_beams heads reach (a few reductions in a warp), the exact
-// ranks of the heads above it, then the ranks of at most n_beams^2 offers.
+// (score - ln z) + (x - m), and the order (score, then the lower beam, then the
+// lower token) of which no two offers are equal.  Lists are sorted, so the n_beams
+// best offers are in the n_beams lists of highest heads: a floor that n_beams
+// heads reach (a few reductions in a warp), the exact ranks of the heads above it,
+// then the ranks of at most n_beams^2 offers.
+//
+// Sums and scores are pairs of fp32 numbers (a number and what it leaves: 48
+// bits), so that the order of offers of different beams is not left to fp32, whose
+// steps at a score of -30 are 2e-6; an offer's pair is one 64-bit integer to
+// compare.  (fp64 runs at a 64th of fp32's rate here: one group of 4 beams took 30
+// us with the reorder when it joined in fp64, now 17.)  The one logarithm of each
+// row is fp64, a row a lane.
 #include <math.h>
 
 #include "beam.h"
@@ -26,28 +33,32 @@ using beam::Select;
 constexpr int kMaxBeams = SPARK_MAX_BEAMS;
 constexpr int kLists = beam::kMaxPairs;  // of a group at most
 
-struct Offers {
-  double value[kLists];
-  uint32_t id[kLists];     // beam * vocab + token
-  uint16_t list[kLists];
-  double base[kMaxBeams];  // score - ln z; -inf: the beam offers nothing
-  float top[kMaxBeams];    // m
-  int ended[kMaxBeams];
-  double t_value;          // the least head that counts
-  uint32_t t_id;
-  int count, n_lists;
-  uint16_t lists[kMaxBeams];
-  double best[kMaxBeams];
-  uint32_t best_id[kMaxBeams];
+// x + y, exactly where |x_lo|, |y_lo| are what their parts leave, to 2^-48
+struct Two {
+  float hi, lo;
 };
-static_assert(kLists >= kMaxBeams * kMaxBeams, "room for the offers of the lists that count");
-
-__device__ __forceinline__ bool above(double v, uint32_t i, double w, uint32_t j) { return v > w || (v == w && i < j); }
-
-__device__ __forceinline__ double warp_sum_double(double v) {
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+  return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
+}
+__device__ __forceinline__ Two add(Two x, Two y) {
+  const Two s = two_sum(x.hi, y.hi);
+  return Two{s.hi, __fadd_rn(s.lo, __fadd_rn(x.lo, y.lo))};
+}
+// so that hi is the sum rounded
+__device__ __forceinline__ Two settle(Two x) {
+  const float s = __fadd_rn(x.hi, x.lo);
+  return Two{s, __fsub_rn(x.lo, __fsub_rn(s, x.hi))};
+}
+__device__ __forceinline__ Two scaled(Two x, float f) {
+  const float p = __fmul_rn(x.hi, f);
+  return Two{p, __fmaf_rn(x.lo, f, __fmaf_rn(x.hi, f, -p))};
+}
+__device__ __forceinline__ Two warp_sum(Two x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = 16; o > 0; o >>= 1)
+    x = add(x, Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
+  return x;
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -55,8 +66,37 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// An offer: its score in the order of integers (a settled pair, the first
+// number's order above the second's), and beam * vocab + token.  Value 0: none.
+struct Offer {
+  unsigned long long value;
+  uint32_t id;
+};
+__device__ __forceinline__ unsigned long long value_key(Two v) {
+  return ((unsigned long long)order_of(v.hi) << 32) | order_of(v.lo);
+}
+__device__ __forceinline__ float offer_score(unsigned long long value) { return value_of((uint32_t)(value >> 32)); }
+__device__ __forceinline__ bool above(unsigned long long v, uint32_t i, unsigned long long w, uint32_t j) {
+  return v > w || (v == w && i < j);
+}
+
+struct Offers {
+  unsigned long long value[kLists];
+  uint32_t id[kLists];     // beam * vocab + token
+  uint16_t list[kLists];
+  Two base[kMaxBeams];     // score - ln z; hi -inf: the beam offers nothing
+  Two z[kMaxBeams];
+  float top[kMaxBeams];    // m
+  int ended[kMaxBeams];
+  int count, n_lists;
+  uint16_t lists[kMaxBeams];
+  unsigned long long best[kMaxBeams];
+  uint32_t best_id[kMaxBeams];
+};
+static_assert(kLists >= kMaxBeams * kMaxBeams, "room for the offers of the lists that count");
+
 // the rank of offer (v, i) among the n in sm, all different
-__device__ __forceinline__ int rank_of(const Offers& sm, int n, double v, uint32_t i) {
+__device__ __forceinline__ int rank_of(const Offers& sm, int n, unsigned long long v, uint32_t i) {
   int r = 0;
   for (int j = 0; j < n; ++j) r += above(sm.value[j], sm.id[j], v, i);
   return r;
@@ -69,42 +109,42 @@ __device__ __forceinline__ bool is_live(float score, int done) { return done == 
 __device__ __forceinline__ void join_group(const Select& a, int group, int k, int parts, Offers& sm, Smem& reach) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.n_beams, slot0 = group * W;
-  // the rows' bases: a warp each in turn
+  // the rows' sums, a warp each in turn
   for (int b = warp; b < W; b += kWarps) {
     const float score = __ldcg(a.score + slot0 + b);
     const int done = a.done ? __ldcg(a.done + slot0 + b) : 0;
     const bool live = is_live(score, done);
-    double base = -INFINITY;
     float top = -INFINITY;
+    Two z = {0.f, 0.f};
+    bool bad = false;
     if (live) {
-      float m[beam::kMaxParts / 32];
-      double z[beam::kMaxParts / 32];
-      bool bad = false;
+      constexpr int kEach = beam::kMaxParts / 32;
+      float m[kEach];
+      Two part[kEach];
 #pragma unroll
-      for (int i = 0; i < beam::kMaxParts / 32; ++i) {
+      for (int i = 0; i < kEach; ++i) {
         const int c = lane + 32 * i;
         m[i] = -INFINITY;
-        z[i] = 0.0;
+        part[i] = Two{0.f, 0.f};
         if (c < parts) {
-          const Part* q = a.part + (int64_t)(slot0 + b) * parts + c;
-          m[i] = __ldcg(&q->m);
-          z[i] = __ldcg(&q->z);
-          bad = bad || __ldcg(&q->bad) != 0;
+          const float4 q = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)(slot0 + b) * parts + c));
+          m[i] = q.x;
+          bad = bad || __float_as_int(q.y) != 0;
+          part[i] = Two{q.z, q.w};
         }
         top = fmaxf(top, m[i]);
       }
       top = warp_max(top);
-      double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < beam::kMaxParts / 32; ++i)
-        if (m[i] > -INFINITY) sum += z[i] * exp((double)(m[i] - top));
-      sum = warp_sum_double(sum);
-      if (!__any_sync(0xffffffffu, bad) && top > -INFINITY) base = (double)score - log(sum);
-    } else if (done != 0 && fabsf(score) < INFINITY) {
-      base = (double)score;
+      for (int i = 0; i < kEach; ++i)
+        if (m[i] > -INFINITY) z = add(z, scaled(part[i], expf(m[i] - top)));
+      z = warp_sum(z);
+      bad = __any_sync(0xffffffffu, bad);
     }
     if (lane == 0) {
-      sm.base[b] = base;
+      const bool any = live ? !bad && top > -INFINITY : done != 0 && fabsf(score) < INFINITY;
+      sm.base[b] = Two{any ? score : -INFINITY, 0.f};
+      sm.z[b] = z;
       sm.top[b] = top;
       sm.ended[b] = done != 0;
     }
@@ -112,42 +152,39 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
   if (tid == 0) {
     sm.count = 0;
     sm.n_lists = 0;
-    sm.t_value = -INFINITY;
-    sm.t_id = 0xFFFFFFFFu;
+  }
+  __syncthreads();
+  if (tid < W && sm.base[tid].hi > -INFINITY && !sm.ended[tid]) {
+    const double base = (double)sm.base[tid].hi - log((double)sm.z[tid].hi + (double)sm.z[tid].lo);
+    const float hi = (float)base;
+    sm.base[tid] = Two{hi, (float)(base - (double)hi)};
   }
   __syncthreads();
   // list l: part l % parts of beam l / parts; an ended beam has one, of one offer
   const int lists = W * parts;
-  auto entry = [&](int l, int i, double& v, uint32_t& id) {
+  auto entry = [&](int l, int i) {
     const int b = l / parts, c = l - b * parts;
-    const double base = sm.base[b];
-    v = -INFINITY;
-    id = 0xFFFFFFFFu;
-    if (!(base > -INFINITY)) return;
+    const Two base = sm.base[b];
+    if (!(base.hi > -INFINITY)) return Offer{0, 0};
     if (sm.ended[b]) {
-      if (c == 0 && i == 0) {
-        v = base;
-        id = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)a.eos;
-      }
-      return;
+      if (c != 0 || i != 0) return Offer{0, 0};
+      return Offer{value_key(base), (uint32_t)b * (uint32_t)a.vocab + (uint32_t)a.eos};
     }
     const Key key = __ldcg(&a.part[(int64_t)(slot0 + b) * parts + c].key[i]);
-    if (key == 0) return;
-    // (x - m first: logits may be far larger than the scores; -inf: no offer)
-    v = base + ((double)key_value(key) - (double)sm.top[b]);
-    id = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)key_index(key);
+    const float x = key_value(key);
+    if (key == 0 || !(x > -INFINITY)) return Offer{0, 0};
+    // (x - m first: logits may be far larger than the scores)
+    const Two v = settle(add(settle(two_sum(x, -sm.top[b])), base));
+    return Offer{value_key(v), (uint32_t)b * (uint32_t)a.vocab + (uint32_t)key_index(key)};
   };
   constexpr int kHeads = kLists / kThreads;
-  double v[kHeads];
-  uint32_t id[kHeads];
+  Offer head[kHeads];
   float mine = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
     const int l = tid + i * kThreads;
-    v[i] = -INFINITY;
-    id[i] = 0xFFFFFFFFu;
-    if (l < lists) entry(l, 0, v[i], id[i]);
-    mine = fmaxf(mine, (float)v[i]);
+    head[i] = l < lists ? entry(l, 0) : Offer{0, 0};
+    if (head[i].value != 0) mine = fmaxf(mine, offer_score(head[i].value));
   }
   // a floor that W heads reach, in fp32 (rounding keeps the order)
   const uint32_t o = warp_kth(mine, (W + kWarps - 1) / kWarps, lane);
@@ -156,10 +193,10 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
   const float floor = floor_now(reach, lane);
 #pragma unroll
   for (int i = 0; i < kHeads; ++i)
-    if (v[i] > -INFINITY && !((float)v[i] < floor)) {
+    if (head[i].value != 0 && !(offer_score(head[i].value) < floor)) {
       const int at = atomicAdd(&sm.count, 1);
-      sm.value[at] = v[i];
-      sm.id[at] = id[i];
+      sm.value[at] = head[i].value;
+      sm.id[at] = head[i].id;
       sm.list[at] = (uint16_t)(tid + i * kThreads);
     }
   __syncthreads();
@@ -172,19 +209,17 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
   if (tid == 0) sm.count = 0;
   __syncthreads();
   for (int e = tid; e < n_lists * k; e += kThreads) {
-    double x;
-    uint32_t xi;
-    entry(sm.lists[e / k], e % k, x, xi);
-    if (x > -INFINITY) {
+    const Offer x = entry(sm.lists[e / k], e % k);
+    if (x.value != 0) {
       const int at = atomicAdd(&sm.count, 1);
-      sm.value[at] = x;
-      sm.id[at] = xi;
+      sm.value[at] = x.value;
+      sm.id[at] = x.id;
     }
   }
   __syncthreads();
   const int n = sm.count;
   for (int e = tid; e < n; e += kThreads) {
-    const double x = sm.value[e];
+    const unsigned long long x = sm.value[e];
     const uint32_t xi = sm.id[e];
     const int r = rank_of(sm, n, x, xi);
     if (r < W) {
@@ -200,7 +235,7 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
     const int b = (int)(sm.best_id[tid] / (uint32_t)a.vocab);
     token = (int)(sm.best_id[tid] - (uint32_t)b * (uint32_t)a.vocab);
     parent = slot0 + b;
-    score = (float)sm.best[tid];
+    score = offer_score(sm.best[tid]);
     const bool was = sm.ended[b] != 0;
     done = was || token == a.eos;
     if (a.length) {
@@ -238,26 +273,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(const __grid_consta
     top.reset();
     const Stat st = row_pass<T, false>(static_cast<const T*>(a.logits) + row * a.ld, a.vocab, k, share, c, parts, sm, top);
     join_tops(sm, top, k);
-    // the block's sum in 64 bits: scores of different beams are compared
     const float wm = warp_max(st.m);
-    const double wz = warp_sum_double(st.m > -INFINITY ? (double)st.z * (double)expf(st.m - wm) : 0.0);
+    const Two wz = warp_sum(scaled(Two{st.z, 0.f}, st.m > -INFINITY ? expf(st.m - wm) : 0.f));
     const bool wbad = __any_sync(0xffffffffu, st.bad != 0);
-    if (lane == 0) {
-      sm.stat[warp].m = wm;
-      sm.stat[warp].bad = wbad;
-      offers.value[warp] = wz;
-    }
+    if (lane == 0) sm.stat[warp] = Stat{wm, wz.hi, wz.lo, wbad};
     __syncthreads();
     Part* mine = a.part + (int64_t)row * parts + c;
     if (warp == 0) {
-      const float m = lane < kWarps ? sm.stat[lane].m : -INFINITY, bm = warp_max(m);
-      const double z = warp_sum_double(m > -INFINITY ? offers.value[lane] * exp((double)(m - bm)) : 0.0);
-      const bool bad = __any_sync(0xffffffffu, lane < kWarps && sm.stat[lane].bad != 0);
-      if (lane == 0) {
-        mine->m = bm;
-        mine->bad = bad;
-        mine->z = z;
-      }
+      const Stat w = lane < kWarps ? sm.stat[lane] : Stat{-INFINITY, 0.f, 0.f, 0};
+      const float m = warp_max(w.m);
+      const Two z = warp_sum(scaled(Two{w.z, w.u}, w.m > -INFINITY ? expf(w.m - m) : 0.f));
+      const bool bad = __any_sync(0xffffffffu, w.bad != 0);
+      if (lane == 0) *reinterpret_cast<float4*>(mine) = make_float4(m, __int_as_float(bad), z.hi, z.lo);
     }
     if (tid < k) mine->key[tid] = tid < sm.count ? sm.best[tid] : 0;
     __threadfence();

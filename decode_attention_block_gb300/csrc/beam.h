@@ -19,7 +19,7 @@ constexpr int kWantedCtas = 512;
 struct alignas(16) Part {
   float m;
   int bad;   // a NaN or +inf among its logits
-  double z;  // sum of e^(x - m)
+  float z, z_rest;  // sum of e^(x - m), as a number and what it leaves
   unsigned long long key[SPARK_MAX_BEAMS];
 };
 

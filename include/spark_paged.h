@@ -120,8 +120,8 @@ int spark_rope_table(const spark_geom* g, int32_t layer_class, int32_t n_positio
 
 /* spark_paged_append of new tokens whose queries and keys are not rotated
  * yet: NeoX rope on the way (the class's rotary dim r, pairs i and i + r / 2,
- * the dims behind r as they are), each result of the rotation rounded once to
- * fp32 and once to its type.
+ * the dims behind r as they are), in fp32 within 1.5 ulp, rounded once to its
+ * type; the codes of 4-bit pages are those of the exact rotation rounded to fp32.
  *   q       rows [n_q * head_dim] of element type `dtype`, row t at element
  *           t * ld; null: no queries.
  *   k, v    rows [n_kv * head_dim], likewise at t * ld (three slices of a
