@@ -9,7 +9,7 @@
 // lower token) of which no two offers are equal.  Lists are sorted, so the n_beams
 // best offers are in the n_beams lists of highest heads: a floor that n_beams
 // heads reach (a few reductions in a warp), the exact ranks of the heads above it,
-// then the ranks of at most n_beams^2 offers.
+// then the ranks of their offers that reach the last of these n_beams.
 //
 // Sums and scores are pairs of fp32 numbers (a number and what it leaves: 48
 // bits), so that the order of offers of different beams is not left to fp32, whose
@@ -89,6 +89,8 @@ struct Offers {
   float top[kMaxBeams];    // m
   int ended[kMaxBeams];
   int count, n_lists;
+  unsigned long long least;  // the head that n_beams - 1 others are above, if there are as many
+  uint32_t least_id;
   uint16_t lists[kMaxBeams];
   unsigned long long best[kMaxBeams];
   uint32_t best_id[kMaxBeams];
@@ -109,6 +111,14 @@ __device__ __forceinline__ bool is_live(float score, int done) { return done == 
 __device__ __forceinline__ void join_group(const Select& a, int group, int k, int parts, Offers& sm, Smem& reach) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.n_beams, slot0 = group * W;
+  // the lists' heads, asked for while the rows' sums are joined: list l is part l %
+  // parts of beam l / parts; an ended beam has one, of one offer
+  const int lists = W * parts;
+  constexpr int kHeads = kLists / kThreads;
+  auto key_of = [&](int l, int i) { return __ldcg(&a.part[(int64_t)slot0 * parts + l].key[i]); };
+  Key first[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) first[i] = tid + i * kThreads < lists ? key_of(tid + i * kThreads, 0) : 0;
   // the rows' sums, a warp each in turn
   for (int b = warp; b < W; b += kWarps) {
     const float score = __ldcg(a.score + slot0 + b);
@@ -152,6 +162,8 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
   if (tid == 0) {
     sm.count = 0;
     sm.n_lists = 0;
+    sm.least = 0;
+    sm.least_id = 0xFFFFFFFFu;
   }
   __syncthreads();
   if (tid < W && sm.base[tid].hi > -INFINITY && !sm.ended[tid]) {
@@ -160,9 +172,8 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
     sm.base[tid] = Two{hi, (float)(base - (double)hi)};
   }
   __syncthreads();
-  // list l: part l % parts of beam l / parts; an ended beam has one, of one offer
-  const int lists = W * parts;
-  auto entry = [&](int l, int i) {
+  // offer i of list l, whose key it is (a beam that offers none left stale ones)
+  auto entry = [&](int l, int i, Key key) {
     const int b = l / parts, c = l - b * parts;
     const Two base = sm.base[b];
     if (!(base.hi > -INFINITY)) return Offer{0, 0};
@@ -170,20 +181,18 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
       if (c != 0 || i != 0) return Offer{0, 0};
       return Offer{value_key(base), (uint32_t)b * (uint32_t)a.vocab + (uint32_t)a.eos};
     }
-    const Key key = __ldcg(&a.part[(int64_t)(slot0 + b) * parts + c].key[i]);
     const float x = key_value(key);
     if (key == 0 || !(x > -INFINITY)) return Offer{0, 0};
     // (x - m first: logits may be far larger than the scores)
     const Two v = settle(add(settle(two_sum(x, -sm.top[b])), base));
     return Offer{value_key(v), (uint32_t)b * (uint32_t)a.vocab + (uint32_t)key_index(key)};
   };
-  constexpr int kHeads = kLists / kThreads;
   Offer head[kHeads];
   float mine = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
     const int l = tid + i * kThreads;
-    head[i] = l < lists ? entry(l, 0) : Offer{0, 0};
+    head[i] = l < lists ? entry(l, 0, first[i]) : Offer{0, 0};
     if (head[i].value != 0) mine = fmaxf(mine, offer_score(head[i].value));
   }
   // a floor that W heads reach, in fp32 (rounding keeps the order)
@@ -201,16 +210,23 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
     }
   __syncthreads();
   const int heads = sm.count;
-  for (int e = tid; e < heads; e += kThreads)
-    if (rank_of(sm, heads, sm.value[e], sm.id[e]) < W) sm.lists[atomicAdd(&sm.n_lists, 1)] = sm.list[e];
+  for (int e = tid; e < heads; e += kThreads) {
+    const int r = rank_of(sm, heads, sm.value[e], sm.id[e]);
+    if (r < W) sm.lists[atomicAdd(&sm.n_lists, 1)] = sm.list[e];
+    if (r == W - 1) {
+      sm.least = sm.value[e];
+      sm.least_id = sm.id[e];
+    }
+  }
   __syncthreads();
-  // the offers of these lists
+  // the offers of these lists that are not below all n_beams heads
   const int n_lists = sm.n_lists;
   if (tid == 0) sm.count = 0;
   __syncthreads();
   for (int e = tid; e < n_lists * k; e += kThreads) {
-    const Offer x = entry(sm.lists[e / k], e % k);
-    if (x.value != 0) {
+    const int l = sm.lists[e / k], i = e % k;
+    const Offer x = entry(l, i, key_of(l, i));
+    if (x.value != 0 && !above(sm.least, sm.least_id, x.value, x.id)) {
       const int at = atomicAdd(&sm.count, 1);
       sm.value[at] = x.value;
       sm.id[at] = x.id;

@@ -12,7 +12,11 @@ namespace beam {
 
 constexpr int kMaxParts = 64;      // parts a row is split into at most
 constexpr int kMaxPairs = 1024;    // (row, part) pairs of a call at most
-constexpr int kPartElems = 4096;   // elements of a part at least: one tile
+constexpr int kPartElems = 8192;   // elements of a part at least: two tiles
+// Parts for CTAs as far as they run at once (four an SM).  us on the GPU, fp32 rows
+// of 131072, parts of 4096 elements at least and of 8192: one group of 4 beams 13.9
+// and 12.7, four 15.8 and 13.7; up to 512 CTAs and up to 300: 16 groups of 4 beams
+// 19.1 and 17.5, 32 of 8 35 and 36.5, 8 of 32 (whole rows then, long lists) 51 and 99.
 constexpr int kWantedCtas = 512;
 
 // what one part of a row leaves for the join of its group
