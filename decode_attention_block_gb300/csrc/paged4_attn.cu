@@ -553,6 +553,9 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
 }  // namespace
 
 cudaError_t launch_paged4_attention(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st) {
+#ifdef FORCE_PAIR
+  if (p.max_q > 1) return launch_paged4_pair(p, qdtype, k, v, st);
+#endif
   if (p.max_q > paged::kChunkTokens && (2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q || p.n_tokens > 128 * p.n_seqs))
     return launch_paged4_pair(p, qdtype, k, v, st);
   if (p.max_q > 1) return launch_paged4_chunk(p, qdtype, k, v, st);

@@ -7,7 +7,7 @@
 // scaled row by row by a power of two (fp32 ones as two fp16 halves), and
 // probabilities are fp16 (fp32 queries: two halves).  Warp 0 loads the queries,
 // which warps 4-7 (softmax) convert, warp 1 issues the MMAs, warps 8-15 fill
-// the ring: warp 8 + w the positions 16 w .. 16 w + 15 of each tile, one block.
+// the ring, warp 8 + w half w % 2 of the dims of positions 32 (w / 2) .. + 31.
 // Rows of V that no token of the group sees are stored as zeros.
 #include "paged4_chunk_parts.cuh"
 
@@ -97,58 +97,68 @@ __global__ void __launch_bounds__(kThreads4, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp >= kFirstDequant) {
-    // ---- K(0), then K(i), V(i - 1) for the tiles of each group, a half of the dims a slot
+    // ---- K(0), then K(i), V(i - 1) for the tiles of each group, a half of the dims
+    // a slot: warp 8 + w positions 16 w .. 16 w + 15, one block
     fewer_registers<kRegsDequant>();
     const int w = warp - kFirstDequant;
-    uint32_t k = 0;
+    int s0 = 0;           // the next slot, and the one behind it
+    uint32_t turn = 1;    // parity to wait for in s0: the first time round it is free
     bool ok = true;
-    const Lanes in_k(pk, lane), in_v(pv, lane);
-    uint32_t places[4];
-    part_places(places, lane);
+    const RowLanes in_k(pk, lane), in_v(pv, lane);
     // the lane's line in a slot
-    unsigned char* line = base + S::kRing + (2 * w) * kGroupBytes<2> + (lane >> 4) * kAtom;
-    // both halves of the dims, a slot each
-    auto store = [&](const Part (&x)[2]) {
+    const uint32_t line = smem_u32(base + S::kRing) + 2 * w * kGroupBytes<2> + in_k.line * kAtom;
+    auto store = [&](const RowPart (&x)[4]) {
+      const int s1 = s0 + 1 < NS ? s0 + 1 : 0;
+      const uint32_t turn1 = s0 + 1 < NS ? turn : turn ^ 1u;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&empty[s0], turn, flags, kWaitLimitNs) &&
+                                       mbar_wait_bounded(&empty[s1], turn1, flags, kWaitLimitNs));
+      if (!ok) return;
+      const uint32_t to = line + (in_k.h ? s1 : s0) * kSlot;
 #pragma unroll
-      for (int h = 0; h < 2; ++h, ++k) {
-        const int s = (int)(k % NS);
-        const uint32_t r = k / NS;
-        if (ok && r > 0 && !mbar_wait_bounded(&empty[s], (r - 1) & 1, flags, kWaitLimitNs)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        store_part(line + s * kSlot, places, kGroupBytes<2>, x[h]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-      }
+      for (int u = 0; u < 4; ++u) store_rows(to + ((u & 1) ? in_k.at1 : in_k.at0) + (u >> 1) * kGroupBytes<2>, x[u]);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it through the async proxy
+      __syncwarp();
+      if (lane < 2) mbar_arrive(&full[lane ? s1 : s0]);
+      s0 = s1 + 1 < NS ? s1 + 1 : 0;
+      turn = s1 + 1 < NS ? turn1 : turn1 ^ 1u;
+    };
+    auto load = [&](RowPart (&x)[4], const RowLanes& l, uint32_t at) {
+      load_rows<0>(x[0], l, at);
+      load_rows<1>(x[1], l, at);
+      load_rows<2>(x[2], l, at);
+      load_rows<3>(x[3], l, at);
     };
     for (;;) {
       const int64_t t0 = cur.begin > u0 ? cur.begin : u0, t1 = cur.end < u1 ? cur.end : u1;
       const int n = (int)(t1 - t0);
       int x = (cur.g.tile0 + (int)(t0 - cur.begin)) * kPos + 16 * w;
       const int end = x + n * kPos;  // behind the share's tiles
-      Blocks blocks;
+      Blocks<1> blocks;
       blocks.find(p, cur, x, end, lane);
-      Part kp[2], vp[2];
+      RowPart kp[4], vp[4];
       uint32_t at = blocks.of(0);
-      in_k.load(kp, at);
+      load(kp, in_k, at);
       for (int i = 0; i <= n && ok; ++i, x += kPos) {
-        if (i < n) store(kp);
         const uint32_t at_v = at;
         if (i < n) {
-          if (((i + 1) & 31) == 0) blocks.find(p, cur, x + kPos, end, lane);
+          store(kp);
+          if ((i + 1) % Blocks<1>::kTiles == 0) blocks.find(p, cur, x + kPos, end, lane);
           at = blocks.of(i + 1);
-          in_k.load(kp, at);
+          load(kp, in_k, at);
         }
         if (i > 0 && ok) {
           // rows that no token of the group sees: their P is 0, but they may hold anything
-          const int row = x - kPos + (lane & 7);
+          if (x - kPos < cur.g.lo || x - kPos + 15 > cur.g.hi) {
+            const int r0 = x - kPos + ((lane & 3) < 2 ? lane & 3 : (lane & 3) + 4), r1 = x - kPos + (lane & 3) + 2;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (row + 8 * e < cur.g.lo || row + 8 * e > cur.g.hi) vp[0].scale[e] = vp[1].scale[e] = 0u;
+            for (int u = 0; u < 4; ++u) {
+              const int row = ((u & 1) ? r1 : r0) + 8 * (u >> 1);
+              if (row < cur.g.lo || row > cur.g.hi) vp[u].scale = 0u;
+            }
+          }
           store(vp);
         }
-        if (i < n) in_v.load(vp, at_v);
+        if (i < n) load(vp, in_v, at_v);
       }
       if (!ok || !cur.advance(p, sh, u1)) break;
     }

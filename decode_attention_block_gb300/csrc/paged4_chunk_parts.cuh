@@ -2,7 +2,7 @@
 // share (paged4_chunk.cu: one CTA and 32 tokens a group; paged4_pair.cu: two
 // CTAs and 64): blocks of pages into fp16 operands in shared memory.
 //
-// A warp takes 16 positions, one block: plain loads of codes and scales into registers, a
+// A warp takes half of the dims of a block or two: plain loads of codes and scales into registers, a
 // tile ahead of their use (a block's parts are contiguous, so nothing is gained
 // by a copy engine, and no shared memory is spent on bytes that are read once),
 // then conversion and 16-byte stores in the layout of paged_chunk_parts.cuh.
@@ -68,55 +68,39 @@ struct Lanes {
     for (int i = 0; i < 2; ++i)
       x.scale[i] = __ldcg(reinterpret_cast<const unsigned short*>(y + at + 8 * h + 8 * i * fp4::kScales));
   }
-  // both halves' parts
-  __device__ __forceinline__ void load(Part (&x)[2], uint32_t block) const {
-    if (block == kNone) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          x[h].code[i] = make_uint4(0u, 0u, 0u, 0u);
-          x[h].scale[i] = 0u;
-        }
-      return;
-    }
-    const uint64_t at = (uint64_t)block * (uint64_t)fp4::kBlock;
-    const unsigned char *a = x0 + at, *b = x1 + at, *s = y + at;
-    x[0].code[0] = __ldcg(reinterpret_cast<const uint4*>(a));
-    x[0].code[1] = __ldcg(reinterpret_cast<const uint4*>(b + 8 * fp4::kCodes));
-    x[1].code[0] = __ldcg(reinterpret_cast<const uint4*>(b));
-    x[1].code[1] = __ldcg(reinterpret_cast<const uint4*>(a + 8 * fp4::kCodes));
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        x[h].scale[i] = __ldcg(reinterpret_cast<const unsigned short*>(s + 8 * h + 8 * i * fp4::kScales));
-  }
 };
 
-// The blocks of a warp's positions x, x + 128 .. of a group's tiles, found for 32
-// tiles at a time, one per lane.
+// The blocks of a warp's positions in a group's tiles, N neighbours a tile, found
+// for 32 / N tiles at a time, one per lane.
+template <int N>
 struct Blocks {
+  static constexpr int kTiles = 32 / N;
   uint32_t mine;
-  // those of the tiles at x + 128 lane, before `end`
+  // those at x and the N - 1 behind it in the tile there and the ones 128 and so
+  // on further, before `end`
   __device__ __forceinline__ void find(const Args& p, const Cursor& cur, int x, int end, int lane) {
-    x += lane * kPos;
+    x += lane / N * kPos;
     mine = Lanes::kNone;
-    if (x < end && x <= cur.g.hi && x + fp4::kRows > cur.g.lo) {
-      const int col = paged::page_col(p, x), in_page = (x - col * p.page_size) / fp4::kRows;
-      const int page = paged::page_of(p, paged::page_entry(p, cur.s, col));
-      // (pages * page_size < 2^31: the blocks of all heads are below 2^30)
-      mine = ((uint32_t)page * (uint32_t)(p.page_size / fp4::kRows) + (uint32_t)in_page) * (uint32_t)p.n_kv + (uint32_t)cur.j;
+    if (x < end) {
+      x += lane % N * fp4::kRows;
+      if (x <= cur.g.hi && x + fp4::kRows > cur.g.lo) {
+        const int col = paged::page_col(p, x), in_page = (x - col * p.page_size) / fp4::kRows;
+        const int page = paged::page_of(p, paged::page_entry(p, cur.s, col));
+        // (pages * page_size < 2^31: the blocks of all heads are below 2^30)
+        mine = ((uint32_t)page * (uint32_t)(p.page_size / fp4::kRows) + (uint32_t)in_page) * (uint32_t)p.n_kv + (uint32_t)cur.j;
+      }
     }
   }
-  __device__ __forceinline__ uint32_t of(int tile) const { return __shfl_sync(0xffffffffu, mine, tile & 31); }
+  __device__ __forceinline__ uint32_t of(int tile, int b = 0) const {
+    return __shfl_sync(0xffffffffu, mine, tile % kTiles * N + b);
+  }
 };
 
 // The part's 32 dims of each row as fp16: with c = lane / 8, line c / 2 of 64
 // dims, four 16-byte chunks of a row of 128 bytes, chunk 4 (c % 2) + e of row r at
 // (4 (c % 2) + e) ^ (r % 8): the lane's places are at[e] in the line; the second
 // row lies `group` bytes behind.
-__device__ __forceinline__ void store_part(unsigned char* line, const uint32_t (&at)[4], uint32_t group, const Part& x) {
+__device__ __forceinline__ void store_part(uint32_t line, const uint32_t (&at)[4], uint32_t group, const Part& x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t w[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
@@ -127,10 +111,67 @@ __device__ __forceinline__ void store_part(unsigned char* line, const uint32_t (
       fp4::halves8(w[k], h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = fp4::mul2(h[j], f[k >> 1]);
-      *reinterpret_cast<uint4*>(line + at[k] + i * group) = make_uint4(h[0], h[1], h[2], h[3]);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + at[k] + i * group), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
     }
   }
 }
+// Whole rows of a block by a warp: chunk c = lane / 8 ^ 5 (lane / 4 % 2) of four
+// rows of each of the block's row groups u < 4, rows 0 1 6 7, 2 3 4 5, then 8
+// further.  A group's codes are four lines of 128 bytes, read whole (half lines of
+// eight rows cost a load twice the passes of the memory pipe, which these kernels
+// are bound by), and eight lanes store 16 bytes each in different banks: their four
+// rows and two chunks of either parity differ in (4 (c % 2)) ^ (r % 8).
+struct RowLanes {
+  const unsigned char *x0, *x1, *y0, *y1;  // codes and scales of groups 0 and 1
+  int d0, d1;         // codes from group 0 to 2, from 1 to 3
+  uint32_t at0, at1;  // places in the line, of rows of groups 0 and 1, of the chunk's first 16 bytes (the k-th: ^ 16 k)
+  int h, line;        // half of the dims, line of it
+  __device__ __forceinline__ RowLanes(const unsigned char* pool, int lane) {
+    const int s = lane & 3, c = (lane >> 3) ^ ((lane & 4) ? 5 : 0), r0 = s < 2 ? s : s + 4, r1 = s + 2;
+    const uint32_t a0 = (uint32_t)(r0 * fp4::kCodes + ((c ^ fp4::turn(r0)) << 4)), a1 = (uint32_t)(r1 * fp4::kCodes + ((c ^ fp4::turn(r1)) << 4));
+    x0 = pool + a0;
+    x1 = pool + a1;
+    y0 = pool + fp4::scale_at(r0, 32 * c);
+    y1 = pool + fp4::scale_at(r1, 32 * c);
+    d0 = (int)((a0 ^ 64u) - a0) + 8 * fp4::kCodes;
+    d1 = (int)((a1 ^ 64u) - a1) + 8 * fp4::kCodes;
+    at0 = (uint32_t)(r0 * 128 + (((c & 1) * 4 ^ r0) << 4));
+    at1 = (uint32_t)(r1 * 128 + (((c & 1) * 4 ^ r1) << 4));
+    h = c >> 2;
+    line = (c >> 1) & 1;
+  }
+};
+struct RowPart {
+  uint4 code;
+  uint32_t scale;
+};
+template <int U>
+__device__ __forceinline__ void load_rows(RowPart& x, const RowLanes& l, uint32_t block) {
+  if (block == Lanes::kNone) {
+    x.code = make_uint4(0u, 0u, 0u, 0u);
+    x.scale = 0u;
+    return;
+  }
+  const uint64_t at = (uint64_t)block * (uint64_t)fp4::kBlock;
+  x.code = __ldcg(reinterpret_cast<const uint4*>(((U & 1) ? l.x1 : l.x0) + at + (U < 2 ? 0 : (U & 1) ? l.d1 : l.d0)));
+  x.scale = __ldcg(reinterpret_cast<const unsigned short*>(((U & 1) ? l.y1 : l.y0) + at + (U < 2 ? 0 : 8 * fp4::kScales)));
+}
+// to: the lane's place of the row's first 16 bytes
+__device__ __forceinline__ void store_rows(uint32_t to, const RowPart& x) {
+  const uint32_t w[4] = {x.code.x, x.code.y, x.code.z, x.code.w};
+  const uint32_t f[2] = {__byte_perm(x.scale, 0u, 0x4040u) << 7, __byte_perm(x.scale, 0u, 0x4141u) << 7};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t h[4];
+    fp4::halves8(w[k], h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = fp4::mul2(h[j], f[k >> 1]);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to ^ (uint32_t)(16 * k)), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                 : "memory");
+  }
+}
+
 // the lane's places
 __device__ __forceinline__ void part_places(uint32_t (&at)[4], int lane) {
 #pragma unroll

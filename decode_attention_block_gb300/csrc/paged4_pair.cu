@@ -113,18 +113,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
 
   if (warp >= kFirstDequant) {
     // ---- K(0), then K(i), V(i - 1) for the tiles of each group.  Of K warp 8 + w
-    // takes half w % 2 of the dims of block w / 2 of this CTA's four, of V this
+    // takes half w % 2 of the rows of block w / 2 of this CTA's four, of V this
     // CTA's half of the dims of block w.
     fewer_registers<kRegsDequant>();
-    const int w = warp - kFirstDequant, h_k = w & 1;
+    const int w = warp - kFirstDequant;
     uint32_t kk = 0, kv = 0;
     bool ok = true;
-    const Lanes in_k(pk, lane), in_v(pv, lane);
+    RowLanes in_k(pk, lane);
+    if (w & 1) {
+      in_k.x0 += in_k.d0;
+      in_k.x1 += in_k.d1;
+      in_k.y0 += 8 * fp4::kScales;
+      in_k.y1 += 8 * fp4::kScales;
+    }
+    const Lanes in_v(pv, lane);
     uint32_t places[4];
     part_places(places, lane);
     // the lane's line in a slot
-    unsigned char* line_k = base + S::kRingK + (w & ~1) * kGroupBytes<4> + (2 * h_k + (lane >> 4)) * kAtom;
-    unsigned char* line_v = base + S::kRingV + 2 * w * kGroupBytes<2> + (lane >> 4) * kAtom;
+    const uint32_t line_k = smem_u32(base + S::kRingK) + w * kGroupBytes<4> + (2 * in_k.h + in_k.line) * kAtom;
+    const uint32_t line_v = smem_u32(base + S::kRingV) + 2 * w * kGroupBytes<2> + (lane >> 4) * kAtom;
     auto freed = [&](uint64_t* bar, uint32_t use) {
       if (ok && use > 0 && !mbar_wait_bounded(bar, (use - 1) & 1, flags, kWaitLimitNs)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
@@ -141,20 +148,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       const int x0 = (cur.g.tile0 + (int)(t0 - cur.begin)) * kPos;
       int xk = x0 + 64 * rank + 16 * (w >> 1), xv = x0 + 16 * w;
       const int end_k = xk + n * kPos, end_v = xv + n * kPos;  // behind the share's tiles
-      Blocks blocks_k, blocks_v;
+      Blocks<1> blocks_k, blocks_v;
       blocks_k.find(p, cur, xk, end_k, lane);
       blocks_v.find(p, cur, xv, end_v, lane);
-      Part kp, vp;
-      in_k.load(kp, blocks_k.of(0), h_k);
+      RowPart kp[2];
+      Part vp;
+      auto load_k = [&](uint32_t block) {
+        load_rows<0>(kp[0], in_k, block);
+        load_rows<1>(kp[1], in_k, block);
+      };
+      load_k(blocks_k.of(0));
       for (int i = 0; i <= n && ok; ++i, xk += kPos, xv += kPos) {
         if (i < n) {
           const int s = (int)(kk % S::kK);
           if (!freed(&k_empty[s], kk / S::kK)) break;
-          store_part(line_k + s * kSlot, places, kGroupBytes<4>, kp);
+          store_rows(line_k + s * kSlot + in_k.at0, kp[0]);
+          store_rows(line_k + s * kSlot + in_k.at1, kp[1]);
           report(&k_here[s]);
           ++kk;
           if (((i + 1) & 31) == 0) blocks_k.find(p, cur, xk + kPos, end_k, lane);
-          in_k.load(kp, blocks_k.of(i + 1), h_k);
+          load_k(blocks_k.of(i + 1));
         }
         if (i > 0) {
           // rows that no token of the group sees: their P is 0, but they may hold anything
