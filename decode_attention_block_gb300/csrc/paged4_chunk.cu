@@ -9,6 +9,15 @@
 // which warps 4-7 (softmax) convert, warp 1 issues the MMAs, warps 8-15 fill
 // the ring, warp 8 + w half w % 2 of the dims of positions 32 (w / 2) .. + 31.
 // Rows of V that no token of the group sees are stored as zeros.
+//
+// Bound by shared memory: a tile's operands are written (128 KB) and read by the
+// MMAs (192 KB; 384 with fp32 queries), 2560 cycles at 128 bytes a cycle against
+// 2048 of MMA, and the codes' loads go through the same pipe.  32 sequences at
+// 4096-8192 (0.23 GB), bf16 queries: 4 tokens each 96 us, 32 tokens 110 (bf16 pages,
+// 0.82 GB: 132 and 147); fp32 queries 137; a mixed batch of 32, 4 of them with
+// chunks of ~400 tokens, 131 and 182.  What it cost on the way (4 tokens each): half
+// lines of codes a load 113, scores kept in 240 registers a thread, the MMA warp
+// spilling, 102.
 #include "paged4_chunk_parts.cuh"
 
 namespace spark {
@@ -40,6 +49,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
   constexpr bool kSplit = std::is_same<QT, float>::value;
   using S = Chunk4Smem<kSplit>;
   constexpr int NS = S::kSlots;
+  using R = Regs<120, 152, 120>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -99,7 +109,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
   if (warp >= kFirstDequant) {
     // ---- K(0), then K(i), V(i - 1) for the tiles of each group, a half of the dims
     // a slot: warp 8 + w positions 16 w .. 16 w + 15, one block
-    fewer_registers<kRegsDequant>();
+    fewer_registers<R::kDequant>();
     const int w = warp - kFirstDequant;
     int s0 = 0;           // the next slot, and the one behind it
     uint32_t turn = 1;    // parity to wait for in s0: the first time round it is free
@@ -167,12 +177,12 @@ __global__ void __launch_bounds__(kThreads4, 1)
       flags[0] = 1;
     }
   } else if (warp >= kFirstSoft) {
-    more_registers<kRegsSoft>();
-    softmax_warps<QT, 1, false, true>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, q_raw, s_full, pv_done, flags, nullptr,
+    more_registers<R::kSoft>();
+    softmax_warps<QT, 1, false, true, true>(p, sh, cur, u0, u1, total, G, c, 0, base, tmem, q_raw, s_full, pv_done, flags, nullptr,
                                       warp, tid - 32 * kFirstSoft, [&] { mbar_arrive(q_full); },
                                       [&](uint32_t buf) { mbar_arrive(&p_full[buf]); });
   } else {
-    fewer_registers<kRegsIssue>();
+    fewer_registers<R::kIssue>();
     if (warp == 0) {
       // ---- the groups' queries, each once the group before has its last S
       uint32_t item = 0;

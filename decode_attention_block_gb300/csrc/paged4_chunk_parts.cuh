@@ -18,13 +18,16 @@ using namespace chunk;
 constexpr int kDequant = 8;          // warps
 constexpr int kThreads4 = 128 * 2 + 32 * kDequant;
 constexpr int kFirstSoft = 4, kFirstDequant = 8;  // warps, in warpgroups: 0 and 1 load queries and issue MMAs
-// Registers a thread, by warpgroup (setmaxnreg): the softmax warps hold a row's
-// 128 scores.
-constexpr int kRegsLaunch = 128;     // of 65536 for 512 threads
-constexpr int kRegsIssue = 72, kRegsSoft = 240, kRegsDequant = 96;
-static_assert(kRegsIssue < kRegsLaunch && kRegsSoft > kRegsLaunch && kRegsDequant < kRegsLaunch &&
-                  kRegsIssue + kRegsSoft + 2 * kRegsDequant <= 4 * kRegsLaunch,
-              "some give up what the others take (a dec to more than a thread has is an illegal instruction)");
+// Registers a thread, by warpgroup (setmaxnreg): each group gives up or takes of
+// the launch's 4 x 128 (a dec to more than a thread has is an illegal instruction).
+constexpr int kRegsLaunch = 128;  // of 65536 for 512 threads
+template <int ISSUE, int SOFT, int DEQUANT>
+struct Regs {
+  static constexpr int kIssue = ISSUE, kSoft = SOFT, kDequant = DEQUANT;
+  static_assert(ISSUE < kRegsLaunch && SOFT > kRegsLaunch && DEQUANT < kRegsLaunch && ISSUE + SOFT + 2 * DEQUANT <= 4 * kRegsLaunch &&
+                    ISSUE % 8 + SOFT % 8 + DEQUANT % 8 == 0,
+                "registers of the launch");
+};
 
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }

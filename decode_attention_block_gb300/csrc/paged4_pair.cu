@@ -8,6 +8,16 @@
 // 2560 cycles at 128 bytes a cycle, against 2048 of MMA; of a pair each writes 64
 // and reads 128.
 //
+// The softmax warps keep a row's 128 scores in registers here (240 a thread): their
+// chain of a tile is what is longest (read twice with 152 registers: 278 us for a
+// chunk of 4096 tokens at 4096, against 262).
+//
+// Measured, a chunk of 4096 tokens at 4096: bf16 queries 262 us in a graph, 1570
+// TFLOP/s, 0.80 of the measured bf16 rate (bf16 pages 223: a tile takes 2600 cycles
+// against 2048 of MMA, the softmax slowed by the converting warps beside it on its
+// schedulers); fp32 queries 411, two MMAs for each; a window of 512 71. On single
+// CTAs 357 and more.
+//
 // Each CTA's eight converting warps report a half to its own warp 1; that of rank
 // 1 passes it on to rank 0, whose warp 1 issues the MMAs over both.
 #include "paged4_chunk_parts.cuh"
@@ -43,6 +53,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
                   const __grid_constant__ CUtensorMap tm_q8, const __grid_constant__ Args p) {
   constexpr bool kSplit = std::is_same<QT, float>::value;
   using S = Pair4Smem<kSplit>;
+  using R = Regs<96, 240, 88>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -115,7 +126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
     // ---- K(0), then K(i), V(i - 1) for the tiles of each group.  Of K warp 8 + w
     // takes half w % 2 of the rows of block w / 2 of this CTA's four, of V this
     // CTA's half of the dims of block w.
-    fewer_registers<kRegsDequant>();
+    fewer_registers<R::kDequant>();
     const int w = warp - kFirstDequant;
     uint32_t kk = 0, kv = 0;
     bool ok = true;
@@ -193,13 +204,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       flags[0] = 1;
     }
   } else if (warp >= kFirstSoft) {
-    more_registers<kRegsSoft>();
+    more_registers<R::kSoft>();
     const uint32_t q_bar = in_rank0(q_full), p_bar = in_rank0(p_full);
     softmax_warps<QT, 2, !kSplit, true>(p, sh, cur, u0, u1, total, G, c, rank, base, tmem, q_raw, s_full, pv_done, flags,
                                         base + S::kStage, warp, tid - 32 * kFirstSoft, [&] { arrive_at(q_bar); },
                                         [&](uint32_t buf) { arrive_tmem_at(p_bar + 8 * buf); });
   } else {
-    fewer_registers<kRegsIssue>();
+    fewer_registers<R::kIssue>();
     if (warp == 0) {
       // ---- the groups' queries, each once the group before has its last S
       uint32_t item = 0;

@@ -320,8 +320,9 @@ constexpr int kStageBytes = 32 * kStageRow;    // of a warp
 // lane per warp tells the MMA warp that fp32 queries are in halves, or the
 // probabilities in a buffer.  STAGE: whole groups' outputs leave through
 // `stage`.  FP16: queries of either type become fp16, scaled row by row, and so
-// do the probabilities.
-template <typename QT, int RANKS, bool STAGE, bool FP16 = false, typename ArriveQ, typename ArriveP>
+// do the probabilities.  TWICE: the scores are read from tensor memory twice, 64
+// at a time, for a smaller register file and code that other warps share.
+template <typename QT, int RANKS, bool STAGE, bool FP16 = false, bool TWICE = false, typename ArriveQ, typename ArriveP>
 __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cursor cur, int64_t u0, int64_t u1,
                                               int64_t total, int G, int c, int rank, unsigned char* q_s, uint32_t tmem,
                                               uint64_t* q_raw, uint64_t* s_full, uint64_t* pv_done,
@@ -381,32 +382,55 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         const bool whole = pos + kPos - 1 <= w_hi && pos >= w_lo;  // every row of the warp sees every position
         const int x0 = pos_lo - pos, x1 = pos_hi - pos;            // columns the row sees
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t s0[32], s1[32], s2[32], s3[32];
-        tc::ld32(ts, s0);
-        tc::ld32(ts + 32, s1);
-        tc::ld32(ts + 64, s2);
-        tc::ld32(ts + 96, s3);
-        tc::wait_ld(s0);
-        tc::wait_ld(s1);
-        tc::wait_ld(s2);
-        tc::wait_ld(s3);
-        if (sign != 1.f) {
-          sign32(s0, sign);
-          sign32(s1, sign);
-          sign32(s2, sign);
-          sign32(s3, sign);
+        uint32_t s0[32], s1[32], s2[TWICE ? 1 : 32], s3[TWICE ? 1 : 32];
+        auto half = [&](int at) {
+          tc::ld32(ts + at, s0);
+          tc::ld32(ts + at + 32, s1);
+          tc::wait_ld(s0);
+          tc::wait_ld(s1);
+          if (sign != 1.f) {
+            sign32(s0, sign);
+            sign32(s1, sign);
+          }
+          if (!whole) {
+            mask32(s0, seen32(x0, x1, at));
+            mask32(s1, seen32(x0, x1, at + 32));
+          }
+        };
+        if constexpr (TWICE) {
+#pragma unroll 1
+          for (int at = 0; at < kPos; at += 64) {
+            half(at);
+            max32(s0, mx);
+            max32(s1, mx);
+          }
+        } else {
+          tc::ld32(ts, s0);
+          tc::ld32(ts + 32, s1);
+          tc::ld32(ts + 64, s2);
+          tc::ld32(ts + 96, s3);
+          tc::wait_ld(s0);
+          tc::wait_ld(s1);
+          tc::wait_ld(s2);
+          tc::wait_ld(s3);
+          if (sign != 1.f) {
+            sign32(s0, sign);
+            sign32(s1, sign);
+            sign32(s2, sign);
+            sign32(s3, sign);
+          }
+          if (!whole) {
+            uint32_t seen[4] = {seen32(x0, x1, 0), seen32(x0, x1, 32), seen32(x0, x1, 64), seen32(x0, x1, 96)};
+            mask32(s0, seen[0]);
+            mask32(s1, seen[1]);
+            mask32(s2, seen[2]);
+            mask32(s3, seen[3]);
+          }
+          max32(s0, mx);
+          max32(s1, mx);
+          max32(s2, mx);
+          max32(s3, mx);
         }
-        if (!whole) {
-          uint32_t seen[4] = {seen32(x0, x1, 0), seen32(x0, x1, 32), seen32(x0, x1, 64), seen32(x0, x1, 96)};
-          mask32(s0, seen[0]);
-          mask32(s1, seen[1]);
-          mask32(s2, seen[2]);
-          mask32(s3, seen[3]);
-        }
-        max32(s0, mx);
-        max32(s1, mx);
-        max32(s2, mx);
-        max32(s3, mx);
         float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         mt = mt == -INFINITY || tok >= g.n_tok ? -INFINITY : mt * scale;
         if (u == t0) {
@@ -430,10 +454,19 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         }
         const float ref = m == -INFINITY ? 0.f : m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        exp32<kSplit, FP16>(ts, s0, scale, ref, sum);
-        exp32<kSplit, FP16>(ts + 32, s1, scale, ref, sum);
-        exp32<kSplit, FP16>(ts + 64, s2, scale, ref, sum);
-        exp32<kSplit, FP16>(ts + 96, s3, scale, ref, sum);
+        if constexpr (TWICE) {
+#pragma unroll 1
+          for (int at = 64; at >= 0; at -= 64) {
+            if (at == 0) half(0);
+            exp32<kSplit, FP16>(ts + at, s0, scale, ref, sum);
+            exp32<kSplit, FP16>(ts + at + 32, s1, scale, ref, sum);
+          }
+        } else {
+          exp32<kSplit, FP16>(ts, s0, scale, ref, sum);
+          exp32<kSplit, FP16>(ts + 32, s1, scale, ref, sum);
+          exp32<kSplit, FP16>(ts + 64, s2, scale, ref, sum);
+          exp32<kSplit, FP16>(ts + 96, s3, scale, ref, sum);
+        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::wait_st();
       }
