@@ -58,6 +58,11 @@ constexpr int kTile4 = kTileBlocks * fp4::kRows;  // positions of a tile
 constexpr int kCtas4 = 3;        // CTAs per SM
 constexpr int kSlots4 = 3;       // halves of tiles (K or V) a warp has room for
 constexpr int kMinUnits4 = 4;    // tiles per CTA at least: one per warp
+// Tiles of a warp after which its output is added to a sum in memory: the MMAs cut
+// a sum off below its last bit, up to 2^-23 of it a step, two steps a tile (128
+// sequences at 130000, fp32 queries, 32000 positions a warp: 2.5e-5 of the output,
+// so 1.6e-6, for 3280 us instead of 3260).
+constexpr int kFoldTiles4 = 64;
 constexpr int kPad = 4;          // floats behind each 32 of a state in shared memory
 constexpr int kPRow = kTile4 + 4;  // floats of a head's scores of a tile, and a shift of banks
 constexpr float kRaise4 = 8.0f;
@@ -192,11 +197,36 @@ __device__ __forceinline__ uint32_t scale2(uint32_t w, int i) { return __byte_pe
 struct State4 {
   float o[kHeadDim / 16][4];
   float m[2], mg, l;
+  float m_sum[2];  // maxima of the sum in memory, -inf while there is none
   __device__ __forceinline__ void reset() {
+    clear();
+    m[0] = m[1] = mg = m_sum[0] = m_sum[1] = -INFINITY;
+    l = 0.f;
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kHeadDim / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    m[0] = m[1] = mg = -INFINITY;
-    l = 0.f;
+  }
+  // o += the lane's part of the sum in memory, under the maxima of now
+  __device__ __forceinline__ void add(const float4* sum) {
+    float f[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f[j] = m_sum[j] == -INFINITY ? 0.f : ex2(m_sum[j] - m[j]);
+#pragma unroll
+    for (int i = 0; i < kHeadDim / 16; ++i) {
+      const float4 x = sum[32 * i];
+      o[i][0] = fmaf(f[0], x.x, o[i][0]);
+      o[i][1] = fmaf(f[1], x.y, o[i][1]);
+      o[i][2] = fmaf(f[0], x.z, o[i][2]);
+      o[i][3] = fmaf(f[1], x.w, o[i][3]);
+    }
+  }
+  __device__ __forceinline__ void put(float4* sum) {
+#pragma unroll
+    for (int i = 0; i < kHeadDim / 16; ++i) sum[32 * i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+    m_sum[0] = m[0];
+    m_sum[1] = m[1];
+    clear();
   }
 };
 
@@ -463,6 +493,10 @@ __global__ void __launch_bounds__(kThreads4, kCtas4)
   int skip = warp;  // the CTA's tiles before the warp's next one
   Queries Q;
   State4 st;
+  auto sum = [&] {
+    return reinterpret_cast<float4*>(p.part + paged::kTokenPartBytes / sizeof(float) +
+                                     (int64_t)(c * kConsumers + warp) * paged::kWarpSums) + lane;
+  };
   bool ok = true;
   for (;;) {
     int n, tiles, pos, lo, hi;
@@ -497,6 +531,10 @@ __global__ void __launch_bounds__(kThreads4, kCtas4)
     };
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i, pos += kConsumers * kTile4) {
+      if (i % kFoldTiles4 == 0 && i > 0) {
+        if (i > kFoldTiles4) st.add(sum());
+        st.put(sum());
+      }
       const int r0 = lo > pos ? lo - pos : 0, r1 = hi + 1 - pos < kTile4 ? hi + 1 - pos : kTile4;
       float mx[2];
       if (!landed()) break;
@@ -518,6 +556,7 @@ __global__ void __launch_bounds__(kThreads4, kCtas4)
         in.advance();
       }
     }
+    if (ok && tiles > kFoldTiles4) st.add(sum());
     // the warps' states lie in a slot of each: the slots are all free now
     const MergeSmem msm{reinterpret_cast<float*>(base + S::kM), reinterpret_cast<float*>(base + S::kL),
                         reinterpret_cast<float*>(base)};
@@ -553,13 +592,14 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
 }  // namespace
 
 cudaError_t launch_paged4_attention(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st) {
-#ifdef FORCE_PAIR
-  if (p.max_q > 1) return launch_paged4_pair(p, qdtype, k, v, st);
-#endif
+  if (p.max_q == 1) return qdtype == SPARK_BF16 ? launch_token4<__nv_bfloat16>(p, k, v, st) : launch_token4<float>(p, k, v, st);
+  // Pairs of CTAs or single ones by the rule of launch_paged_attention, for its
+  // reasons (bf16 queries: 32 sequences of 33 tokens at 4096-8192 158 us on pairs,
+  // 200 on single CTAs, a chunk of 4096 262 and 357; 4 tokens each 151 and 96, 32
+  // of them 4 with chunks of ~400 tokens 157 and 131, fp32 queries 211 and 182).
   if (p.max_q > paged::kChunkTokens && (2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q || p.n_tokens > 128 * p.n_seqs))
     return launch_paged4_pair(p, qdtype, k, v, st);
-  if (p.max_q > 1) return launch_paged4_chunk(p, qdtype, k, v, st);
-  return qdtype == SPARK_BF16 ? launch_token4<__nv_bfloat16>(p, k, v, st) : launch_token4<float>(p, k, v, st);
+  return launch_paged4_chunk(p, qdtype, k, v, st);
 }
 
 }  // namespace spark

@@ -7,17 +7,17 @@
 // scaled row by row by a power of two (fp32 ones as two fp16 halves), and
 // probabilities are fp16 (fp32 queries: two halves).  Warp 0 loads the queries,
 // which warps 4-7 (softmax) convert, warp 1 issues the MMAs, warps 8-15 fill
-// the ring, warp 8 + w half w % 2 of the dims of positions 32 (w / 2) .. + 31.
+// the ring, warp 8 + w with positions 16 w .. + 15 of a tile.
 // Rows of V that no token of the group sees are stored as zeros.
 //
 // Bound by shared memory: a tile's operands are written (128 KB) and read by the
 // MMAs (192 KB; 384 with fp32 queries), 2560 cycles at 128 bytes a cycle against
 // 2048 of MMA, and the codes' loads go through the same pipe.  32 sequences at
-// 4096-8192 (0.23 GB), bf16 queries: 4 tokens each 96 us, 32 tokens 110 (bf16 pages,
-// 0.82 GB: 132 and 147); fp32 queries 137; a mixed batch of 32, 4 of them with
-// chunks of ~400 tokens, 131 and 182.  What it cost on the way (4 tokens each): half
-// lines of codes a load 113, scores kept in 240 registers a thread, the MMA warp
-// spilling, 102.
+// 4096-8192 (0.23 GB), bf16 queries: 4 tokens each 98 us, 32 tokens 111 (bf16 pages,
+// 0.82 GB: 132 and 147); fp32 queries 156; a mixed batch of 32, 4 of them with
+// chunks of ~400 tokens, 134 and 211.  What it cost on the way (4 tokens each): half
+// lines of codes a load 15 more, scores kept in 240 registers a thread, the MMA
+// warp spilling, 4.
 #include "paged4_chunk_parts.cuh"
 
 namespace spark {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
       const int n = (int)(t1 - t0);
       int x = (cur.g.tile0 + (int)(t0 - cur.begin)) * kPos + 16 * w;
       const int end = x + n * kPos;  // behind the share's tiles
-      Blocks<1> blocks;
+      Blocks blocks;
       blocks.find(p, cur, x, end, lane);
       RowPart kp[4], vp[4];
       uint32_t at = blocks.of(0);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
         const uint32_t at_v = at;
         if (i < n) {
           store(kp);
-          if ((i + 1) % Blocks<1>::kTiles == 0) blocks.find(p, cur, x + kPos, end, lane);
+          if ((i + 1) % Blocks::kTiles == 0) blocks.find(p, cur, x + kPos, end, lane);
           at = blocks.of(i + 1);
           load(kp, in_k, at);
         }
@@ -231,13 +231,13 @@ __global__ void __launch_bounds__(kThreads4, 1)
           const uint64_t a0 = tc::desc_k_major(q_addr + 2 * half * S::kQLine);
           if (one) {
 #pragma unroll
-            for (int line = 0; line < 2; ++line)
+            for (int part = S::kQ - 1; part >= 0; --part)  // (the remainders first: kFoldTiles)
 #pragma unroll
-              for (int part = 0; part < S::kQ; ++part)
+              for (int line = 0; line < 2; ++line)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                   tc::mma_ss(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
-                             b0 + (line * kAtom >> 4) + 2 * ks, kIdS, half + line + part + ks > 0);
+                             b0 + (line * kAtom >> 4) + 2 * ks, kIdS, half > 0 || part < S::kQ - 1 || line + ks > 0);
             tc::commit(&empty[s]);
             if (half == 1) tc::commit(&s_full[i & 1]);
           }

@@ -2,10 +2,11 @@
 // share (paged4_chunk.cu: one CTA and 32 tokens a group; paged4_pair.cu: two
 // CTAs and 64): blocks of pages into fp16 operands in shared memory.
 //
-// A warp takes half of the dims of a block or two: plain loads of codes and scales into registers, a
-// tile ahead of their use (a block's parts are contiguous, so nothing is gained
-// by a copy engine, and no shared memory is spent on bytes that are read once),
-// then conversion and 16-byte stores in the layout of paged_chunk_parts.cuh.
+// A warp takes a block or half of its rows or dims: plain loads of codes and scales
+// into registers, a tile ahead of their use (a block's parts are contiguous, so
+// nothing is gained by a copy engine, and no shared memory is spent on bytes that
+// are read once), then conversion and 16-byte stores in the layout of
+// paged_chunk_parts.cuh.
 #pragma once
 
 #include "paged_chunk_parts.cuh"
@@ -73,30 +74,23 @@ struct Lanes {
   }
 };
 
-// The blocks of a warp's positions in a group's tiles, N neighbours a tile, found
-// for 32 / N tiles at a time, one per lane.
-template <int N>
+// The block of a warp's positions in each of a group's tiles, found for 32 tiles at
+// a time, one per lane.
 struct Blocks {
-  static constexpr int kTiles = 32 / N;
+  static constexpr int kTiles = 32;
   uint32_t mine;
-  // those at x and the N - 1 behind it in the tile there and the ones 128 and so
-  // on further, before `end`
+  // those at x and at the 31 places kPos apart behind it, before `end`
   __device__ __forceinline__ void find(const Args& p, const Cursor& cur, int x, int end, int lane) {
-    x += lane / N * kPos;
+    x += lane * kPos;
     mine = Lanes::kNone;
-    if (x < end) {
-      x += lane % N * fp4::kRows;
-      if (x <= cur.g.hi && x + fp4::kRows > cur.g.lo) {
-        const int col = paged::page_col(p, x), in_page = (x - col * p.page_size) / fp4::kRows;
-        const int page = paged::page_of(p, paged::page_entry(p, cur.s, col));
-        // (pages * page_size < 2^31: the blocks of all heads are below 2^30)
-        mine = ((uint32_t)page * (uint32_t)(p.page_size / fp4::kRows) + (uint32_t)in_page) * (uint32_t)p.n_kv + (uint32_t)cur.j;
-      }
+    if (x < end && x <= cur.g.hi && x + fp4::kRows > cur.g.lo) {
+      const int col = paged::page_col(p, x), in_page = (x - col * p.page_size) / fp4::kRows;
+      const int page = paged::page_of(p, paged::page_entry(p, cur.s, col));
+      // (pages * page_size < 2^31: the blocks of all heads are below 2^30)
+      mine = ((uint32_t)page * (uint32_t)(p.page_size / fp4::kRows) + (uint32_t)in_page) * (uint32_t)p.n_kv + (uint32_t)cur.j;
     }
   }
-  __device__ __forceinline__ uint32_t of(int tile, int b = 0) const {
-    return __shfl_sync(0xffffffffu, mine, tile % kTiles * N + b);
-  }
+  __device__ __forceinline__ uint32_t of(int tile) const { return __shfl_sync(0xffffffffu, mine, tile % kTiles); }
 };
 
 // The part's 32 dims of each row as fp16: with c = lane / 8, line c / 2 of 64

@@ -15,8 +15,8 @@
 // Measured, a chunk of 4096 tokens at 4096: bf16 queries 262 us in a graph, 1570
 // TFLOP/s, 0.80 of the measured bf16 rate (bf16 pages 223: a tile takes 2600 cycles
 // against 2048 of MMA, the softmax slowed by the converting warps beside it on its
-// schedulers); fp32 queries 411, two MMAs for each; a window of 512 71. On single
-// CTAs 357 and more.
+// schedulers); fp32 queries 551, two MMAs for each and their sums into memory
+// (kFoldTiles); a window of 512 72.  On single CTAs 357 and more.
 //
 // Each CTA's eight converting warps report a half to its own warp 1; that of rank
 // 1 passes it on to rank 0, whose warp 1 issues the MMAs over both.
@@ -159,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       const int x0 = (cur.g.tile0 + (int)(t0 - cur.begin)) * kPos;
       int xk = x0 + 64 * rank + 16 * (w >> 1), xv = x0 + 16 * w;
       const int end_k = xk + n * kPos, end_v = xv + n * kPos;  // behind the share's tiles
-      Blocks<1> blocks_k, blocks_v;
+      Blocks blocks_k, blocks_v;
       blocks_k.find(p, cur, xk, end_k, lane);
       blocks_v.find(p, cur, xv, end_v, lane);
       RowPart kp[2];
@@ -262,13 +262,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
         const uint64_t b0 = tc::desc_k_major(ring_k + s * kSlot, kGroupBytes<4>);
         if (one) {
 #pragma unroll
-          for (int line = 0; line < 4; ++line)
+          for (int part = S::kQ - 1; part >= 0; --part)  // (the remainders first: kFoldTiles)
 #pragma unroll
-            for (int part = 0; part < S::kQ; ++part)
+            for (int line = 0; line < 4; ++line)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 tc::mma_ss2(d, a0 + ((part * kLineBytes + line * S::kQLine) >> 4) + 2 * ks,
-                            b0 + (line * kAtom >> 4) + 2 * ks, kIdS, line + part + ks > 0);
+                            b0 + (line * kAtom >> 4) + 2 * ks, kIdS, part < S::kQ - 1 || line + ks > 0);
           tc::commit_both(&k_empty[s]);
           tc::commit_both(&s_full[i & 1]);
         }

@@ -41,6 +41,19 @@ template <int LINES>  // of a slot
 constexpr uint32_t kGroupBytes = LINES * kAtom;
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O starts at 0
+// The MMAs cut each sum in O off below its last bit instead of rounding it: a
+// step takes up to 2^-23 of a sum, always towards zero, and a tile is 8 steps, 16
+// with fp32 queries (130000 positions in one share, fp32: 1.8e-4 of the output).
+// So over fp16 operands O is added to a sum in memory, in the group's part of the
+// workspace, every so many tiles.  bf16 outputs: 64, at most 2^-14 of a sum, for 1
+// to 2% of the time.  fp32 ones: 4, 1.3e-6 of the output at any length, where fp32
+// products of fp32 operands have 1e-6; a mixed batch of 32 takes 211 us for it, a
+// chunk of 4096 551 (8 tiles, 2.2e-6: 193 and 477; 16, 4e-6: 183 and 443; never: 183
+// and 410).  Done before a tile's probabilities, not behind them, it left the
+// MMAs idle: 237 us.  The remainders of fp32 queries are multiplied first, into
+// scores still small (1.5e-6 else).
+template <typename QT>
+constexpr int kFoldTiles = std::is_same<QT, float>::value ? 4 : 64;
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
 
 // L2 policies of the pool's rows.  A sequence of one group reads its rows
@@ -341,6 +354,8 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
   uint32_t tile = 0;
   bool ok = true;
   constexpr bool kSplit = std::is_same<QT, float>::value, kConvert = kSplit || FP16;
+  constexpr int kFold = FP16 ? kFoldTiles<QT> : 0;
+  constexpr int kAll = RANKS * kRows;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, flags, kWaitLimitNs));
     tc::fence_after();
@@ -372,6 +387,48 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     const bool live = tok0 + 8 * quad < g.n_tok;  // the warp has a row
     const int w_hi = __shfl_sync(0xffffffffu, pos_hi, 0), w_lo = __shfl_sync(0xffffffffu, pos_lo, 31);
     float m = -INFINITY, l = 0.f;
+    bool folded = false;
+    float m_sum = -INFINITY;  // of the sums in memory
+    // O and those so far into memory and O cleared, or (end) into O; they are the
+    // row's part of the group's partial state, free until the group ends
+    auto fold = [&](bool end) {
+      constexpr int kAhead = 4;  // pieces of 16 dims asked for ahead of their use
+      float4* sums = reinterpret_cast<float4*>(p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) *
+                                                            (RANKS * paged::kChunkPart)) + prow;
+      const float old = m_sum == -INFINITY ? 0.f : ex2(m_sum - m);
+      float4 x[kAhead][4];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[k][i] = folded ? sums[(4 * k + i) * kAll] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int d = 0; d < kHeadDim; d += 16 * kAhead)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          float4* at = sums + (d / 4 + 4 * k) * kAll;
+          uint32_t o[16];
+          tc::ld16(tmem + lanes + d + 16 * k, o);
+          tc::wait_ld(o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 y = x[k][i];
+            o[4 * i] = __float_as_uint(fmaf(old, y.x, __uint_as_float(o[4 * i])));
+            o[4 * i + 1] = __float_as_uint(fmaf(old, y.y, __uint_as_float(o[4 * i + 1])));
+            o[4 * i + 2] = __float_as_uint(fmaf(old, y.z, __uint_as_float(o[4 * i + 2])));
+            o[4 * i + 3] = __float_as_uint(fmaf(old, y.w, __uint_as_float(o[4 * i + 3])));
+            if (folded && d + 16 * kAhead < kHeadDim) x[k][i] = at[(4 * kAhead + i) * kAll];
+            if (!end) {
+              at[i * kAll] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                         __uint_as_float(o[4 * i + 3]));
+              o[4 * i] = o[4 * i + 1] = o[4 * i + 2] = o[4 * i + 3] = 0u;
+            }
+          }
+          tc::st16(tmem + lanes + d + 16 * k, o);
+        }
+      tc::wait_st();
+      folded = true;
+      m_sum = m;
+    };
     for (int64_t u = t0; u < t1; ++u, ++tile) {
       const uint32_t buf = tile & 1;
       if (!wait(&s_full[buf], (tile >> 1) & 1)) break;
@@ -470,6 +527,10 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::wait_st();
       }
+      if (kFold > 0 && u > t0 && (int)(u - t0) % (kFold > 0 ? kFold : 1) == 0) {
+        if (!wait(&pv_done[buf ^ 1], ((tile - 1) >> 1) & 1)) break;
+        if (live) fold(false);
+      }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) arrive_p(buf);
@@ -486,7 +547,7 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       float* part = p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) * (RANKS * paged::kChunkPart);
       QT* dst = out + ((r * p.n_kv + cur.j) * kGroup + (row & 3)) * kHeadDim;
       const float inv = 1.0f / l;
-      constexpr int kAll = RANKS * kRows;
+      if (kFold > 0 && folded) fold(true);
       // A partial state is [dims / 4][row][4], then the maxima and the sums: the
       // lanes' rows lie next to one another (row by row, 32 lines of 128 bytes
       // per store, the output took 10000 cycles a group).

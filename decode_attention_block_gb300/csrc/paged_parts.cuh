@@ -16,10 +16,13 @@ constexpr int kMaxCtas = 480;
 constexpr int kChunkTokens = 32;
 constexpr int kMaxChunkCtas = 160;
 constexpr int kChunkPart = kGroup * kChunkTokens * (kHeadDim + 2);
-// bytes of the partial states of either kernel
+// bytes of the partial states of either kernel; behind the token kernel's what a
+// warp over 4-bit pages sums up beside its registers (4 warps a CTA, 8 rows)
 constexpr size_t kTokenPartBytes = sizeof(float) * 2 * kMaxCtas * kPartFloats;
+constexpr int kWarpSums = 8 * kHeadDim;
 constexpr size_t kChunkPartBytes = sizeof(float) * 2 * kMaxChunkCtas * kChunkPart;
 constexpr size_t kPartBytes = kTokenPartBytes > kChunkPartBytes ? kTokenPartBytes : kChunkPartBytes;
+static_assert(kTokenPartBytes % 16 == 0 && kTokenPartBytes + sizeof(float) * 4 * kMaxCtas * kWarpSums <= kPartBytes, "room for both");
 
 // A group of the chunk kernel that begins in a CTA's share and goes on behind
 // it: what the join needs.  n_rows 0: there is none.

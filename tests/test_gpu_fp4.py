@@ -472,6 +472,42 @@ def test_large_scores_and_one_dominant_row(B):
             assert err.max().item() <= 1.0
 
 
+@pytest.mark.parametrize("n_seqs, n, c, q_type", [(480, 1, 400000, F32), (160, 8, 50000, F32), (80, 40, 50000, F32),
+                                                  (160, 8, 50000, BF16), (80, 40, 50000, BF16)])
+def test_long_sums_keep_their_bits(B, n_seqs, n, c, q_type):
+    """Sums of positive values over a whole long sequence per share: what the matrix instructions cut off (up to 2^-23 of
+    the sum a step, towards zero) may come to 2^-15 of it for fp32 queries, 2^-14 for bf16 ones, whatever the length.
+    Scores are tiny (2 |ds| below 2^-20), probabilities as above (the sum of a row's rounded to nearest: sqrt(12500) 2^-24
+    is within the 2^-17)."""
+    g, gen = _geom(B, 1, 512, 0.0625), torch.Generator("cuda").manual_seed(5)
+    page = 256
+    entries = torch.randperm(-(-c // page), generator=gen, device="cuda").int()
+    pools, vals = [], []
+    for make in (torch.randn, torch.rand):
+        code, sc = fp4_ref.quantize(make(c, 1, D, generator=gen, device="cuda"))
+        pool = torch.full((len(entries), page // 16, 1, fp4_ref.BLOCK), 0xFF, dtype=torch.uint8, device="cuda")
+        fp4_ref.write(pool, entries, page, torch.arange(c, device="cuda"), code, sc)
+        pools.append(pool)
+        vals.append(fp4_ref.values(code, sc)[:, 0])
+        del code, sc
+    some = 3  # sequences with queries of their own, all of the same pages
+    q3 = (torch.randn(some, n, 4, D, generator=gen, device="cuda") * 2.0 ** -10).to(q_type)
+    q = q3[torch.arange(n_seqs, device="cuda") % some].reshape(n_seqs * n, 4 * D)
+    batch = B.PagedBatch(entries.repeat(n_seqs, 1).contiguous(), _i32([n * i for i in range(n_seqs + 1)]), _i32([c] * n_seqs), n_seqs * n, n)
+    a, ws = torch.zeros(n_seqs * n, 4 * D, device="cuda", dtype=q_type), B.make_paged_workspace(g)
+    B.spark_paged_attention(g, q, B.PagePool(*pools), B.SPARK_FULL, batch, a, ws)
+    torch.cuda.synchronize()
+    assert B.spark_attn_error_word(ws) == 0
+    z = 0.0625 * torch.einsum("sthd,xd->sthx", q3.double(), vals[0])
+    late = torch.arange(c, device="cuda")[None] > torch.arange(c - n, c, device="cuda")[:, None]
+    want = torch.softmax(z.masked_fill(late[None, :, None], -np.inf), -1) @ vals[1]
+    rel = 2.0 ** -20 + 2.0 ** -17 + (2.0 ** -22 + 2.0 ** -15 if q_type == F32 else 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -8)
+    want = want[torch.arange(n_seqs, device="cuda") % some]
+    err = (a.double().view(n_seqs, n, 4, D) - want).abs()
+    worst = (err / want).max().item()
+    assert worst <= rel, f"{worst:.2g} of the output, bound {rel:.2g}"
+
+
 def test_repeated_and_unordered_calls_agree(B):
     g = _geom(B)
     ws, runs = B.make_paged_workspace(g), []
