@@ -16,7 +16,7 @@
 // TFLOP/s, 0.80 of the measured bf16 rate (bf16 pages 223: a tile takes 2600 cycles
 // against 2048 of MMA, the softmax slowed by the converting warps beside it on its
 // schedulers); fp32 queries 551, two MMAs for each and their sums into memory
-// (kFoldTiles); a window of 512 72.  On single CTAs 357 and more.
+// (kFoldTiles); a window of 512 72.  On single CTAs 328, 596 and 77.
 //
 // Each CTA's eight converting warps report a half to its own warp 1; that of rank
 // 1 passes it on to rank 0, whose warp 1 issues the MMAs over both.
