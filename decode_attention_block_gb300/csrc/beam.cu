@@ -153,7 +153,7 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
     }
     if (lane == 0) {
       const bool any = live ? !bad && top > -INFINITY : done != 0 && fabsf(score) < INFINITY;
-      sm.base[b] = Two{any ? score : -INFINITY, 0.f};
+      sm.base[b] = Two{any ? score + 0.f : -INFINITY, 0.f};  // (-0 is 0: equal scores have equal keys)
       sm.z[b] = z;
       sm.top[b] = top;
       sm.ended[b] = done != 0;
@@ -185,6 +185,7 @@ __device__ __forceinline__ void join_group(const Select& a, int group, int k, in
     if (key == 0 || !(x > -INFINITY)) return Offer{0, 0};
     // (x - m first: logits may be far larger than the scores)
     const Two v = settle(add(settle(two_sum(x, -sm.top[b])), base));
+    if (!(fabsf(v.hi) < INFINITY)) return Offer{0, 0};  // below what fp32 holds
     return Offer{value_key(v), (uint32_t)b * (uint32_t)a.vocab + (uint32_t)key_index(key)};
   };
   Offer head[kHeads];

@@ -57,16 +57,35 @@ int spark_beam_reorder(const int32_t* parent, const int32_t* keep_len, const int
     return SPARK_ERR_INVALID_ARG;
   if (!aligned4(keep_len) || !aligned4(new_len)) return SPARK_ERR_INVALID_ARG;
   beam::States all = {};
+  // what a call writes is nothing that it reads or writes elsewhere
+  struct Span {
+    uintptr_t begin, end;
+    bool meets(const Span& o) const { return begin < o.end && o.begin < end; }
+  };
+  auto span = [](const void* p, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Span{a, p ? a + (uintptr_t)bytes : a};
+  };
+  const Span lists[3] = {span(parent, 4 * (int64_t)n_slots), span(keep_len, 4 * (int64_t)n_slots), span(new_len, 4 * (int64_t)n_slots)};
   for (int i = 0; i < n_states; ++i) {
     const spark_beam_state& t = states[i];
     if (!words(t.src) || !words(t.dst) || t.pitch < 4 || t.pitch % 4 != 0 || t.pitch >= ((int64_t)1 << 31) || t.elem < 0 ||
         t.elem % 4 != 0 || t.elem > t.pitch || !aligned4(t.push) || (t.push && t.elem != 4))
       return SPARK_ERR_INVALID_ARG;
     if (t.elem > 0 && (!keep_len || !new_len)) return SPARK_ERR_INVALID_ARG;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(t.src), b = reinterpret_cast<uintptr_t>(t.dst);
-    const uintptr_t n = (uintptr_t)n_slots * (uintptr_t)t.pitch;
-    if (a < b + n && b < a + n) return SPARK_ERR_INVALID_ARG;
+    const Span dst = span(t.dst, n_slots * t.pitch);
+    for (const Span& l : lists)
+      if (dst.meets(l)) return SPARK_ERR_INVALID_ARG;
     all.s[i] = t;
+  }
+  for (int i = 0; i < n_states; ++i) {
+    const Span dst = span(states[i].dst, n_slots * states[i].pitch);
+    for (int j = 0; j < n_states; ++j) {
+      const spark_beam_state& o = states[j];
+      if (dst.meets(span(o.src, n_slots * o.pitch)) || dst.meets(span(o.push, 4 * (int64_t)n_slots)) ||
+          (i != j && dst.meets(span(o.dst, n_slots * o.pitch))))
+        return SPARK_ERR_INVALID_ARG;
+    }
   }
   const int s = check_beam_ws(workspace, workspace_bytes);
   if (s != SPARK_OK) return s;

@@ -53,7 +53,8 @@ size_t spark_beam_workspace_bytes(int32_t n_groups, int32_t n_beams);
  * A group with fewer offers than beams leaves slots over: score -inf, token
  * and parent -1, done 1, lengths 0.  Logits of -inf are no offers; a row with
  * no distribution (every logit -inf, a +inf or a NaN in it) offers nothing,
- * a score of +inf or NaN neither.
+ * a score of +inf or NaN neither, nor what would have a score below fp32's
+ * range.
  * Sums are fp32, the scores are compared in 64 bits and rounded to fp32 once.
  * new_score may be score, new_done done and new_len length.
  * n_beams: 1 .. SPARK_MAX_BEAMS; n_groups * n_beams: 1 .. SPARK_MAX_BATCH;
@@ -72,7 +73,7 @@ int spark_beam_select(const void* logits, int64_t ld, int32_t dtype, int32_t n_g
  *            them go along (a token history).
  *   push     device [slots] int32 (elem 4 only, or null): where new_len is more
  *            than keep_len, push[s] is written behind the positions kept.
- * src and dst do not overlap. */
+ * No dst overlaps another, a src, a push or the lists of the call. */
 typedef struct spark_beam_state {
   const void* src;
   void* dst;

@@ -167,7 +167,9 @@ int spark_paged_read(const spark_geom* g, const spark_page_pool* pool, const spa
  * and head: fp32 ones as q = hi + lo (22 bits of the token's and head's
  * largest element), bf16 ones as they are (elements below 2^-23 of the
  * largest lose bits); probabilities as hi + lo, but rounded to fp16 (11 bits)
- * for bf16 queries where max_q_len is more than 1.
+ * for bf16 queries where max_q_len is more than 1.  Outputs are summed in
+ * fp32; what the matrix instructions cut off a sum stays below 2^-16 of it for
+ * fp32 queries and 2^-14 for bf16 ones, however long the sequence.
  * Rows that no token of the sequence attends to may hold anything, NaN
  * included; a row that one of its new tokens attends to is expected finite
  * (a non-finite V row may reach every new token of its sequence).

@@ -176,6 +176,33 @@ def test_dominated_and_far_apart_scores(B):
     _check(B, logits * 1e4, score, 6)
 
 
+def test_zeros_of_either_sign_are_equal(B):
+    logits, score = _random(4, 1000, seed=11)
+    out = _check(B, logits, torch.tensor([-0.0, 0.0, 0.0, -0.0], device="cuda"), 4, 9, _i32([1] * 4))
+    assert out["parent"].tolist() == [0, 1, 2, 3]
+    # all of a row's weight on one token: a live beam's score stays 0
+    logits[1:3] = -INF
+    logits[1:3, 5] = -0.0
+    out = _check(B, logits, torch.tensor([-1.0, 0.0, -0.0, -0.0], device="cuda"), 4, 9, _i32([1, 0, 0, 1]))
+    assert out["parent"].tolist() == [1, 2, 3, 0] and out["token"].tolist() == [5, 5, 9, 9]
+
+
+def test_what_fp32_cannot_hold_is_no_offer(B):
+    """Next to a logit of 3e38 one of -3e38 has a log probability of -6e38."""
+    logits = torch.full((6, 70000), -3e38, device="cuda")
+    logits[:, 3] = 3e38
+    logits[:3, 69999] = 3e38
+    out = _lists(6)
+    ws = B.make_beam_workspace(2, 3)
+    _select(B, logits, torch.full((6,), -1.0, device="cuda"), None, _i32([4] * 6), 3, -1, ws, out)
+    assert out["token"].tolist() == [3, 69999, 3, 3, 3, 3] and out["parent"].tolist() == [0, 0, 1, 3, 4, 5]
+    half = -1.0 - np.log(2.0)
+    assert np.allclose(out["new_score"].tolist(), [half] * 3 + [-1.0] * 3, atol=2.0 ** -18)
+    _select(B, logits[3:], torch.tensor([-1.0, -INF, -INF], device="cuda"), None, _i32([4] * 3), 3, -1, ws, first := _lists(3))
+    assert first["parent"].tolist() == [0, -1, -1] and first["new_score"].tolist()[1:] == [-INF, -INF]
+    assert B.spark_attn_error_word(ws) == 0
+
+
 def test_outputs_in_place_of_inputs(B):
     for n, W, vocab in ((64, 8, 9001), (4, 4, 131072)):
         logits, score = _random(n, vocab, seed=2)

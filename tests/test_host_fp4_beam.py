@@ -122,7 +122,18 @@ def test_beam_reorder_arguments_are_validated(B):
                dict(dst=FAKE), dict(dst=FAKE + 1596), dict(dst=FAKE - 1596), dict(keep=FAKE + 2)):
         assert call(**kw) == -1, kw
     one = B.SparkBeamState(FAKE, FAKE + (1 << 20), 400, 0, 0)
-    assert call(states=[one] * 33) == -1 and call(states=[one] * 32, ws=0) == -4
+    far = [B.SparkBeamState(FAKE, FAKE + (i << 20), 400, 0, 0) for i in range(1, 34)]
+    assert call(states=far) == -1 and call(states=far[:32], ws=0) == -4
+    # what is written is read or written nowhere else in the call
+    at = FAKE + (2 << 20)
+    other = lambda **kw: B.SparkBeamState(*dict(dict(src=at, dst=at + (1 << 20), pitch=400, elem=4, push=0), **kw).values())  # noqa: E731
+    assert call(states=[one, other()], ws=0) == -4
+    for kw in (dict(src=FAKE + (1 << 20) + 1596), dict(dst=FAKE + (1 << 20) - 1596), dict(dst=FAKE + 1596),
+               dict(push=FAKE + (1 << 20) + 1596), dict(push=at + (1 << 20) - 12)):
+        assert call(states=[one, other(**kw)], ws=0) == -1, kw
+    inside = FAKE + (1 << 20) + 1584
+    for kw in (dict(parent=inside), dict(keep=inside), dict(new=inside)):
+        assert call(**kw, ws=0) == -1 and call(**{k: v + 16 for k, v in kw.items()}, ws=0) == -4
     assert call(dst=FAKE + 1600, ws=0) == -4 and call(keep=0, new=0, ws=0) == -4 and call(nbytes=need - 1) == -4
 
 
