@@ -15,11 +15,18 @@
 // Measured, a chunk of 4096 tokens at 4096: bf16 queries 262 us in a graph, 1570
 // TFLOP/s, 0.80 of the measured bf16 rate (bf16 pages 223: a tile takes 2600 cycles
 // against 2048 of MMA, the softmax slowed by the converting warps beside it on its
-// schedulers); fp32 queries 551, two MMAs for each and their sums into memory
+// schedulers); fp32 queries 547, two MMAs for each and their sums into memory
 // (kFoldTiles); a window of 512 72.  On single CTAs 328, 596 and 77.
 //
-// Each CTA's eight converting warps report a half to its own warp 1; that of rank
-// 1 passes it on to rank 0, whose warp 1 issues the MMAs over both.
+// A tile's scores, softmax and product follow one another, and two tiles are in
+// flight: 1024 + 1800 + 1024 cycles and the reports between them.  Neither two
+// softmax warps a row (64 positions each: 406 us, their maxima exchanged and their
+// registers short) nor a report of the first 64 probabilities ahead of the others
+// (280, one more wait of the issuing warp) made that shorter.
+//
+// Each CTA's eight converting warps report a half to its own CTA, rank 1's warp 1
+// passes it on to rank 0, whose warp 1 issues the MMAs over both: one wait for the
+// nine (one for each CTA's, fp32 queries: 559 us, now 547).
 #include "paged4_chunk_parts.cuh"
 #include "paged_pair_parts.cuh"
 
@@ -41,7 +48,7 @@ struct Pair4Smem {
   static constexpr uint32_t kRingV = kRingK + kK * kSlot;
   static constexpr uint32_t kStage = kRingV + kV * kSlot;  // the output's, where there is room
   static constexpr uint32_t kBars = kStage + (SPLIT ? 0 : 4 * kStageBytes);
-  static constexpr uint32_t kBytes = kBars + 8 * (3 * kK + 3 * kV + 10) + 32;
+  static constexpr uint32_t kBytes = kBars + 8 * (2 * kK + 2 * kV + 10) + 32;
   static constexpr uint32_t kAlloc = kBytes + 1024;  // slack to align the base (128-byte swizzle)
 };
 static_assert(Pair4Smem<true>::kAlloc <= 232448 && Pair4Smem<false>::kAlloc <= 232448, "227 KB per CTA");
@@ -57,12 +64,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* k_here = reinterpret_cast<uint64_t*>(base + S::kBars);  // this CTA's half of a K tile is there
-  uint64_t* k_peer = k_here + S::kK;   // rank 0: rank 1's is
-  uint64_t* k_empty = k_peer + S::kK;
+  // this CTA's half of a tile is there; rank 0: rank 1's too
+  uint64_t* k_here = reinterpret_cast<uint64_t*>(base + S::kBars);
+  uint64_t* k_empty = k_here + S::kK;
   uint64_t* v_here = k_empty + S::kK;
-  uint64_t* v_peer = v_here + S::kV;
-  uint64_t* v_empty = v_peer + S::kV;
+  uint64_t* v_empty = v_here + S::kV;
   uint64_t* s_full = v_empty + S::kV;  // [2] S(i) is in its buffer
   uint64_t* p_full = s_full + 2;       // [2] rank 0: P(i) is, in both CTAs
   uint64_t* pv_done = p_full + 2;      // [2] P(i) V(i) is in O
@@ -77,13 +83,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
   const int rank = (int)cluster_rank();
   if (tid == 0) {
     for (int s = 0; s < S::kK; ++s) {
-      mbar_init(&k_here[s], kDequant);
-      mbar_init(&k_peer[s], 1);
+      mbar_init(&k_here[s], kDequant + (rank == 0 ? 1 : 0));
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < S::kV; ++s) {
-      mbar_init(&v_here[s], kDequant);
-      mbar_init(&v_peer[s], 1);
+      mbar_init(&v_here[s], kDequant + (rank == 0 ? 1 : 0));
       mbar_init(&v_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -257,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       auto scores = [&](uint32_t i) {
         const uint32_t d = tmem + kColS + (i & 1) * kPos;
         const int s = (int)(kk % S::kK);
-        if (!here(&k_here[s], (kk / S::kK) & 1) || !both(&k_peer[s], (kk / S::kK) & 1)) return;
+        if (!both(&k_here[s], (kk / S::kK) & 1)) return;
         const uint64_t a0 = tc::desc_k_major(q_addr);
         const uint64_t b0 = tc::desc_k_major(ring_k + s * kSlot, kGroupBytes<4>);
         if (one) {
@@ -278,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
       auto values = [&](uint32_t i, bool first) {
         const uint32_t a = tmem + kColS + (i & 1) * kPos;
         const int s = (int)(kv % S::kV);
-        if (!here(&v_here[s], (kv / S::kV) & 1) || !both(&v_peer[s], (kv / S::kV) & 1)) return;
+        if (!both(&v_here[s], (kv / S::kV) & 1)) return;
         if (!both(&p_full[i & 1], (i >> 1) & 1)) return;
         const uint64_t b0 = tc::desc_mn_major(ring_v + s * kSlot, kAtom, kGroupBytes<2>);
         if (one) {
@@ -306,11 +310,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads4, 1)
             if (i > 0 && ok) values(tile + i - 1, i == 1);
           } else {
             if (i < n && here(&k_here[kk % S::kK], (kk / S::kK) & 1)) {
-              if (lane == 0) arrive_at(in_rank0(&k_peer[kk % S::kK]));
+              if (lane == 0) arrive_at(in_rank0(&k_here[kk % S::kK]));
               ++kk;
             }
             if (i > 0 && here(&v_here[kv % S::kV], (kv / S::kV) & 1)) {
-              if (lane == 0) arrive_at(in_rank0(&v_peer[kv % S::kV]));
+              if (lane == 0) arrive_at(in_rank0(&v_here[kv % S::kV]));
               ++kv;
             }
           }
