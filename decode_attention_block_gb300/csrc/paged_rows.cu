@@ -10,8 +10,8 @@
 //
 // Measured (in a graph): one token, 24 rows, 2.9 us; 64 into 4-bit pages and out
 // again 6.6; 9000 tokens of prompts, bf16, all dims rotated, into 4-bit pages and
-// out again 64 (0.26 GB: 4.1 TB/s), bound by the rotation's and the quotients'
-// instructions; 47000 rows of prefixes out of 4-bit pages 47 (0.23 GB: 4.9 TB/s).
+// out again 61 (0.26 GB: 4.3 TB/s), bound by the rotation's and the quotients'
+// instructions; 47000 rows of prefixes out of 4-bit pages 41 (0.23 GB: 5.7 TB/s).
 #include <math.h>
 
 #include <type_traits>
@@ -26,12 +26,17 @@ namespace {
 
 using paged::Args;
 
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 4;      // of a CTA (9000 tokens of prompts in and out again 61.2 us, with 8 62.3, with 2 60.8)
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kWantedWarps = 32;  // an SM, before a token has a warp alone
-constexpr int kRowCtas = 3;       // CTAs an SM of the append (4: 64 registers, spilled: 8 prompts no faster)
+constexpr int kRowCtas = 6;       // CTAs an SM of the append (32 warps: 64 registers, spilled: 8 prompts no faster)
 constexpr int kBatch = 2;         // rows of a warp in flight, behind the two being rotated (1, 3, 4: 65, 63, 71 us)
 constexpr int kReadBatch = 8;
+// Tokens of a warp of a long read: 47000 rows 47.7 us with one, 41.5 with two, 43
+// with three, 47.5 with four (the writes spread), 10 CTAs an SM.
+constexpr int kReadTokens = 2;
+constexpr int kReadCtas = 10;
+constexpr int kReadWarps = 24;    // an SM at least, for that (9000 tokens: two 2 us less)
 
 // The warp's token and its rows: first, first + step, ..
 struct Task {
@@ -50,8 +55,8 @@ struct Place {
   int pos, page, row;
 };
 
-// The sequence that token t belongs to, by a warp: 32 starts a step.
-__device__ __forceinline__ Place find_place(const Args& p, int t, int lane) {
+// The sequence that token t belongs to, if any does, by a warp: 32 starts a step.
+__device__ __forceinline__ int find_seq(const Args& p, int t, int lane) {
   int lo = 0, n = p.n_seqs;  // the last start at or before t is one of lo .. lo + n - 1, or none is
   while (n > 1) {
     const int step = (n + 31) / 32, s = lo + lane * step;
@@ -62,19 +67,26 @@ __device__ __forceinline__ Place find_place(const Args& p, int t, int lane) {
     n = min(step, n - last * step);
     if (step == 1) break;
   }
-  const paged::Seq s = paged::load_seq(p, lo);
+  return lo;
+}
+// token t's place, of sequence i; `report` a bad entry
+__device__ __forceinline__ Place place_in(const Args& p, int i, const paged::Seq& s, int t, bool report) {
   Place at = {-1, -1, 0};
   if (t < s.q0 || t >= s.q0 + s.n) return at;
   at.pos = s.p0 + (t - s.q0);
-  const int pg = paged::page_entry(p, lo, paged::page_col(p, at.pos));
+  const int pg = paged::page_entry(p, i, paged::page_col(p, at.pos));
   if (pg < 0 || pg >= p.n_pages) {
-    if (lane == 0) atomicOr(p.err, kErrIndex);
+    if (report) atomicOr(p.err, kErrIndex);
     at.pos = -1;
     return at;
   }
   at.page = pg;
   at.row = paged::page_row(p, at.pos);
   return at;
+}
+__device__ __forceinline__ Place find_place(const Args& p, int t, int lane) {
+  const int i = find_seq(p, t, lane);
+  return place_in(p, i, paged::load_seq(p, i), t, lane == 0);
 }
 
 // every sequence is looked at, also one that no token's search ends in
@@ -419,9 +431,60 @@ cudaError_t rope_t(const Args& p, const paged::RopeRows& a, cudaStream_t st) {
                     static_cast<unsigned char*>(a.pv), split, p);
 }
 
+// The same of kReadTokens tokens a warp: their places are looked up at once, a lane
+// each, and a token's rows are on their way while the one before is written.
+template <typename XT>
+__global__ void __launch_bounds__(kRowThreads, kReadCtas)
+    k_paged_read_run(const unsigned char* pk, const unsigned char* pv, XT* k, XT* v, int64_t ld, const __grid_constant__ Args p) {
+  const int lane = threadIdx.x & 31;
+  const int t0 = (int)(blockIdx.x * kRowWarps * kReadTokens + (threadIdx.x >> 5));  // and every kRowWarps-th behind it
+  pdl_wait();
+  report_bad(p);
+  if (t0 >= p.n_tokens) return;
+  const int i0 = find_seq(p, t0, lane);
+  const paged::Seq s = paged::load_seq(p, i0);
+  Place mine = {-1, -1, 0};
+  if (lane < kReadTokens) mine = place_in(p, i0, s, t0 + lane * kRowWarps, true);
+  PageRow<Fp4> row[2][kReadBatch];
+  Place at[2];
+  auto load = [&](int i, Place& to, PageRow<Fp4> (&x)[kReadBatch]) {
+    to.pos = __shfl_sync(0xffffffffu, mine.pos, i);
+    to.page = __shfl_sync(0xffffffffu, mine.page, i);
+    to.row = __shfl_sync(0xffffffffu, mine.row, i);
+    const int t = t0 + i * kRowWarps;
+    if (t >= p.n_tokens)
+      to.pos = -1;
+    else if (t >= s.q0 + s.n)
+      to = find_place(p, t, lane);  // another sequence's
+    if (to.pos < 0) return;
+#pragma unroll
+    for (int r = 0; r < kReadBatch; ++r)
+      if (r < 2 * p.n_kv) x[r].load((r & 1) ? pv : pk, p, to, r >> 1, lane);
+  };
+  load(0, at[0], row[0]);
+#pragma unroll
+  for (int i = 0; i < kReadTokens; ++i) {
+    if (i + 1 < kReadTokens) load(i + 1, at[(i + 1) & 1], row[(i + 1) & 1]);
+    if (at[i & 1].pos < 0) continue;
+#pragma unroll
+    for (int r = 0; r < kReadBatch; ++r) {
+      if (r >= 2 * p.n_kv) break;
+      float x[8];
+      row[i & 1][r].get(x);
+      put8(((r & 1) ? v : k) + (t0 + i * kRowWarps) * ld + (r >> 1) * kHeadDim + 8 * lane, x);
+    }
+  }
+}
+
 template <typename XT, typename CT>
 cudaError_t read_t(const Args& p, const void* pk, const void* pv, void* k, void* v, int64_t ld, cudaStream_t st) {
   const int split = split_for(p.n_tokens, 2 * p.n_kv);
+  // (4-bit rows: two registers each)
+  if constexpr (std::is_same<CT, Fp4>::value)
+    if (2 * p.n_kv <= kReadBatch && p.n_tokens / kReadTokens >= kReadWarps * device_sm_count())
+      return launch_pdl(k_paged_read_run<XT>, row_grid((p.n_tokens + kReadTokens - 1) / kReadTokens, 1), dim3(kRowThreads), 0, st,
+                        static_cast<const unsigned char*>(pk), static_cast<const unsigned char*>(pv), static_cast<XT*>(k),
+                        static_cast<XT*>(v), ld, p);
   return launch_pdl(k_paged_read<XT, CT>, row_grid(p.n_tokens, split), dim3(kRowThreads), 0, st,
                     static_cast<const unsigned char*>(pk), static_cast<const unsigned char*>(pv), static_cast<XT*>(k),
                     static_cast<XT*>(v), ld, split, p);

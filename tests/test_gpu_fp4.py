@@ -295,6 +295,44 @@ def test_read(B, name, page, n_kv, x_type, pool):
     assert bool((x[used:] == 3.0).all()) and bool((x[:, 2 * n_kv * D:] == 3.0).all())
 
 
+@pytest.mark.parametrize("x_type", [BF16, F32])
+@pytest.mark.parametrize("n_kv,page,most", [(1, 16, 70), (3, 48, 70), (4, 16, 9000), (8, 64, 70)])
+def test_long_reads(B, n_kv, page, most, x_type):
+    """As many tokens as a long prompt's, of a few long sequences or of many short ones, the empty among them."""
+    rng = np.random.default_rng(n_kv)
+    seqs, tokens = [], 0
+    while tokens < 9100:
+        n = int(rng.integers(0, most + 1)) if most < 9000 else (9000, 0, 7, 400)[len(seqs) % 4]
+        seqs.append((n + int(rng.integers(0, 40)), n))
+        tokens += n
+    case = Fp4Case(seqs, n_kv=n_kv, page=page, seed=5, pad=37)
+    case.fill()
+    g = _geom(B, n_kv)
+    ws = B.make_paged_workspace(g)
+    k, v = (torch.full((case.n_tokens, n_kv * D), 3.0, device="cuda", dtype=x_type) for _ in "kv")
+    B.spark_paged_read(g, B.PagePool(case.k, case.v), case.batch(B), k, v, ws)
+    assert B.spark_attn_error_word(ws) == 0
+    used = sum(case.new)
+    want = [torch.cat([r[c - n:] for r, (c, n) in zip(rows, case.seqs)]).reshape(used, -1).to(x_type)
+            for rows in (case.rows_k, case.rows_v)]
+    for got, w in zip((k, v), want):
+        assert torch.equal(got[:used], w) and bool((got[used:] == 3.0).all())
+    # an entry outside the pool: its rows are left out, and no others
+    s = max(range(len(seqs)), key=lambda i: seqs[i][1])
+    c, n = seqs[s]
+    col = (c - 1) // page
+    case.table[s, col] = case.k.shape[0]
+    k.fill_(3.0), v.fill_(3.0)
+    B.spark_paged_read(g, B.PagePool(case.k, case.v), case.batch(B), k, v, ws)
+    assert B.spark_attn_error_word(ws) == 2
+    lost = torch.zeros(case.n_tokens, dtype=torch.bool, device="cuda")
+    at = sum(m for _, m in seqs[:s]) + torch.arange(n, device="cuda")
+    lost[at[torch.arange(c - n, c, device="cuda") >= col * page]] = True
+    assert bool(lost.any())
+    for got, w in zip((k, v), want):
+        assert bool((got[lost] == 3.0).all()) and torch.equal(got[:used][~lost[:used]], w[~lost[:used]])
+
+
 def test_bad_entries_of_row_calls(B):
     """Reported, never followed; the other sequences' rows are written."""
     g = _geom(B)
