@@ -154,10 +154,15 @@ __device__ __forceinline__ void unpack(uint4 w, float (&x)[8]) {
 }
 __device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
-// the larger of two, a NaN if one is
+// the larger of two or three, a NaN if one is
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float load1(const float* p) { return __ldcg(p); }
@@ -171,6 +176,7 @@ template <typename T, bool ENTROPY>
 __device__ __forceinline__ Stat row_pass(const T* x, int vocab, int k, int share, int c, int parts, Smem& sm, WarpTop& top) {
   constexpr int kE = 16 / sizeof(T);  // elements of a 16-byte word
   constexpr int kPer = kVecs * 4;     // elements of a thread's tile: 16 either way
+  static_assert(kPer == 16, "the maximum below");
   constexpr int kWords = kPer / kE;   // 16-byte words of it
   const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));  // elements before the row in its first word
   const T* base = x - shift;
@@ -228,10 +234,10 @@ __device__ __forceinline__ Stat row_pass(const T* x, int vocab, int k, int share
     }
     // the next tile's loads run while this one is folded in
     if (t + kTileWords < w1) fetch(t + kTileWords, word);
-    float mx[4];
+    float mx[5];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx[i] = max_nan(max_nan(v[4 * i], v[4 * i + 1]), max_nan(v[4 * i + 2], v[4 * i + 3]));
-    const float tm = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+    for (int i = 0; i < 5; ++i) mx[i] = max_nan(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+    const float tm = max_nan(max_nan(mx[0], mx[1], mx[2]), mx[3], max_nan(mx[4], v[15]));
     st.bad |= !(tm < INFINITY);
     if (tm > st.m) {
       const float d = st.m == -INFINITY ? 0.f : st.m - tm, e = expf(d);
@@ -243,9 +249,10 @@ __device__ __forceinline__ Stat row_pass(const T* x, int vocab, int k, int share
     float2 z = make_float2(0.f, 0.f), u = z;
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) {
-      // e^-200 is 0 in fp32: what lies lower (-inf, a mask's value) adds the same nothing
+      // e^-200 is 0 in fp32: what lies lower (-inf, a mask's value) adds the same
+      // nothing, but its d e would be a NaN
       float2 d = ffma2(make_float2(v[i], v[i + 1]), make_float2(1.f, 1.f), make_float2(-ref, -ref));
-      d = make_float2(fmaxf(d.x, -200.f), fmaxf(d.y, -200.f));
+      if (ENTROPY) d = make_float2(fmaxf(d.x, -200.f), fmaxf(d.y, -200.f));
       const float2 x2 = ffma2(d, make_float2(1.4426950408889634f, 1.4426950408889634f), make_float2(0.f, 0.f));
       const float2 e = make_float2(ex2(x2.x), ex2(x2.y));
       z = ffma2(e, make_float2(1.f, 1.f), z);
