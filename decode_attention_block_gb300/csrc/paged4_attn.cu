@@ -579,12 +579,28 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
   auto kern = k_paged4_token<QT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem4::kBytes);
   if (e != cudaSuccess) return e;
-  // no more CTAs than the tables' rows could give work to
-  const int64_t rows = (int64_t)p.max_pages * p.page_size, parts = (rows + kTile4 * kMinUnits4 - 1) / (kTile4 * kMinUnits4);
-  const int64_t most = (int64_t)p.n_seqs * p.n_kv * p.max_q * parts;
+  // CTAs for sqrt(2 U) parts a group of as many tiles U as the tables have room for
+  // (where a group has fewer, ctas_for takes fewer): with 456 always, parts that
+  // were fewer lay two on an SM beside SMs without (one sequence at 8000 18.8 us, now
+  // 16.7; at 32768 30.9 and 29.4).  sqrt(4 U), the limit of bf16 pages, 17.7 and
+  // 30.3; sqrt(U) 18.6 and 26.7.
+  int64_t tiles = ((int64_t)p.max_pages * p.page_size + kTile4 - 1) / kTile4;
+  if (p.window > 0 && tiles > p.window / kTile4 + 2) tiles = p.window / kTile4 + 2;
+  int64_t parts = tiles / kMinUnits4;
+  const int64_t cap = (int64_t)sqrt(2.0 * (double)tiles);
+  if (parts > cap) parts = cap;
+  if (parts < 1) parts = 1;
+  const int groups = p.n_seqs * p.n_kv;
   int grid = kCtas4 * device_sm_count();
   if (grid > paged::kMaxCtas) grid = paged::kMaxCtas;
-  if (grid > most) grid = (int)most;
+  // Where groups have parts for more, a whole number of CTAs each if that leaves an
+  // eighth of them at most: 16 sequences at 2000, 64 groups on 448 CTAs 18.9 us, cut
+  // by all 456 22.8.
+  const int whole = grid / groups * groups;
+  if (groups * parts <= grid)
+    grid = (int)(groups * parts);
+  else if ((grid - whole) * 8 <= grid)
+    grid = whole;
   return launch_pdl(kern, dim3(grid), dim3(kThreads4), Smem4::kBytes, st, static_cast<const unsigned char*>(k),
                     static_cast<const unsigned char*>(v), p);
 }
