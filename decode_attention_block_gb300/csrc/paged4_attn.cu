@@ -31,9 +31,9 @@
 // cache.  64 sequences at 512-32768 (1.2 GB of pages): 338 us with a producer
 // warp, 16-position tiles and 8 folding warps an SM, 288 with 12 (of 128
 // registers), 275 with 8 and 32-position tiles, 245 with loops over their blocks,
-// 223 as it is: 5.4 TB/s, 0.80 of the measured copy bandwidth.  A pair of warps a
-// tile, each half of the output's dims, took 268.  One sequence at 700: 11 us,
-// latency.
+// 229 as it is: 5.25 TB/s, 0.78 of the measured copy bandwidth (128 sequences at
+// 130000 0.87).  A pair of warps a tile, each half of the output's dims, took 268.  One
+// sequence at 700: 11 us, latency.
 #include <math.h>
 
 #include <type_traits>
