@@ -546,6 +546,45 @@ def test_long_sums_keep_their_bits(B, n_seqs, n, c, q_type):
     assert worst <= rel, f"{worst:.2g} of the output, bound {rel:.2g}"
 
 
+@pytest.mark.parametrize("n_seqs, n, c, q_type", [(480, 1, 40000, F32), (480, 1, 40000, BF16), (160, 8, 12000, F32), (80, 40, 12000, F32),
+                                                  (160, 8, 30000, BF16), (80, 40, 30000, BF16)])
+@pytest.mark.parametrize("rising", [True, False])
+def test_long_sums_under_maxima_that_move(B, n_seqs, n, c, q_type, rising):
+    """Scores that rise by some 24 over a third of a long sequence and stay there, or stay and fall: sums put aside under an
+    earlier maximum count for less, or for all."""
+    g, gen = _geom(B, 1, 512, 0.0625), torch.Generator("cuda").manual_seed(6)
+    page = 128
+    entries = torch.randperm(-(-c // page), generator=gen, device="cuda").int()
+    x = torch.arange(c, device="cuda", dtype=torch.float32)
+    ramp = (3.0 * x / c).clamp(max=1.0)
+    ramp = ramp if rising else ramp.flip(0)
+    way = torch.randn(D, generator=gen, device="cuda").sign()
+    keys = (way * ramp[:, None] + 0.05 * torch.randn(c, D, generator=gen, device="cuda"))[:, None]
+    pools, vals = [], []
+    for rows in (keys, torch.rand(c, 1, D, generator=gen, device="cuda")):
+        code, sc = fp4_ref.quantize(rows)
+        pool = torch.full((len(entries), page // 16, 1, fp4_ref.BLOCK), 0xFF, dtype=torch.uint8, device="cuda")
+        fp4_ref.write(pool, entries, page, torch.arange(c, device="cuda"), code, sc)
+        pools.append(pool)
+        vals.append(fp4_ref.values(code, sc)[:, 0])
+    q = (1.5 * way + 0.1 * torch.randn(n * 4, D, generator=gen, device="cuda")).to(q_type).reshape(n, 4 * D)
+    batch = B.PagedBatch(entries.repeat(n_seqs, 1).contiguous(), _i32([n * i for i in range(n_seqs + 1)]), _i32([c] * n_seqs), n_seqs * n, n)
+    a, ws = torch.zeros(n_seqs * n, 4 * D, device="cuda", dtype=q_type), B.make_paged_workspace(g)
+    B.spark_paged_attention(g, q.repeat(n_seqs, 1), B.PagePool(*pools), B.SPARK_FULL, batch, a, ws)
+    torch.cuda.synchronize()
+    assert B.spark_attn_error_word(ws) == 0
+    qd = q.double().view(n, 4, D)
+    z = 0.0625 * torch.einsum("thd,xd->thx", qd, vals[0])
+    late = torch.arange(c, device="cuda")[None] > torch.arange(c - n, c, device="cuda")[:, None]
+    want = torch.softmax(z.masked_fill(late[:, None], -np.inf), -1) @ vals[1]
+    ds = 0.0625 * (torch.einsum("thd,xd->thx", qd.abs(), vals[0].abs()) * (2.0 ** -22 + 2.0 ** -15) +
+                   2.0 ** -25 * qd.abs().amax(-1, keepdim=True) * vals[0].abs().sum(-1)).amax(-1, keepdim=True)
+    rel = 2 * ds + 2.0 ** -17 + (2.0 ** -22 + 2.0 ** -15 if q_type == F32 else 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -8)
+    err = ((a.double().view(n_seqs, n, 4, D) - want).abs() / want - 2.0 ** -25 * vals[1].sum(0) / want).clamp(min=0)
+    worst = (err / rel).max().item()
+    assert worst <= 1.0, f"error {worst:.2f} of its bound"
+
+
 def test_repeated_and_unordered_calls_agree(B):
     g = _geom(B)
     ws, runs = B.make_paged_workspace(g), []
