@@ -30,7 +30,7 @@ constexpr int kRowWarps = 4;      // of a CTA (9000 tokens of prompts in and out
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kWantedWarps = 32;  // an SM, before a token has a warp alone
 constexpr int kRowCtas = 6;       // CTAs an SM of the append (32 warps: 64 registers, spilled: 8 prompts no faster)
-constexpr int kBatch = 2;         // rows of a warp in flight, behind the two being rotated (1, 3, 4: 65, 63, 71 us)
+constexpr int kBatch = 2;         // rows of a warp in flight, behind the two being rotated (8 prompts: with 1 10 us more, with 3 as many)
 constexpr int kReadBatch = 8;
 // Tokens of a warp of a long read: 47000 rows 47.7 us with one, 41.5 with two, 43
 // with three, 47.5 with four (the writes spread), 10 CTAs an SM.
