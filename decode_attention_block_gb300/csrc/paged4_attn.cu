@@ -612,7 +612,7 @@ cudaError_t launch_paged4_attention(const paged::Args& p, int qdtype, const void
   // Pairs of CTAs or single ones by the rule of launch_paged_attention, for its
   // reasons (bf16 queries: 32 sequences of 33 tokens at 4096-8192 163 us on pairs,
   // 184 on single CTAs, a chunk of 4096 264 and 328; 4 tokens each 150 and 98, 32 of
-  // them 4 with chunks of ~400 tokens 155 and 135, fp32 queries 265 and 213).
+  // them 4 with chunks of ~400 tokens 155 and 135, fp32 queries 265 and 224).
   if (p.max_q > paged::kChunkTokens && (2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q || p.n_tokens > 128 * p.n_seqs))
     return launch_paged4_pair(p, qdtype, k, v, st);
   return launch_paged4_chunk(p, qdtype, k, v, st);

@@ -14,8 +14,8 @@
 // MMAs (192 KB; 384 with fp32 queries), 2560 cycles at 128 bytes a cycle against
 // 2048 of MMA, and the codes' loads go through the same pipe.  32 sequences at
 // 4096-8192 (0.23 GB), bf16 queries: 4 tokens each 98 us, 32 tokens 111 (bf16 pages,
-// 0.82 GB: 132 and 147); fp32 queries 156; a mixed batch of 32, 4 of them with
-// chunks of ~400 tokens, 134 and 211.  What it cost on the way (4 tokens each): half
+// 0.82 GB: 132 and 147); fp32 queries 164; a mixed batch of 32, 4 of them with
+// chunks of ~400 tokens, 134 and 224.  What it cost on the way (4 tokens each): half
 // lines of codes a load 15 more, scores kept in 240 registers a thread, the MMA
 // warp spilling, 4.
 #include "paged4_chunk_parts.cuh"

@@ -46,14 +46,15 @@ constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O
 // with fp32 queries (130000 positions in one share, fp32: 1.8e-4 of the output).
 // So over fp16 operands O is added to a sum in memory, in the group's part of the
 // workspace, every so many tiles.  bf16 outputs: 64, at most 2^-14 of a sum, for 1
-// to 2% of the time.  fp32 ones: 4, 1.3e-6 of the output at any length, where fp32
-// products of fp32 operands have 1e-6; a mixed batch of 32 takes 211 us for it, a
-// chunk of 4096 551 (8 tiles, 2.2e-6: 193 and 477; 16, 4e-6: 183 and 443; never: 183
-// and 410).  Done before a tile's probabilities, not behind them, it left the
-// MMAs idle: 237 us.  The remainders of fp32 queries are multiplied first, into
-// scores still small (1.5e-6 else).
-template <typename QT>
-constexpr int kFoldTiles = std::is_same<QT, float>::value ? 4 : 64;
+// to 2% of the time.  fp32 ones: 3, on pairs 4, 1.1e-6 of the output at any length,
+// where fp32 products of fp32 operands have 0.6e-6 to 1.6e-6 (2 tiles: 0.9e-6, 4:
+// 1.3e-6, 8: 2.2e-6, 16: 4e-6).  That costs a mixed batch of 32 224 us (2 tiles 249,
+// 4 212, 8 193, never 183), a chunk of 4096 547 (3 tiles 597, 8 477, never 410).
+// Done before a tile's probabilities, not behind them, it left the MMAs idle: 237 us
+// for 212.  The remainders of fp32 queries are multiplied first, into scores still
+// small (1.5e-6 for 1.3e-6).
+template <typename QT, int RANKS>
+constexpr int kFoldTiles = !std::is_same<QT, float>::value ? 64 : RANKS == 2 ? 4 : 3;
 constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
 
 // L2 policies of the pool's rows.  A sequence of one group reads its rows
@@ -354,7 +355,7 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
   uint32_t tile = 0;
   bool ok = true;
   constexpr bool kSplit = std::is_same<QT, float>::value, kConvert = kSplit || FP16;
-  constexpr int kFold = FP16 ? kFoldTiles<QT> : 0;
+  constexpr int kFold = FP16 ? kFoldTiles<QT, RANKS> : 0;
   constexpr int kAll = RANKS * kRows;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, flags, kWaitLimitNs));
