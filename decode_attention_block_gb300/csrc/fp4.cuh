@@ -90,6 +90,14 @@ __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*re
 // x, or what its fp16 leaves of it
 __device__ __forceinline__ float split_part(float x, bool lo) { return lo ? x - __half2float(__float2half_rn(x)) : x; }
 
+// Where a row's probabilities lie in fp16's range: e^(s - ref) with the largest
+// score kBelow above ref (base 2) when ref is set, and ref raised once a score
+// passes it by kMost, so that none passes 2^15.  Half of fp16's smallest step then
+// is 2^-36 of the row's largest or less.  (With ref the maximum itself, a dominant
+// key and 131071 others 17.4 nats below it: all of their weight was lost, 3.6e-3
+// of the row's.)
+constexpr float kBelow = 11.f, kMost = 15.f;
+
 // The power of two that takes values of largest magnitude m into [1, 2), and
 // its inverse: 1 where m is infinite, NaN or below the smallest normal number.
 __device__ __forceinline__ float2 unit_of(float m) {

@@ -19,8 +19,9 @@
 // the conversion: four operations for 16 elements.
 //
 // Queries are scaled by a power of two into fp16's range; scores take it back
-// in fp32.  The running maximum is raised once a score passes it by 2^8 (as in
-// the chunk kernels): most tiles cost one vote for it.
+// in fp32.  Probabilities are relative to a reference below the running maximum
+// (fp4::kBelow), raised once a score passes it by 2^15 (as in the chunk kernels):
+// most tiles cost one vote for it.
 //
 // With a quarter of the bytes of bf16 pages the instructions count: a tile costs
 // a warp some 1200, 256 conversions and 256 products among them, each two cycles
@@ -65,7 +66,6 @@ constexpr int kMinUnits4 = 4;    // tiles per CTA at least: one per warp
 constexpr int kFoldTiles4 = 64;
 constexpr int kPad = 4;          // floats behind each 32 of a state in shared memory
 constexpr int kPRow = kTile4 + 4;  // floats of a head's scores of a tile, and a shift of banks
-constexpr float kRaise4 = 8.0f;
 constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
 
 // The walk over the groups waits in shared memory, a copy for each warp, while
@@ -191,13 +191,13 @@ struct Places {
 __device__ __forceinline__ uint32_t scale2(uint32_t w, int i) { return __byte_perm(w, 0u, 0x4040u | (uint32_t)(i | (i << 8))) << 7; }
 
 // One warp's running state: o[i] holds dims 32 g + 2 i in [0], [1], the next in
-// [2], [3], of columns 2 t and 2 t + 1; m the maxima (base 2) of the columns'
+// [2], [3], of columns 2 t and 2 t + 1; m the references (base 2) of the columns'
 // heads 2 (t & 1) + j, mg of head g & 3, l the sum of head g & 3 over positions 4
 // t .. 4 t + 3 of every block.
 struct State4 {
   float o[kHeadDim / 16][4];
   float m[2], mg, l;
-  float m_sum[2];  // maxima of the sum in memory, -inf while there is none
+  float m_sum[2];  // references of the sum in memory, -inf while there is none
   __device__ __forceinline__ void reset() {
     clear();
     m[0] = m[1] = mg = m_sum[0] = m_sum[1] = -INFINITY;
@@ -207,7 +207,7 @@ struct State4 {
 #pragma unroll
     for (int i = 0; i < kHeadDim / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
-  // o += the lane's part of the sum in memory, under the maxima of now
+  // o += the lane's part of the sum in memory, under the references of now
   __device__ __forceinline__ void add(const float4* sum) {
     float f[2];
 #pragma unroll
@@ -291,14 +291,14 @@ __device__ __forceinline__ void fold_keys(uint32_t kst, int r0, int r1, const Qu
 __device__ __forceinline__ void fold_values(uint32_t vst, int r0, int r1, const Places& at, uint32_t p_w, float (&mx)[2], State4& st) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool whole = r0 == 0 && r1 == kTile4;
-  if (__any_sync(0xffffffffu, mx[0] > st.m[0] + kRaise4 || mx[1] > st.m[1] + kRaise4)) {
+  if (__any_sync(0xffffffffu, mx[0] > st.m[0] + fp4::kMost || mx[1] > st.m[1] + fp4::kMost)) {
     float corr[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-      const float mn = fmaxf(st.m[j], mx[j]);
+      const float mn = fmaxf(st.m[j], mx[j] - fp4::kBelow);
       corr[j] = st.m[j] == -INFINITY ? 0.f : exp2f(st.m[j] - mn);
       st.m[j] = mn;
     }
@@ -333,7 +333,7 @@ __device__ __forceinline__ void fold_values(uint32_t vst, int r0, int r1, const 
     }
     // B fragments of [p_hi | p_lo]^T: the MMA's steps 2 t, 2 t + 1, 2 t + 8, 2 t +
     // 9 are positions 4 t .. 4 t + 3 (a masked one's probability is 0, also
-    // under a maximum of -inf)
+    // under a reference of -inf)
     const uint4 s4 = lds128(p_w + 4 * ((g & 3) * kPRow + 16 * blk + 4 * t));
     const float4 p4 = make_float4(ex2(__uint_as_float(s4.x) - ref), ex2(__uint_as_float(s4.y) - ref),
                                   ex2(__uint_as_float(s4.z) - ref), ex2(__uint_as_float(s4.w) - ref));

@@ -55,7 +55,13 @@ constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O
 // small (1.5e-6 for 1.3e-6).
 template <typename QT, int RANKS>
 constexpr int kFoldTiles = !std::is_same<QT, float>::value ? 64 : RANKS == 2 ? 4 : 3;
-constexpr float kRaise = 8.0f;                  // m is raised once a score passes it by 2^8
+// The running state's m: the row's maximum, raised once a score passes it by 2^8
+// (bf16 probabilities have fp32's exponents); with fp16 ones it lies below the
+// maximum (fp4::kBelow).
+template <bool FP16>
+constexpr float kRaise = FP16 ? fp4::kMost : 8.0f;
+template <bool FP16>
+constexpr float kBelowMax = FP16 ? fp4::kBelow : 0.0f;
 
 // L2 policies of the pool's rows.  A sequence of one group reads its rows
 // once: they make room first, or they would drive out the rows of longer
@@ -492,9 +498,9 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         mt = mt == -INFINITY || tok >= g.n_tok ? -INFINITY : mt * scale;
         if (u == t0) {
-          m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + kRaise)) {
-          const float mn = fmaxf(m, mt);
+          m = mt - kBelowMax<FP16>;
+        } else if (__any_sync(0xffffffffu, mt > m + kRaise<FP16>)) {
+          const float mn = fmaxf(m, mt - kBelowMax<FP16>);
           const float corr = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;
           l *= corr;

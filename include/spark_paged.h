@@ -165,9 +165,10 @@ int spark_paged_read(const spark_geom* g, const spark_page_pool* pool, const spa
  * bf16 (8 bits) where it is more.  An fp32 pool is read by fp32 arithmetic.
  * 4-bit pages are met in fp16, queries scaled by a power of two for each token
  * and head: fp32 ones as q = hi + lo (22 bits of the token's and head's
- * largest element), bf16 ones as they are (elements below 2^-23 of the
- * largest lose bits); probabilities as hi + lo, but rounded to fp16 (11 bits)
- * for bf16 queries where max_q_len is more than 1.  Outputs are summed in
+ * largest element), bf16 ones as they are (elements below 2^-17 of the
+ * largest lose bits); probabilities as hi + lo (22 bits), but rounded to fp16
+ * (11 bits) for bf16 queries where max_q_len is more than 1, and in steps of
+ * 2^-35 of the row's largest at the least.  Outputs are summed in
  * fp32; what the matrix instructions cut off a sum stays below 2^-16 of it for
  * fp32 queries and 2^-14 for bf16 ones, however long the sequence.
  * Rows that no token of the sequence attends to may hold anything, NaN
