@@ -59,11 +59,15 @@ constexpr int kTile4 = kTileBlocks * fp4::kRows;  // positions of a tile
 constexpr int kCtas4 = 3;        // CTAs per SM
 constexpr int kSlots4 = 3;       // halves of tiles (K or V) a warp has room for
 constexpr int kMinUnits4 = 4;    // tiles per CTA at least: one per warp
-// Tiles of a warp after which its output is added to a sum in memory: the MMAs cut
-// a sum off below its last bit, up to 2^-23 of it a step, two steps a tile (128
-// sequences at 130000, fp32 queries, 32000 positions a warp: 2.5e-5 of the output,
-// so 1.6e-6, for 3280 us instead of 3260).
-constexpr int kFoldTiles4 = 64;
+// Tiles of a warp after which its output (of fp32 queries the probabilities' sum
+// too) is added to a sum in memory: the MMAs cut off towards zero, of a sum what lies
+// 2^-23 below it a step of 16 positions, of a product 2^-25 (paged_chunk_parts.cuh:
+// kFoldTiles).  fp32 queries: at most 1.25 * 2^-15 of the output.  Beside one dominant
+// position 2.0e-5 of it (64 tiles 3.8e-5, 16 1.3e-5); values alike, 32000 positions a
+// warp, never 2.5e-5, 64 tiles 1.6e-6.  128 sequences at 130000: 3340 us, 64 tiles
+// 3310, 16 3400.
+template <typename QT>
+constexpr int kFoldTiles4 = std::is_same<QT, float>::value ? 32 : 64;
 constexpr int kPad = 4;          // floats behind each 32 of a state in shared memory
 constexpr int kPRow = kTile4 + 4;  // floats of a head's scores of a tile, and a shift of banks
 constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
@@ -207,8 +211,12 @@ struct State4 {
 #pragma unroll
     for (int i = 0; i < kHeadDim / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
-  // o += the lane's part of the sum in memory, under the references of now
-  __device__ __forceinline__ void add(const float4* sum) {
+  // o and (L) l += the lane's part of the sums in memory, under the references of now
+  template <bool L>
+  __device__ __forceinline__ void add(const float* sums, int lane) {
+    const float4* sum = reinterpret_cast<const float4*>(sums) + lane;
+    const float* sum_l = sums + 8 * kHeadDim + lane;
+    if (L && sum_l[32] != -INFINITY) l = fmaf(sum_l[0], ex2(sum_l[32] - mg), l);
     float f[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) f[j] = m_sum[j] == -INFINITY ? 0.f : ex2(m_sum[j] - m[j]);
@@ -221,7 +229,15 @@ struct State4 {
       o[i][3] = fmaf(f[1], x.w, o[i][3]);
     }
   }
-  __device__ __forceinline__ void put(float4* sum) {
+  template <bool L>
+  __device__ __forceinline__ void put(float* sums, int lane) {
+    float4* sum = reinterpret_cast<float4*>(sums) + lane;
+    float* sum_l = sums + 8 * kHeadDim + lane;
+    if (L) {
+      sum_l[0] = l;
+      sum_l[32] = mg;
+      l = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < kHeadDim / 16; ++i) sum[32 * i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
     m_sum[0] = m[0];
@@ -493,9 +509,10 @@ __global__ void __launch_bounds__(kThreads4, kCtas4)
   int skip = warp;  // the CTA's tiles before the warp's next one
   Queries Q;
   State4 st;
-  auto sum = [&] {
-    return reinterpret_cast<float4*>(p.part + paged::kTokenPartBytes / sizeof(float) +
-                                     (int64_t)(c * kConsumers + warp) * paged::kWarpSums) + lane;
+  constexpr int kFold = kFoldTiles4<QT>;
+  constexpr bool kFoldL = std::is_same<QT, float>::value;
+  auto sums = [&] {
+    return p.part + paged::kTokenPartBytes / sizeof(float) + (int64_t)(c * kConsumers + warp) * paged::kWarpSums;
   };
   bool ok = true;
   for (;;) {
@@ -531,9 +548,9 @@ __global__ void __launch_bounds__(kThreads4, kCtas4)
     };
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i, pos += kConsumers * kTile4) {
-      if (i % kFoldTiles4 == 0 && i > 0) {
-        if (i > kFoldTiles4) st.add(sum());
-        st.put(sum());
+      if (i % kFold == 0 && i > 0) {
+        if (i > kFold) st.add<kFoldL>(sums(), lane);
+        st.put<kFoldL>(sums(), lane);
       }
       const int r0 = lo > pos ? lo - pos : 0, r1 = hi + 1 - pos < kTile4 ? hi + 1 - pos : kTile4;
       float mx[2];
@@ -556,7 +573,7 @@ __global__ void __launch_bounds__(kThreads4, kCtas4)
         in.advance();
       }
     }
-    if (ok && tiles > kFoldTiles4) st.add(sum());
+    if (ok && tiles > kFold) st.add<kFoldL>(sums(), lane);
     // the warps' states lie in a slot of each: the slots are all free now
     const MergeSmem msm{reinterpret_cast<float*>(base + S::kM), reinterpret_cast<float*>(base + S::kL),
                         reinterpret_cast<float*>(base)};

@@ -41,18 +41,21 @@ template <int LINES>  // of a slot
 constexpr uint32_t kGroupBytes = LINES * kAtom;
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 256;                 // first column of S buffer 0; O starts at 0
-// The MMAs cut each sum in O off below its last bit instead of rounding it: a
-// step takes up to 2^-23 of a sum, always towards zero, and a tile is 8 steps, 16
-// with fp32 queries (130000 positions in one share, fp32: 1.8e-4 of the output).
-// So over fp16 operands O is added to a sum in memory, in the group's part of the
-// workspace, every so many tiles.  bf16 outputs: 64, at most 2^-14 of a sum, for 1
-// to 2% of the time.  fp32 ones: 3, on pairs 4, 1.1e-6 of the output at any length,
-// where fp32 products of fp32 operands have 0.6e-6 to 1.6e-6 (2 tiles: 0.9e-6, 4:
-// 1.3e-6, 8: 2.2e-6, 16: 4e-6).  That costs a mixed batch of 32 224 us (2 tiles 249,
-// 4 212, 8 193, never 183), a chunk of 4096 547 (3 tiles 597, 8 477, never 410).
-// Done before a tile's probabilities, not behind them, it left the MMAs idle: 237 us
-// for 212.  The remainders of fp32 queries are multiplied first, into scores still
-// small (1.5e-6 for 1.3e-6).
+// The MMAs cut sums in O off instead of rounding them, always towards zero: a step
+// takes up to 2^-23 of a sum, and up to 2^-25 of it of each product (what 512 to
+// 8192 small products beside a large one lose fits this); a tile is 8 steps, 16
+// with fp32 queries (130000 positions alike in one share, fp32: 1.8e-4 of the
+// output).  So over fp16 operands O is added to a sum in memory, in the group's
+// part of the workspace, every so many tiles.  bf16 outputs: 64, at most 1.25 *
+// 2^-12 of a sum, for 1 to 2% of the time.  fp32 ones: 3, on pairs 4: at most 1.25 *
+// 2^-15, 1.1e-5 of the output beside one dominant position, 1.1e-6 at any length
+// where values and scores are alike; there fp32 products of fp32 operands have
+// 0.6e-6 to 1.6e-6 (2 tiles: 0.9e-6, 4: 1.3e-6, 8: 2.2e-6, 16: 4e-6).  A mixed batch
+// of 32 takes 226 us, a chunk of 4096 555; 1 us and 6 of that is the sum of the
+// probabilities that goes along (without it: mixed 2 tiles 249, 4 212, 8 193, never
+// 183; chunk 3 tiles 597, 8 477, never 410).  Done before a tile's probabilities, not
+// behind them, it left the MMAs idle: 237 us for 212.  The remainders of fp32 queries
+// are multiplied first, into scores still small (1.5e-6 for 1.3e-6).
 template <typename QT, int RANKS>
 constexpr int kFoldTiles = !std::is_same<QT, float>::value ? 64 : RANKS == 2 ? 4 : 3;
 // The running state's m: the row's maximum, raised once a score passes it by 2^8
@@ -396,13 +399,31 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
     float m = -INFINITY, l = 0.f;
     bool folded = false;
     float m_sum = -INFINITY;  // of the sums in memory
-    // O and those so far into memory and O cleared, or (end) into O; they are the
-    // row's part of the group's partial state, free until the group ends
+    // O and those so far into memory and O cleared, or (end) into O, of fp32 queries l
+    // too; they are the row's part of the group's partial state, free until the group ends
     auto fold = [&](bool end) {
       constexpr int kAhead = 4;  // pieces of 16 dims asked for ahead of their use
-      float4* sums = reinterpret_cast<float4*>(p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) *
-                                                            (RANKS * paged::kChunkPart)) + prow;
+      float* state = p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) * (RANKS * paged::kChunkPart);
+      float4* sums = reinterpret_cast<float4*>(state) + prow;
       const float old = m_sum == -INFINITY ? 0.f : ex2(m_sum - m);
+      if constexpr (kSplit) {
+        // (with what l's sum leaves, in place of the maximum: beside one large
+        // probability the small ones of a tile would be rounded to its steps)
+        float* sum_l = state + kAll * kHeadDim + prow;
+        float rest = 0.f;
+        if (folded) {
+          const float x = old * sum_l[kAll], s = __fadd_rn(x, l), y = __fsub_rn(s, x);
+          rest = __fmaf_rn(old, sum_l[0], __fadd_rn(__fsub_rn(x, __fsub_rn(s, y)), __fsub_rn(l, y)));
+          l = s;
+        }
+        if (end) {
+          l += rest;
+        } else {
+          sum_l[0] = rest;
+          sum_l[kAll] = l;
+          l = 0.f;
+        }
+      }
       float4 x[kAhead][4];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
@@ -553,8 +574,8 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
       const int64_t r = cur.seq.q0 + g.tok + tok;
       float* part = p.part + (int64_t)paged::partial_slot(c, cur.begin, total, G) * (RANKS * paged::kChunkPart);
       QT* dst = out + ((r * p.n_kv + cur.j) * kGroup + (row & 3)) * kHeadDim;
-      const float inv = 1.0f / l;
       if (kFold > 0 && folded) fold(true);
+      const float inv = 1.0f / l;
       // A partial state is [dims / 4][row][4], then the maxima and the sums: the
       // lanes' rows lie next to one another (row by row, 32 lines of 128 bytes
       // per store, the output took 10000 cycles a group).

@@ -17,9 +17,10 @@ constexpr int kChunkTokens = 32;
 constexpr int kMaxChunkCtas = 160;
 constexpr int kChunkPart = kGroup * kChunkTokens * (kHeadDim + 2);
 // bytes of the partial states of either kernel; behind the token kernel's what a
-// warp over 4-bit pages sums up beside its registers (4 warps a CTA, 8 rows)
+// warp over 4-bit pages sums up beside its registers (4 warps a CTA, 8 rows, two
+// values a lane)
 constexpr size_t kTokenPartBytes = sizeof(float) * 2 * kMaxCtas * kPartFloats;
-constexpr int kWarpSums = 8 * kHeadDim;
+constexpr int kWarpSums = 8 * kHeadDim + 64;
 constexpr size_t kChunkPartBytes = sizeof(float) * 2 * kMaxChunkCtas * kChunkPart;
 constexpr size_t kPartBytes = kTokenPartBytes > kChunkPartBytes ? kTokenPartBytes : kChunkPartBytes;
 static_assert(kTokenPartBytes % 16 == 0 && kTokenPartBytes + sizeof(float) * 4 * kMaxCtas * kWarpSums <= kPartBytes, "room for both");

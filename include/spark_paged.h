@@ -169,8 +169,9 @@ int spark_paged_read(const spark_geom* g, const spark_page_pool* pool, const spa
  * largest lose bits); probabilities as hi + lo (22 bits), but rounded to fp16
  * (11 bits) for bf16 queries where max_q_len is more than 1, and in steps of
  * 2^-35 of the row's largest at the least.  Outputs are summed in
- * fp32; what the matrix instructions cut off a sum stays below 2^-16 of it for
- * fp32 queries and 2^-14 for bf16 ones, however long the sequence.
+ * fp32; what the matrix instructions cut off a sum stays below 2^-14 of the sum
+ * of its magnitudes for fp32 queries and 2^-11 for bf16 ones, however long the
+ * sequence and whatever the order of large and small terms.
  * Rows that no token of the sequence attends to may hold anything, NaN
  * included; a row that one of its new tokens attends to is expected finite
  * (a non-finite V row may reach every new token of its sequence).
