@@ -82,10 +82,12 @@ int spark_paged_rope_append(const spark_geom* g, const void* q, const void* k, c
     if ((s = check_rows(q_out, dtype, q_out_ld, q_width)) != SPARK_OK) return s;
     // rows are read while others are written, but a row rotated in place
     const RowSpan out(q_out, dtype, q_out_ld, q_width, batch->n_tokens);
-    const bool in_place = q_out == q && q_out_ld == ld;
-    if (!in_place && out.meets(RowSpan(q, dtype, ld, q_width, batch->n_tokens))) return SPARK_ERR_INVALID_ARG;
-    const RowSpan ks(k, dtype, ld, kv_width, batch->n_tokens), vs(v, dtype, ld, kv_width, batch->n_tokens);
-    if (in_place ? out.meets_rows(ks) || out.meets_rows(vs) : out.meets(ks) || out.meets(vs)) return SPARK_ERR_INVALID_ARG;
+    const bool alike = q_out_ld == ld, in_place = q_out == q && alike;
+    auto hits = [&](const void* p, int64_t width) {
+      const RowSpan rows(p, dtype, ld, width, batch->n_tokens);
+      return alike ? out.meets_rows(rows) : out.meets(rows);
+    };
+    if ((!in_place && hits(q, q_width)) || hits(k, kv_width) || hits(v, kv_width)) return SPARK_ERR_INVALID_ARG;
   }
   if ((s = check_paged_ws(workspace, workspace_bytes)) != SPARK_OK) return s;
   const paged::Args p = paged_args(g, pool, SPARK_FULL, batch, workspace);

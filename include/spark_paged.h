@@ -129,7 +129,8 @@ int spark_rope_table(const spark_geom* g, int32_t layer_class, int32_t n_positio
  *   q_out   rows [n_q * head_dim] of the same type, row t at element
  *           t * q_out_ld: the rotated queries of the tokens that belong to a
  *           sequence, other rows are left as they were.  It is q itself with
- *           q_out_ld == ld (in place), or overlaps neither q, k nor v.
+ *           q_out_ld == ld (in place), or overlaps no row of q, k or v (with
+ *           another q_out_ld, nothing from their first row to their last).
  *   rope    the class's table (spark_rope_table), n_positions long.
  * A token's position is that of its cache row (seq_len, a device value: a
  * captured call replays for the next token).  One at or behind n_positions
