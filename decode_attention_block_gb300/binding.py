@@ -939,7 +939,12 @@ class BeamState(_CachedC):
 def spark_beam_reorder(parent: torch.Tensor, keep_len, new_len, states, ws: torch.Tensor, stream=None) -> None:
     """Rows of every BeamState to their new slots (spark_beam_select's parent,
     keep_len and new_len; the lengths may be None without ``positions``)."""
-    of, device = parent.shape, _current_device()
+    device = _current_device()
+    if not isinstance(parent, torch.Tensor):
+        raise _not_here(parent, "parent")
+    of = parent.shape
+    if len(of) != 1:
+        raise ValueError("parent must be a list, one slot each")
     built = [st._c or st.to_c() for st in states]
     for st, b in zip(states, built):
         if b[1] != (of[0], device):
