@@ -56,7 +56,8 @@ size_t spark_beam_workspace_bytes(int32_t n_groups, int32_t n_beams);
  * a score of +inf or NaN neither, nor what would have a score below fp32's
  * range.
  * Sums are fp32, the scores are compared in 64 bits and rounded to fp32 once.
- * new_score may be score, new_done done and new_len length.
+ * new_score may be score, new_done done and new_len length; otherwise no output
+ * overlaps another array of the call (this is not checked).
  * n_beams: 1 .. SPARK_MAX_BEAMS; n_groups * n_beams: 1 .. SPARK_MAX_BATCH;
  * vocab: 1 .. 2^24.
  * Errors: INVALID_ARG, WORKSPACE before any work is enqueued; CUDA if a

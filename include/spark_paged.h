@@ -103,7 +103,8 @@ size_t spark_paged_workspace_bytes(const spark_geom* g);
  *            rows do; ld >= n_kv * head_dim, rows 16-byte aligned).
  *   workspace >= spark_paged_workspace_bytes, 256-byte aligned.
  * Two new tokens of one call in the same page row (tables that share a page
- * that both write) leave either's values there.
+ * that both write) leave either's values there (SPARK_FP4: codes of one may
+ * meet the scale of the other).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE before any work is enqueued;
  * CUDA if a launch fails. */
 int spark_paged_append(const spark_geom* g, const void* k, const void* v, int64_t ld, int32_t dtype,
