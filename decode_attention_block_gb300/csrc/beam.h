@@ -47,7 +47,6 @@ struct Select {
   int eos;
   float* new_score;
   int32_t *token, *parent, *new_done, *keep_len, *new_len;
-  uint32_t* err;
   uint32_t* tickets;
   Part* part;
 };

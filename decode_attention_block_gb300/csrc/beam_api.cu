@@ -43,8 +43,7 @@ int spark_beam_select(const void* logits, int64_t ld, int32_t dtype, int32_t n_g
   const int s = check_beam_ws(workspace, workspace_bytes);
   if (s != SPARK_OK) return s;
   beam::Select a = {logits, ld, n_groups, n_beams, vocab, score, done, length, eos, new_score, token, parent, new_done,
-                    keep_len, new_len, nullptr, nullptr, nullptr};
-  a.err = ws_at<uint32_t>(workspace, 0);
+                    keep_len, new_len, nullptr, nullptr};
   a.tickets = ws_at<uint32_t>(workspace, beam::kTickets);
   a.part = ws_at<beam::Part>(workspace, beam::kParts);
   return cuda_status(launch_beam_select(a, dtype, (cudaStream_t)stream));
