@@ -97,6 +97,9 @@ __device__ __forceinline__ float split_part(float x, bool lo) { return lo ? x - 
 // key and 131071 others 17.4 nats below it: all of their weight was lost, 3.6e-3
 // of the row's.)
 constexpr float kBelow = 11.f, kMost = 15.f;
+// (rounded so that no score lies further above, whatever fp32's steps of them)
+__device__ __forceinline__ float below(float top) { return __fsub_ru(top, kBelow); }
+__device__ __forceinline__ bool past(float top, float ref) { return top > __fadd_rd(ref, kMost); }
 
 // The power of two that takes values of largest magnitude m into [1, 2), and
 // its inverse: 1 where m is infinite, NaN or below the smallest normal number.

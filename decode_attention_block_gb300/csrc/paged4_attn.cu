@@ -307,14 +307,14 @@ __device__ __forceinline__ void fold_keys(uint32_t kst, int r0, int r1, const Qu
 __device__ __forceinline__ void fold_values(uint32_t vst, int r0, int r1, const Places& at, uint32_t p_w, float (&mx)[2], State4& st) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool whole = r0 == 0 && r1 == kTile4;
-  if (__any_sync(0xffffffffu, mx[0] > st.m[0] + fp4::kMost || mx[1] > st.m[1] + fp4::kMost)) {
+  if (__any_sync(0xffffffffu, fp4::past(mx[0], st.m[0]) || fp4::past(mx[1], st.m[1]))) {
     float corr[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
       mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-      const float mn = fmaxf(st.m[j], mx[j] - fp4::kBelow);
+      const float mn = fmaxf(st.m[j], fp4::below(mx[j]));
       corr[j] = st.m[j] == -INFINITY ? 0.f : exp2f(st.m[j] - mn);
       st.m[j] = mn;
     }

@@ -60,11 +60,14 @@ template <typename QT, int RANKS>
 constexpr int kFoldTiles = !std::is_same<QT, float>::value ? 64 : RANKS == 2 ? 4 : 3;
 // The running state's m: the row's maximum, raised once a score passes it by 2^8
 // (bf16 probabilities have fp32's exponents); with fp16 ones it lies below the
-// maximum (fp4::kBelow).
+// maximum (fp4::kBelow).  scale s - m is rounded once, from the exact product, where
+// the maximum's own was rounded to fp32: half a step of it (8 from 2^27 on) lies
+// between them, so fp16 ones hold for scores below 2^28.
+constexpr float kRaise = 8.0f;
 template <bool FP16>
-constexpr float kRaise = FP16 ? fp4::kMost : 8.0f;
+__device__ __forceinline__ float reference(float top) { return FP16 ? fp4::below(top) : top; }
 template <bool FP16>
-constexpr float kBelowMax = FP16 ? fp4::kBelow : 0.0f;
+__device__ __forceinline__ bool past(float top, float m) { return FP16 ? fp4::past(top, m) : top > m + kRaise; }
 
 // L2 policies of the pool's rows.  A sequence of one group reads its rows
 // once: they make room first, or they would drive out the rows of longer
@@ -519,9 +522,9 @@ __device__ __forceinline__ void softmax_warps(const Args& p, const Shape& sh, Cu
         float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         mt = mt == -INFINITY || tok >= g.n_tok ? -INFINITY : mt * scale;
         if (u == t0) {
-          m = mt - kBelowMax<FP16>;
-        } else if (__any_sync(0xffffffffu, mt > m + kRaise<FP16>)) {
-          const float mn = fmaxf(m, mt - kBelowMax<FP16>);
+          m = reference<FP16>(mt);
+        } else if (__any_sync(0xffffffffu, past<FP16>(mt, m))) {
+          const float mn = fmaxf(m, reference<FP16>(mt));
           const float corr = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;
           l *= corr;

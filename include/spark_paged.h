@@ -170,7 +170,8 @@ int spark_paged_read(const spark_geom* g, const spark_page_pool* pool, const spa
  * largest element), bf16 ones as they are (elements below 2^-17 of the
  * largest lose bits); probabilities as hi + lo (22 bits), but rounded to fp16
  * (11 bits) for bf16 queries where max_q_len is more than 1, and in steps of
- * 2^-35 of the row's largest at the least.  Outputs are summed in
+ * 2^-35 of the row's largest at the least.  With max_q_len above 1 scores are
+ * expected below 2^27.  Outputs are summed in
  * fp32; what the matrix instructions cut off a sum stays below 2^-14 of the sum
  * of its magnitudes for fp32 queries and 2^-11 for bf16 ones, however long the
  * sequence and whatever the order of large and small terms.

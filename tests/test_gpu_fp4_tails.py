@@ -93,3 +93,28 @@ def test_a_dominant_key_leaves_the_others_their_weight(B, n_seqs, n, q_type, c, 
     sel = torch.arange(n_seqs, device="cuda") % some
     worst = ((a.double().view(n_seqs, n, 4, D) - want[sel]).abs() / bound[sel]).max().item()
     assert worst <= 1.0, f"error {worst:.2f} of its bound"
+
+
+@pytest.mark.parametrize("n_seqs, n, log2", [(s, n, x) for s, n in ((480, 1), (160, 8), (80, 40), (3, 1), (3, 40))
+                                             for x in (20, 23, 24, 25, 25.6, 26, 26.6, 27, 27.5, 28, 29, 35, 60) if n == 1 or x < 28])
+@pytest.mark.parametrize("q_type", [F32, BF16])
+def test_large_scores_leave_probabilities_in_range(B, n_seqs, n, log2, q_type):
+    """A key whose scores are far above all others', where fp32's steps of a score pass 1 and 16 (chunks: up to 2^28, to
+    base 2): its value, whatever a maximum and what is subtracted from it are rounded to.  Its probability over the sum of
+    all is 1, and at least 2^-8: two halves off by 2^-25 are off by 2^-17 of it, one by 2^-11."""
+    g, gen, page, c = _geom(B, 1, 512, SCALE), torch.Generator("cuda").manual_seed(10), 64, 700
+    entries = torch.randperm(-(-c // page), generator=gen, device="cuda").int()
+    keys, rows = torch.zeros(c, 1, D, device="cuda"), torch.rand(c, 1, D, generator=gen, device="cuda")
+    keys[:, :, 0], keys[300, :, 0], rows[300] = 4.0, 6.0, 1.5
+    (pk, _), (pv, v) = _pool(keys, entries, page), _pool(rows, entries, page)
+    # fp32 queries: numbers of all 24 bits, so that products are rounded
+    top = 2.0 ** log2 / (SCALE * 6.0 * 1.4426950408889634) * (1.0 + 0.25 * torch.rand(n_seqs * n, 4, generator=gen, device="cuda"))
+    q = torch.zeros(n_seqs * n, 4, D, device="cuda")
+    q[..., 0] = top
+    q = q.to(q_type).reshape(n_seqs * n, 4 * D)
+    batch = B.PagedBatch(entries.repeat(n_seqs, 1).contiguous(), _i32([n * i for i in range(n_seqs + 1)]), _i32([c] * n_seqs), n_seqs * n, n)
+    a, ws = torch.zeros(n_seqs * n, 4 * D, device="cuda", dtype=q_type), B.make_paged_workspace(g)
+    B.spark_paged_attention(g, q, B.PagePool(pk, pv), B.SPARK_FULL, batch, a, ws)
+    assert B.spark_attn_error_word(ws) == 0
+    err = (a.double().view(-1, 4, D) - v[300]).abs()
+    assert bool((err <= v[300] * (U[q_type] + (2.0 ** -11 if q_type == BF16 else 2.0 ** -16))).all()), err.max().item()
