@@ -32,7 +32,7 @@
 // cache.  64 sequences at 512-32768 (1.2 GB of pages): 338 us with a producer
 // warp, 16-position tiles and 8 folding warps an SM, 288 with 12 (of 128
 // registers), 275 with 8 and 32-position tiles, 245 with loops over their blocks,
-// 229 as it is: 5.25 TB/s, 0.78 of the measured copy bandwidth (128 sequences at
+// 230 as it is: 5.24 TB/s, 0.78 of the measured copy bandwidth (128 sequences at
 // 130000 0.87).  A pair of warps a tile, each half of the output's dims, took 268.  One
 // sequence at 700: 11 us, latency.
 #include <math.h>
@@ -600,7 +600,8 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
   // (where a group has fewer, ctas_for takes fewer): with 456 always, parts that
   // were fewer lay two on an SM beside SMs without (one sequence at 8000 18.8 us, now
   // 16.7; at 32768 30.9 and 29.4).  sqrt(4 U), the limit of bf16 pages, 17.7 and
-  // 30.3; sqrt(U) 18.6 and 26.7.
+  // 30.3; sqrt(U) 18.6 and 26.7.  These tables were as wide as the sequence; with room
+  // for 131072 positions 20.3 and 31.6.
   int64_t tiles = ((int64_t)p.max_pages * p.page_size + kTile4 - 1) / kTile4;
   if (p.window > 0 && tiles > p.window / kTile4 + 2) tiles = p.window / kTile4 + 2;
   int64_t parts = tiles / kMinUnits4;
@@ -627,7 +628,7 @@ cudaError_t launch_token4(const Args& p, const void* k, const void* v, cudaStrea
 cudaError_t launch_paged4_attention(const paged::Args& p, int qdtype, const void* k, const void* v, cudaStream_t st) {
   if (p.max_q == 1) return qdtype == SPARK_BF16 ? launch_token4<__nv_bfloat16>(p, k, v, st) : launch_token4<float>(p, k, v, st);
   // Pairs of CTAs or single ones by the rule of launch_paged_attention, for its
-  // reasons (bf16 queries: 32 sequences of 33 tokens at 4096-8192 163 us on pairs,
+  // reasons (bf16 queries: 32 sequences of 33 tokens at 4096-8192 165 us on pairs,
   // 184 on single CTAs, a chunk of 4096 264 and 328; 4 tokens each 150 and 98, 32 of
   // them 4 with chunks of ~400 tokens 155 and 135, fp32 queries 265 and 224).
   if (p.max_q > paged::kChunkTokens && (2 * (int64_t)p.n_tokens > (int64_t)p.n_seqs * p.max_q || p.n_tokens > 128 * p.n_seqs))

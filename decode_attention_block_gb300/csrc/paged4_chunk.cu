@@ -13,11 +13,13 @@
 // Bound by shared memory: a tile's operands are written (128 KB) and read by the
 // MMAs (192 KB; 384 with fp32 queries), 2560 cycles at 128 bytes a cycle against
 // 2048 of MMA, and the codes' loads go through the same pipe.  32 sequences at
-// 4096-8192 (0.23 GB), bf16 queries: 4 tokens each 98 us, 32 tokens 111 (bf16 pages,
-// 0.82 GB: 132 and 147); fp32 queries 164; a mixed batch of 32, 4 of them with
-// chunks of ~400 tokens, 134 and 224.  What it cost on the way (4 tokens each): half
-// lines of codes a load 15 more, scores kept in 240 registers a thread, the MMA
-// warp spilling, 4.
+// 4096-8192 (0.23 GB), bf16 queries: 4 tokens each 98 us, 32 tokens 113 (bf16 pages,
+// 0.82 GB: 132 and 147); fp32 queries 166; a mixed batch of 32, 4 of them with
+// chunks of ~400 tokens, 135 and 226 (bf16 pages 107 and 131 to 141).  What it cost
+// on the way (4 tokens each): half lines of codes a load 15 more, scores kept in 240
+// registers a thread, the MMA warp spilling, 4.  As it is ptxas spills 48 bytes of a
+// thread with bf16 queries, 368 with fp32 ones (on pairs 496); by which warps is not
+// known, nor what it costs.
 #include "paged4_chunk_parts.cuh"
 
 namespace spark {

@@ -12,11 +12,11 @@
 // chain of a tile is what is longest (read twice with 152 registers: 278 us for a
 // chunk of 4096 tokens at 4096, against 262).
 //
-// Measured, a chunk of 4096 tokens at 4096: bf16 queries 262 us in a graph, 1570
-// TFLOP/s, 0.80 of the measured bf16 rate (bf16 pages 223: a tile takes 2600 cycles
+// Measured, a chunk of 4096 tokens at 4096: bf16 queries 265 us in a graph, 1550
+// TFLOP/s, 0.79 of the measured bf16 rate (bf16 pages 223: a tile takes 2600 cycles
 // against 2048 of MMA, the softmax slowed by the converting warps beside it on its
-// schedulers); fp32 queries 547, two MMAs for each and their sums into memory
-// (kFoldTiles); a window of 512 72.  On single CTAs 328, 596 and 77.
+// schedulers); fp32 queries 555 (bf16 pages 409), two MMAs for each and their sums
+// into memory (kFoldTiles); a window of 512 73.  On single CTAs 328, 596 and 77.
 //
 // A tile's scores, softmax and product follow one another, and two tiles are in
 // flight: 1024 + 1800 + 1024 cycles and the reports between them.  Neither two
@@ -26,7 +26,7 @@
 //
 // Each CTA's eight converting warps report a half to its own CTA, rank 1's warp 1
 // passes it on to rank 0, whose warp 1 issues the MMAs over both: one wait for the
-// nine (one for each CTA's, fp32 queries: 559 us, now 547).
+// nine (one for each CTA's, fp32 queries: 559 us against 547).
 #include "paged4_chunk_parts.cuh"
 #include "paged_pair_parts.cuh"
 

@@ -8,10 +8,11 @@
 // a rotated pair that lie in other lanes come by a shuffle.  The first rows are
 // asked for before the token's place is looked up, a few more at a time after.
 //
-// Measured (in a graph): one token, 24 rows, 2.9 us; 64 into 4-bit pages and out
-// again 6.6; 9000 tokens of prompts, bf16, all dims rotated, into 4-bit pages and
-// out again 61 (0.26 GB: 4.3 TB/s), bound by the rotation's and the quotients'
-// instructions; 47000 rows of prefixes out of 4-bit pages 41 (0.23 GB: 5.7 TB/s).
+// Measured (in a graph): one token, 24 rows, 3.3 to 3.9 us; 64 into 4-bit pages 4.7;
+// 9400 tokens of prompts, bf16, all dims rotated, into 4-bit pages 50 (4.0 TB/s; bf16
+// pages 46, fp32 50, 5.0 and 5.4 TB/s), with 65% of issue slots and 43% of DRAM busy
+// at a third of the warps; their k and v alone 21 (16, 25), out again 10 (13, 19);
+// 47000 rows of prefixes out of 4-bit pages 41 (0.23 GB: 5.7 TB/s).
 #include <math.h>
 
 #include <type_traits>

@@ -44,8 +44,9 @@ constexpr int kStateFloats = kHeadDim + kHeadDim / 32 * PAD;
 // The group's state from the consumer warps' states in `sm`: finished if
 // whole, else this CTA's partial; the last of the group's CTAs to arrive
 // merges them in CTA order.  Warp h takes query head h, lane l its dims
-// [8 l, 8 l + 8); the warps' states are WARP floats apart.  (The parts are worked out before the tiles arrive: their
-// divisions took up to 2000 cycles here.)
+// [8 l, 8 l + 8); the warps' states are WARP floats apart.  (Over fp32 and bf16
+// pages the parts are worked out before the tiles arrive: their divisions took up to
+// 2000 cycles here.  Over 4-bit ones, where registers are short, they are not.)
 template <typename QT, int PAD = 0, int WARP = 4 * kStateFloats<PAD>>
 __device__ __forceinline__ void finish_group(const MergeSmem& sm, volatile int* flags, const Args& p, QT* a_head0,
                                              const Parts& parts) {
